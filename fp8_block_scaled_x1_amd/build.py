@@ -15,7 +15,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfp8bs.so")
-SOURCES = ["api.hip", "quant.hip", "gemm.hip", "moe.hip"]
+SOURCES = ["api.hip", "quant.hip", "gemm.hip", "moe.hip", "attn_api.hip", "mla_prefill.hip", "mla_decode.hip",
+           "verify.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

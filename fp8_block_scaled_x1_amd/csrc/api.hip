@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "fp8bs.h"
+#include "fp8bs_attn.h"
 #include "internal.h"
 
 namespace {
@@ -94,6 +95,7 @@ const char* fp8bs_status_string(int status) {
     case FP8BS_ERR_LAUNCH: return "kernel launch failed";
     case FP8BS_ERR_TOO_LARGE: return "size exceeds the supported 32-bit index range";
     case FP8BS_ERR_SCRATCH: return "the problem needs more scratch memory than the no-allocation entry point holds";
+    case FP8BS_ERR_VALUE: return "a scalar argument is outside its range";
     default: return "unknown status";
   }
 }

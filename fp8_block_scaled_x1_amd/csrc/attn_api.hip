@@ -1,0 +1,263 @@
+// C ABI of the attention and draft-verification operators: host-side argument
+// validation, then the launches on the caller's stream. Declarations and the
+// meaning of every argument are in include/fp8bs_attn.h.
+
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "attn_internal.h"
+#include "fp8bs_attn.h"
+
+namespace {
+
+constexpr int64_t kI32 = (int64_t)1 << 31;
+constexpr int64_t kGridMax = kI32 - 1;
+constexpr int kTile = 64;
+
+bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+bool off8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) != 0; }
+bool off4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+int status_of(hipError_t e) { return e == hipSuccess ? FP8BS_OK : FP8BS_ERR_LAUNCH; }
+hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
+bool bad_scale(float s) { return !(s > 0.f) || !isfinite(s); }
+
+int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
+
+int prefill_sizes(int B, int64_t Tq, int64_t Tk, int H, int64_t q_stride, int64_t kv_stride, int64_t rope_stride,
+                  float scale) {
+  if (B < 0 || Tq < 0 || Tk < 0 || H < 1) return FP8BS_ERR_SHAPE;
+  if (B == 0 && (Tq > 0 || Tk > 0)) return FP8BS_ERR_SHAPE;      // tokens of no request
+  if (H > 65536 || Tq >= kI32 - 65536 || Tk >= kI32 - 65536) return FP8BS_ERR_TOO_LARGE;
+  if (q_stride < (int64_t)H * 192 || kv_stride < (int64_t)H * 256 || rope_stride < 64) return FP8BS_ERR_SHAPE;
+  if (q_stride % 8 || kv_stride % 8 || rope_stride % 8) return FP8BS_ERR_ALIGN;
+  const int64_t most = Tq > Tk ? Tq : Tk;
+  if ((most / 32 + 1 + B) * H > kGridMax || most * H > kGridMax * 8) return FP8BS_ERR_TOO_LARGE;
+  if (bad_scale(scale)) return FP8BS_ERR_VALUE;
+  return FP8BS_OK;
+}
+
+// ---- absorbed form ----
+
+struct DecodeSizes {
+  int64_t rows, max_len, part_floats, ml_floats;
+  fp8bs::MlaDecode p;
+};
+
+// Sizes of one problem (the requests' own tokens, or the prefix's) and its
+// share of the workspace. joined: every piece is kept as a partial.
+int decode_sizes(int B, int64_t rows, int64_t width, int page, bool joined, DecodeSizes& s) {
+  if (width > kI32 / page - kTile) return FP8BS_ERR_TOO_LARGE;
+  s.rows = rows;
+  s.max_len = width * page;
+  const int64_t tiles = (int64_t)B * ((s.max_len + kTile - 1) / kTile);
+  if (tiles >= kI32) return FP8BS_ERR_TOO_LARGE;
+  int64_t row_blocks = 0;
+  fp8bs::mla_decode_plan(rows, tiles, &s.p.block_rows, &row_blocks, &s.p.groups);
+  if (((int64_t)s.p.groups + 8) * row_blocks > kGridMax) return FP8BS_ERR_TOO_LARGE;
+  s.p.row_blocks = (int)row_blocks;
+  const int64_t pieces = 2 * (int64_t)s.p.groups + (joined ? B : 0);
+  s.part_floats = pieces * rows * 512;
+  s.ml_floats = pieces * rows * 2;
+  return FP8BS_OK;
+}
+
+int64_t decode_bytes(const DecodeSizes& s) { return align256(4 * s.part_floats) + align256(4 * s.ml_floats); }
+
+int decode_plan(int B, int T, int H, int64_t width, int page, int64_t prefix_pages, DecodeSizes& own,
+                DecodeSizes& prefix) {
+  if (B < 0 || T < 1 || H < 1 || width < 0 || page < 1 || prefix_pages < 0) return FP8BS_ERR_SHAPE;
+  const int64_t rows = (int64_t)T * H;
+  if (rows >= 1 << 24 || B * rows >= kI32 / 8) return FP8BS_ERR_TOO_LARGE;
+  int st = decode_sizes(B, rows, width, page, prefix_pages > 0, own);
+  if (st == FP8BS_OK && prefix_pages > 0) st = decode_sizes(1, B * rows, prefix_pages, page, true, prefix);
+  return st;
+}
+
+void fill(fp8bs::MlaDecode& p, const uint16_t* q, const void* cache, const float* scales, const uint16_t* rope,
+          int64_t pages, int page, const int32_t* table, int64_t width, const int32_t* lens, int B, int tokens,
+          int heads, const DecodeSizes& s, float scale, uint16_t* out, float* lse, bool join, char*& ws) {
+  p.q = q;
+  p.cache = static_cast<const char*>(cache);
+  p.scales = reinterpret_cast<const char*>(scales);
+  p.rope = reinterpret_cast<const char*>(rope);
+  p.table = table;
+  p.lens = lens;
+  p.table_stride = width;
+  p.B = B;
+  p.rows = (int)s.rows;
+  p.tokens = tokens;
+  p.heads = heads;
+  p.pages = (int)pages;
+  p.page = page;
+  p.max_len = (int)s.max_len;
+  // tok / page for 0 <= tok < 2^31: with 2^L the next power of two, the
+  // multiplier floor(2^(31+L) / page) + 1 errs by at most 2^L in 2^(31+L)
+  int L = 0;
+  while (((int64_t)1 << L) < page) ++L;
+  p.page_shift = 31 + L;
+  p.page_magic = (uint32_t)(((uint64_t)1 << (31 + L)) / (uint64_t)page + 1);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.block_rows = s.p.block_rows;
+  p.row_blocks = s.p.row_blocks;
+  p.groups = s.p.groups;
+  p.join = join;
+  p.out = out;
+  p.lse = lse;
+  p.part = reinterpret_cast<float*>(ws);
+  ws += align256(4 * s.part_floats);
+  p.part_ml = reinterpret_cast<float*>(ws);
+  ws += align256(4 * s.ml_floats);
+}
+
+int decode(const uint16_t* q, int kind, const void* cache, const float* scales, const uint16_t* rope, int64_t pages,
+           int page, const int32_t* prefix_table, int64_t prefix_pages, const int32_t* prefix_len,
+           const int32_t* table, int64_t width, const int32_t* lens, int B, int T, int H, float scale, uint16_t* out,
+           float* lse, void* workspace, void* stream) {
+  if (kind != FP8BS_CACHE_BF16 && kind != FP8BS_CACHE_FP8) return FP8BS_ERR_MODE;
+  DecodeSizes own{}, prefix{};
+  const int st = decode_plan(B, T, H, width, page, prefix_pages, own, prefix);
+  if (st != FP8BS_OK) return st;
+  if (pages < 0) return FP8BS_ERR_SHAPE;
+  if (pages >= kI32) return FP8BS_ERR_TOO_LARGE;
+  if (bad_scale(scale)) return FP8BS_ERR_VALUE;
+  if (B == 0) return FP8BS_OK;
+  const bool reads = width > 0 || prefix_pages > 0;
+  if (reads && pages == 0) return FP8BS_ERR_SHAPE;       // a table into no pages
+  if (!q || !lens || !out || !lse || !workspace) return FP8BS_ERR_NULL_PTR;
+  if (width > 0 && !table) return FP8BS_ERR_NULL_PTR;
+  if (prefix_pages > 0 && (!prefix_table || !prefix_len)) return FP8BS_ERR_NULL_PTR;
+  if (reads && (!cache || (kind == FP8BS_CACHE_FP8 && (!scales || !rope)))) return FP8BS_ERR_NULL_PTR;
+  if (off16(q) || off16(cache) || off16(out) || off16(workspace)) return FP8BS_ERR_ALIGN;
+  if (kind == FP8BS_CACHE_FP8 && (off16(scales) || off16(rope))) return FP8BS_ERR_ALIGN;
+  if (off4(table) || off4(lens) || off4(lse) || off4(prefix_table) || off4(prefix_len)) return FP8BS_ERR_ALIGN;
+  char* ws = static_cast<char*>(workspace);
+  fp8bs::MlaDecode a{}, b{};
+  const bool join = prefix_pages > 0;
+  fill(a, q, cache, scales, rope, pages, page, table, width, lens, B, T, H, own, scale, out, lse, join, ws);
+  // the prefix: one request whose rows are everyone's, nothing hidden
+  if (join)
+    fill(b, q, cache, scales, rope, pages, page, prefix_table, prefix_pages, prefix_len, 1, 1, (int)prefix.rows, prefix,
+         scale, out, lse, true, ws);
+  return status_of(fp8bs::launch_mla_decode(a, join ? &b : nullptr, kind == FP8BS_CACHE_FP8, as_stream(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+int fp8bs_attn_version(void) { return FP8BS_ATTN_VERSION; }
+
+int fp8bs_mla_prefill(const uint16_t* q, int64_t q_stride, const uint16_t* kv, int64_t kv_stride,
+                      const uint16_t* k_rope, int64_t rope_stride, const int32_t* cu_q, const int32_t* cu_k, int B,
+                      int64_t Tq, int64_t Tk, int H, float scale, int causal, uint16_t* out, float* lse,
+                      void* stream) {
+  const int st = prefill_sizes(B, Tq, Tk, H, q_stride, kv_stride, rope_stride, scale);
+  if (st != FP8BS_OK) return st;
+  if (Tq == 0) return FP8BS_OK;
+  if (!q || !cu_q || !cu_k || !out || !lse || (Tk > 0 && (!kv || !k_rope))) return FP8BS_ERR_NULL_PTR;
+  if (off16(q) || off16(kv) || off16(k_rope) || off16(out)) return FP8BS_ERR_ALIGN;
+  if (off4(cu_q) || off4(cu_k) || off4(lse)) return FP8BS_ERR_ALIGN;
+  fp8bs::MlaPrefill p{};
+  p.q = q; p.kv = kv; p.k_rope = k_rope;
+  p.q_stride = q_stride; p.kv_stride = kv_stride; p.rope_stride = rope_stride;
+  p.cu_q = cu_q; p.cu_k = cu_k;
+  p.B = B; p.H = H; p.Tq = (int)Tq; p.Tk = (int)Tk;
+  p.scale = scale;
+  p.causal = causal != 0;
+  p.out = out;
+  p.lse = lse;
+  return status_of(fp8bs::launch_mla_prefill(p, as_stream(stream)));
+}
+
+int64_t fp8bs_mla_prefill_bwd_workspace_bytes(int64_t Tq, int64_t Tk, int H) {
+  if (Tq < 0 || Tk < 0 || H < 1) return FP8BS_ERR_SHAPE;
+  if (Tq >= kI32 || Tk >= kI32 || H > 65536) return FP8BS_ERR_TOO_LARGE;
+  return align256(4 * Tq * H) + 4 * Tk * H * 64;
+}
+
+int fp8bs_mla_prefill_bwd(const uint16_t* dout, const uint16_t* q, int64_t q_stride, const uint16_t* kv,
+                          int64_t kv_stride, const uint16_t* k_rope, int64_t rope_stride, const uint16_t* out,
+                          const float* lse, const int32_t* cu_q, const int32_t* cu_k, int B, int64_t Tq, int64_t Tk,
+                          int H, float scale, int causal, uint16_t* dq, uint16_t* dkv, uint16_t* dk_rope,
+                          void* workspace, void* stream) {
+  const int st = prefill_sizes(B, Tq, Tk, H, q_stride, kv_stride, rope_stride, scale);
+  if (st != FP8BS_OK) return st;
+  if (Tq == 0 && Tk == 0) return FP8BS_OK;
+  if (!cu_q || !cu_k || !workspace) return FP8BS_ERR_NULL_PTR;
+  if (Tq > 0 && (!dout || !q || !out || !lse || !dq)) return FP8BS_ERR_NULL_PTR;
+  if (Tk > 0 && (!kv || !k_rope || !dkv || !dk_rope)) return FP8BS_ERR_NULL_PTR;
+  if (off16(dout) || off16(q) || off16(kv) || off16(k_rope) || off16(out) || off16(dq) || off16(dkv) ||
+      off16(dk_rope) || off16(workspace))
+    return FP8BS_ERR_ALIGN;
+  if (off4(cu_q) || off4(cu_k) || off4(lse)) return FP8BS_ERR_ALIGN;
+  fp8bs::MlaPrefill p{};
+  p.q = q; p.kv = kv; p.k_rope = k_rope;
+  p.q_stride = q_stride; p.kv_stride = kv_stride; p.rope_stride = rope_stride;
+  p.cu_q = cu_q; p.cu_k = cu_k;
+  p.B = B; p.H = H; p.Tq = (int)Tq; p.Tk = (int)Tk;
+  p.scale = scale;
+  p.causal = causal != 0;
+  p.out = const_cast<uint16_t*>(out);
+  p.lse = const_cast<float*>(lse);
+  p.dout = dout;
+  p.delta = static_cast<float*>(workspace);
+  p.rope_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(4 * Tq * H));
+  p.dq = dq; p.dkv = dkv; p.dk_rope = dk_rope;
+  return status_of(fp8bs::launch_mla_prefill_bwd(p, as_stream(stream)));
+}
+
+int64_t fp8bs_mla_decode_workspace_bytes(int B, int T, int H, int64_t table_width, int page, int64_t prefix_pages) {
+  DecodeSizes own{}, prefix{};
+  const int st = decode_plan(B, T, H, table_width, page, prefix_pages, own, prefix);
+  if (st != FP8BS_OK) return st;
+  return decode_bytes(own) + (prefix_pages > 0 ? decode_bytes(prefix) : 0);
+}
+
+int fp8bs_mla_decode(const uint16_t* q, int cache_kind, const void* cache, const float* cache_scales,
+                     const uint16_t* cache_rope, int64_t pages, int page, const int32_t* table, int64_t table_width,
+                     const int32_t* lens, int B, int T, int H, float scale, uint16_t* out, float* lse,
+                     void* workspace, void* stream) {
+  return decode(q, cache_kind, cache, cache_scales, cache_rope, pages, page, nullptr, 0, nullptr, table, table_width,
+                lens, B, T, H, scale, out, lse, workspace, stream);
+}
+
+int fp8bs_mla_decode_shared(const uint16_t* q, int cache_kind, const void* cache, const float* cache_scales,
+                            const uint16_t* cache_rope, int64_t pages, int page, const int32_t* prefix_table,
+                            int64_t prefix_pages, const int32_t* prefix_len, const int32_t* table,
+                            int64_t table_width, const int32_t* lens, int B, int T, int H, float scale, uint16_t* out,
+                            float* lse, void* workspace, void* stream) {
+  return decode(q, cache_kind, cache, cache_scales, cache_rope, pages, page, prefix_table, prefix_pages, prefix_len,
+                table, table_width, lens, B, T, H, scale, out, lse, workspace, stream);
+}
+
+int64_t fp8bs_verify_drafts_workspace_bytes(int B, int64_t V) {
+  if (B < 0 || V < 1) return FP8BS_ERR_SHAPE;
+  if (V > 1 << 24 || B * fp8bs::verify_chunks(V) > kGridMax) return FP8BS_ERR_TOO_LARGE;
+  return 16 * B * fp8bs::verify_chunks(V);
+}
+
+int fp8bs_verify_drafts(const void* p, const void* q, int dtype, const int32_t* drafts, const int32_t* n_drafts,
+                        const float* u, const float* u_next, int B, int K, int64_t V, int32_t* tokens,
+                        int32_t* accepted, void* workspace, void* stream) {
+  if (dtype != FP8BS_F32 && dtype != FP8BS_BF16) return FP8BS_ERR_DTYPE;
+  if (K < 0 || K > 63) return FP8BS_ERR_SHAPE;
+  const int64_t bytes = fp8bs_verify_drafts_workspace_bytes(B, V);
+  if (bytes < 0) return (int)bytes;
+  if (B == 0) return FP8BS_OK;
+  if (!p || !n_drafts || !u_next || !tokens || !accepted || !workspace) return FP8BS_ERR_NULL_PTR;
+  if (K > 0 && (!drafts || !u)) return FP8BS_ERR_NULL_PTR;
+  if (off4(p) || off4(q) || off4(drafts) || off4(n_drafts) || off4(u) || off4(u_next) || off4(tokens) ||
+      off4(accepted) || off8(workspace))
+    return FP8BS_ERR_ALIGN;
+  fp8bs::VerifyDrafts v{};
+  v.p = p; v.q = q;
+  v.drafts = drafts; v.n_drafts = n_drafts;
+  v.u = u; v.u_next = u_next;
+  v.B = B; v.K = K; v.V = (int)V;
+  v.sums = static_cast<uint64_t*>(workspace);
+  v.tokens = tokens; v.accepted = accepted;
+  return status_of(fp8bs::launch_verify_drafts(v, dtype == FP8BS_BF16, as_stream(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,451 @@
+// Latent attention in its expanded form (prefill and training), forward and
+// backward, for a packed batch of requests of any lengths.
+//
+// Per head h, with q = (q^n, q^r), keys (k^n_h, k^r) whose 64-wide rotary part
+// is shared by all heads, and values v_h:
+//   S_ij = scale * (q^n_i . k^n_j + q^r_i . k^r_j),  j <= i + Lk - Lq if causal
+//   P = softmax(S),  O = P V,  lse_i = log sum_j exp(S_ij)
+// and with D_i = dO_i . O_i:
+//   dV = P^T dO,  dS = P * (dO V^T - D),  dq = scale dS K,  dk = scale dS^T q,
+//   dk^r = sum over the heads of their dk's rotary part.
+//
+// Roundings below 32 bits: P and dS to BF16 as operands of the matrix unit
+// (relative 2^-8 at most, on each term of a sum), O to BF16 before D is formed from it,
+// and the outputs. Scores, softmax statistics, D and every sum are FP32; the
+// rotary gradient is summed over the heads in FP32, in head order.
+//
+// All products are 32x32x16 MFMAs, oriented so that the lane that owns a row
+// of the score tile owns it in the next product too.
+
+#include "attn_internal.h"
+#include "device_common.h"
+#include "mla_tiles.h"
+
+namespace fp8bs {
+
+namespace {
+
+// Workgroup -> (unit, head). The heads are dealt over the XCDs, and the units
+// of a head follow each other there: they share its keys and values in L2.
+__device__ __forceinline__ bool unit_of(int units, int H, int& unit, int& head) {
+  const int xcd = blockIdx.x % kAttnXcds, slot = blockIdx.x / kAttnXcds;
+  const int per = (H + kAttnXcds - 1) / kAttnXcds;
+  if (H % kAttnXcds == 0) {
+    head = (slot / units) * kAttnXcds + xcd;
+    unit = slot % units;
+    return slot < per * units;
+  }
+  head = blockIdx.x % H;
+  unit = blockIdx.x / H;
+  return unit < units;
+}
+unsigned unit_grid(int64_t units, int H) { return (unsigned)(units * H); }
+
+constexpr int kBn = 64;      // keys per tile
+constexpr int kNopeTile = kBn * 256, kRopeTile = kBn * 128, kVTile = kBn * 256;
+constexpr int kFwdTile = kNopeTile + kRopeTile + kVTile;
+
+template <int NW>
+__device__ __forceinline__ void load_keys(const MlaPrefill& p, const uint16_t* kv, const uint16_t* kr, int row0,
+                                          int last, int w, int lane, uint32_t lds) {
+  load_tile256<kBn, NW>(kv, p.kv_stride, row0, last, w, lane, lds);
+  load_tile128<kBn, NW>(kr, p.rope_stride, row0, last, w, lane, lds + kNopeTile);
+  load_tile256<kBn, NW>(kv + kNope, p.kv_stride, row0, last, w, lane, lds + kNopeTile + kRopeTile);
+}
+
+// The lane's 32x32x16 operand of 192 query columns (or, offset, 128 of dO).
+template <int N>
+__device__ __forceinline__ void load_operand(bf16x8 (&f)[N], const uint16_t* row, int half) {
+#pragma unroll
+  for (int ks = 0; ks < N; ++ks) f[ks] = *reinterpret_cast<const bf16x8*>(row + 16 * ks + 8 * half);
+}
+
+// S^T of 32 keys of the tile (rows) by the wave's 32 queries (columns).
+__device__ __forceinline__ f32x16 scores(const char* t, const TileLane& L, int key0, const bf16x8 (&qf)[12]) {
+  f32x16 s = zero16();
+#pragma unroll
+  for (int ks = 0; ks < 8; ++ks) s = mfma32(rows256(t, L, key0, ks), qf[ks], s);
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks) s = mfma32(rows128(t + kNopeTile, L, key0, ks), qf[8 + ks], s);
+  return s;
+}
+
+// Forward: NW waves of 32 queries, key tiles of 64 in two LDS buffers.
+template <int NW>
+__global__ __launch_bounds__(64 * NW, 2) void mla_fwd_kernel(const MlaPrefill p, int units) {
+  constexpr int BM = 32 * NW;
+  __shared__ __align__(1024) char tiles[2 * kFwdTile];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int unit, head;
+  if (!unit_of(units, p.H, unit, head)) return;
+  // the last blocks of a causal request see the most keys: they go first
+  const ExpertSlot u = locate_expert(p.cu_q, p.B, p.Tq, units - 1 - unit, BM, 1);
+  if (u.e < 0) return;
+  const int k0 = __builtin_amdgcn_readfirstlane(min(max(p.cu_k[u.e], 0), p.Tk));
+  const int k1 = __builtin_amdgcn_readfirstlane(min(max(p.cu_k[u.e + 1], k0), p.Tk));
+  const int Lq = u.r1 - u.r0, Lk = k1 - k0, off = Lk - Lq;
+  const int first = (units - 1 - unit - u.base) * BM;
+  const int end = min(first + BM, Lq);                                     // queries of the block
+  const int kend = p.causal ? min(Lk, max(end + off, 0)) : Lk;             // keys any of them sees
+  const int nt = (kend + kBn - 1) / kBn;
+
+  const TileLane L(lane);
+  const int qi = first + 32 * w + L.row;                                   // this lane's query
+  const int qc = min(qi, Lq - 1);
+  const int see = p.causal ? min(Lk, qi + off + 1) : Lk;                   // keys it sees
+  const int wave_all = p.causal ? min(Lk, first + 32 * w + off + 1) : Lk;  // keys all the wave's queries see
+  const int wave_any = p.causal ? min(Lk, first + 32 * w + 32 + off) : Lk;
+
+  const uint16_t* kv = p.kv + (int64_t)k0 * p.kv_stride + head * (kNope + kVDim);
+  const uint16_t* kr = p.k_rope + (int64_t)k0 * p.rope_stride;
+  const uint32_t lds = lds_offset(tiles);
+  if (nt > 0) load_keys<NW>(p, kv, kr, 0, Lk - 1, w, lane, lds);
+
+  bf16x8 qf[12];
+  load_operand(qf, p.q + (int64_t)(u.r0 + qc) * p.q_stride + head * kQk, L.half);
+  const float c = p.scale * kLog2e;
+  f32x16 o[4];
+#pragma unroll
+  for (int d = 0; d < 4; ++d) o[d] = zero16();
+  float m = neg_inf(), l = 0.f;      // m: of the raw scores
+
+  for (int t = 0; t < nt; ++t) {
+    attn_wait<0>();
+    attn_barrier();
+    if (t + 1 < nt) load_keys<NW>(p, kv, kr, (t + 1) * kBn, Lk - 1, w, lane, lds + ((t + 1) & 1) * kFwdTile);
+    if (t * kBn >= wave_any) continue;
+    const char* tl = tiles + (t & 1) * kFwdTile;
+    f32x16 s[2];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) s[kb] = scores(tl, L, 32 * kb, qf);
+    if ((t + 1) * kBn > wave_all) {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (t * kBn + 32 * kb + drow(i, L.half) >= see) s[kb][i] = neg_inf();
+    }
+    float mt = s[0][0];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mt = fmaxf(mt, s[kb][i]);
+    mt = fmaxf(mt, __shfl_xor(mt, 32, 64));
+    const float mn = fmaxf(m, mt);
+    const float ref = mn == neg_inf() ? 0.f : mn * c;
+    if (__any(mn > m)) {
+      const float alpha = exp2_fast(m * c - ref);
+      l *= alpha;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) o[d] *= alpha;
+      m = mn;
+    }
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[kb][i] = exp2_fast(fmaf(s[kb][i], c, -ref));
+        sum += s[kb][i];
+      }
+      l += sum;
+    }
+    const char* vt = tl + kNopeTile + kRopeTile;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        const bf16x8 pb = pack8(s[kb], a);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) o[d] = mfma32(cols256(vt, L, 32 * kb + 16 * a, d), pb, o[d]);
+      }
+  }
+
+  l += __shfl_xor(l, 32, 64);
+  if (qi < Lq) {
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    uint16_t* op = p.out + ((int64_t)(u.r0 + qi) * p.H + head) * kVDim + 4 * L.half;
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        bf16x4 b;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[j] = (__bf16)(o[d][4 * i + j] * inv);
+        *reinterpret_cast<bf16x4*>(op + 32 * d + 8 * i) = b;
+      }
+    if (L.half == 0)
+      p.lse[(int64_t)head * p.Tq + u.r0 + qi] = l > 0.f ? (m * c + __builtin_log2f(l)) * kLn2 : neg_inf();
+  }
+}
+
+// D[h][t] = dO . O: 16 lanes per (token, head) row of 128.
+__global__ __launch_bounds__(256) void mla_delta_kernel(const MlaPrefill p) {
+  const int64_t r = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 4;
+  const int part = threadIdx.x & 15;
+  if (r >= (int64_t)p.Tq * p.H) return;
+  const bf16x8 a = *reinterpret_cast<const bf16x8*>(p.dout + r * kVDim + 8 * part);
+  const bf16x8 b = *reinterpret_cast<const bf16x8*>(p.out + r * kVDim + 8 * part);
+  float v = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v = fmaf((float)a[i], (float)b[i], v);
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) v += __shfl_xor(v, d, 64);
+  if (part == 0) p.delta[(r % p.H) * p.Tq + r / p.H] = v;
+}
+
+// Gradients of keys and values: 4 waves of 32 keys each, whose dK and dV stay
+// in registers while the tiles of 64 queries (Q, dO, lse, D) pass.
+constexpr int kBq = 64;
+constexpr int kQNope = kBq * 256, kQRope = kBq * 128, kDo = kBq * 256;
+constexpr int kBwdTile = kQNope + kQRope + kDo + 2 * kBq * 4;
+
+__global__ __launch_bounds__(256, 1) void mla_dkv_kernel(const MlaPrefill p, int units) {
+  constexpr int NW = 4, BK = 32 * NW;
+  __shared__ __align__(1024) char tiles[2 * kBwdTile];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int unit, head;
+  if (!unit_of(units, p.H, unit, head)) return;
+  const ExpertSlot u = locate_expert(p.cu_k, p.B, p.Tk, unit, BK, 1);
+  if (u.e < 0) return;
+  const int q0 = __builtin_amdgcn_readfirstlane(min(max(p.cu_q[u.e], 0), p.Tq));
+  const int q1 = __builtin_amdgcn_readfirstlane(min(max(p.cu_q[u.e + 1], q0), p.Tq));
+  const int Lk = u.r1 - u.r0, Lq = q1 - q0, off = Lk - Lq;
+  const int kb0 = (unit - u.base) * BK;
+  const int key0 = kb0 + 32 * w;
+  const int start = p.causal ? max(0, kb0 - off) : 0;        // first query that sees the block's first key
+  const int nt = Lq > start ? (Lq - start + kBq - 1) / kBq : 0;
+
+  const TileLane L(lane);
+  const int key = key0 + L.row, kc = min(key, Lk - 1);
+  bf16x8 kf[12], vf[8];
+  {
+    const uint16_t* row = p.kv + (int64_t)(u.r0 + kc) * p.kv_stride + head * (kNope + kVDim);
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) kf[ks] = *reinterpret_cast<const bf16x8*>(row + 16 * ks + 8 * L.half);
+    load_operand(vf, row + kNope, L.half);
+    const uint16_t* rr = p.k_rope + (int64_t)(u.r0 + kc) * p.rope_stride;
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) kf[8 + ks] = *reinterpret_cast<const bf16x8*>(rr + 16 * ks + 8 * L.half);
+  }
+  f32x16 dk[6], dv[4];
+#pragma unroll
+  for (int d = 0; d < 6; ++d) dk[d] = zero16();
+#pragma unroll
+  for (int d = 0; d < 4; ++d) dv[d] = zero16();
+
+  const uint16_t* qb = p.q + (int64_t)q0 * p.q_stride + head * kQk;
+  const uint16_t* db = p.dout + ((int64_t)q0 * p.H + head) * kVDim;
+  const float* stat = (w == 0 ? p.lse : p.delta) + (int64_t)head * p.Tq + q0;
+  const uint32_t lds = lds_offset(tiles);
+  auto load = [&](int t) {
+    const uint32_t at = lds + (t & 1) * kBwdTile;
+    const int row0 = start + t * kBq;
+    load_tile256<kBq, NW>(qb, p.q_stride, row0, Lq - 1, w, lane, at);
+    load_tile128<kBq, NW>(qb + kNope, p.q_stride, row0, Lq - 1, w, lane, at + kQNope);
+    load_tile256<kBq, NW>(db, (int64_t)p.H * kVDim, row0, Lq - 1, w, lane, at + kQNope + kQRope);
+    if (w < 2) dma4(stat + min(row0 + lane, Lq - 1), at + kQNope + kQRope + kDo + w * kBq * 4);
+  };
+  if (nt > 0) load(0);
+  const float c = p.scale * kLog2e;
+
+  for (int t = 0; t < nt; ++t) {
+    attn_wait<0>();
+    attn_barrier();
+    if (t + 1 < nt) load(t + 1);
+    const char* tl = tiles + (t & 1) * kBwdTile;
+    const char* dot = tl + kQNope + kQRope;
+    const float* st = reinterpret_cast<const float*>(dot + kDo);
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub) {
+      const int qr = start + t * kBq + 32 * sub;          // first query of the 32
+      if (qr >= Lq || (p.causal && qr + 31 + off < key0)) continue;
+      // S and dP of 32 queries (rows) by the wave's 32 keys (columns)
+      f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) s = mfma32(rows256(tl, L, 32 * sub, ks), kf[ks], s);
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) s = mfma32(rows128(tl + kQNope, L, 32 * sub, ks), kf[8 + ks], s);
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) dp = mfma32(rows256(dot, L, 32 * sub, ks), vf[ks], dp);
+      const bool edge = qr + 32 > Lq || (p.causal && qr + off < key0 + 31);
+#pragma unroll
+      for (int i4 = 0; i4 < 4; ++i4) {
+        const f32x4 ls = *reinterpret_cast<const f32x4*>(st + 32 * sub + 8 * i4 + 4 * L.half);
+        const f32x4 de = *reinterpret_cast<const f32x4*>(st + kBq + 32 * sub + 8 * i4 + 4 * L.half);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = 4 * i4 + j, qi = qr + drow(i, L.half);
+          float e = exp2_fast(fmaf(s[i], c, -ls[j] * kLog2e));
+          if (edge && (qi >= Lq || (p.causal && qi + off < key))) e = 0.f;
+          s[i] = e;
+          dp[i] = e * (dp[i] - de[j]);
+        }
+      }
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        const bf16x8 pb = pack8(s, a), sb = pack8(dp, a);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) dv[d] = mfma32(cols256(dot, L, 32 * sub + 16 * a, d), pb, dv[d]);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) dk[d] = mfma32(cols256(tl, L, 32 * sub + 16 * a, d), sb, dk[d]);
+#pragma unroll
+        for (int d = 0; d < 2; ++d) dk[4 + d] = mfma32(cols128(tl + kQNope, L, 32 * sub + 16 * a, d), sb, dk[4 + d]);
+      }
+    }
+  }
+
+  if (key < Lk) {
+    uint16_t* out = p.dkv + ((int64_t)(u.r0 + key) * p.H + head) * (kNope + kVDim) + 4 * L.half;
+    float* rp = p.rope_part + ((int64_t)head * p.Tk + u.r0 + key) * kRopeDim + 4 * L.half;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        bf16x4 a, b;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          a[j] = (__bf16)(dk[d][4 * i + j] * p.scale);
+          b[j] = (__bf16)dv[d][4 * i + j];
+        }
+        *reinterpret_cast<bf16x4*>(out + 32 * d + 8 * i) = a;
+        *reinterpret_cast<bf16x4*>(out + kNope + 32 * d + 8 * i) = b;
+      }
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        f32x4 v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = dk[4 + d][4 * i + j] * p.scale;
+        *reinterpret_cast<f32x4*>(rp + 32 * d + 8 * i) = v;
+      }
+    }
+  }
+}
+
+// Gradient of the queries: the forward's loop with dS in place of P, so it
+// needs no sums between workgroups.
+template <int NW>
+__global__ __launch_bounds__(64 * NW, 2) void mla_dq_kernel(const MlaPrefill p, int units) {
+  constexpr int BM = 32 * NW;
+  __shared__ __align__(1024) char tiles[2 * kFwdTile];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int unit, head;
+  if (!unit_of(units, p.H, unit, head)) return;
+  const ExpertSlot u = locate_expert(p.cu_q, p.B, p.Tq, units - 1 - unit, BM, 1);
+  if (u.e < 0) return;
+  const int k0 = __builtin_amdgcn_readfirstlane(min(max(p.cu_k[u.e], 0), p.Tk));
+  const int k1 = __builtin_amdgcn_readfirstlane(min(max(p.cu_k[u.e + 1], k0), p.Tk));
+  const int Lq = u.r1 - u.r0, Lk = k1 - k0, off = Lk - Lq;
+  const int first = (units - 1 - unit - u.base) * BM;
+  const int end = min(first + BM, Lq);
+  const int kend = p.causal ? min(Lk, max(end + off, 0)) : Lk;
+  const int nt = (kend + kBn - 1) / kBn;
+
+  const TileLane L(lane);
+  const int qi = first + 32 * w + L.row, qc = min(qi, Lq - 1);
+  const int see = p.causal ? min(Lk, qi + off + 1) : Lk;
+  const int wave_all = p.causal ? min(Lk, first + 32 * w + off + 1) : Lk;
+  const int wave_any = p.causal ? min(Lk, first + 32 * w + 32 + off) : Lk;
+
+  const uint16_t* kv = p.kv + (int64_t)k0 * p.kv_stride + head * (kNope + kVDim);
+  const uint16_t* kr = p.k_rope + (int64_t)k0 * p.rope_stride;
+  const uint32_t lds = lds_offset(tiles);
+  if (nt > 0) load_keys<NW>(p, kv, kr, 0, Lk - 1, w, lane, lds);
+
+  bf16x8 qf[12], df[8];
+  load_operand(qf, p.q + (int64_t)(u.r0 + qc) * p.q_stride + head * kQk, L.half);
+  load_operand(df, p.dout + ((int64_t)(u.r0 + qc) * p.H + head) * kVDim, L.half);
+  const float lse = p.lse[(int64_t)head * p.Tq + u.r0 + qc] * kLog2e;
+  const float delta = p.delta[(int64_t)head * p.Tq + u.r0 + qc];
+  const float c = p.scale * kLog2e;
+  f32x16 dq[6];
+#pragma unroll
+  for (int d = 0; d < 6; ++d) dq[d] = zero16();
+
+  for (int t = 0; t < nt; ++t) {
+    attn_wait<0>();
+    attn_barrier();
+    if (t + 1 < nt) load_keys<NW>(p, kv, kr, (t + 1) * kBn, Lk - 1, w, lane, lds + ((t + 1) & 1) * kFwdTile);
+    const char* tl = tiles + (t & 1) * kFwdTile;
+    const char* vt = tl + kNopeTile + kRopeTile;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      const int key0 = t * kBn + 32 * kb;
+      if (key0 >= wave_any) continue;
+      f32x16 s = scores(tl, L, 32 * kb, qf), dp = zero16();
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) dp = mfma32(rows256(vt, L, 32 * kb, ks), df[ks], dp);
+      const bool edge = key0 + 32 > wave_all;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float e = exp2_fast(fmaf(s[i], c, -lse));
+        if (edge && key0 + drow(i, L.half) >= see) e = 0.f;
+        dp[i] = e * (dp[i] - delta);
+      }
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        const bf16x8 sb = pack8(dp, a);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) dq[d] = mfma32(cols256(tl, L, 32 * kb + 16 * a, d), sb, dq[d]);
+#pragma unroll
+        for (int d = 0; d < 2; ++d) dq[4 + d] = mfma32(cols128(tl + kNopeTile, L, 32 * kb + 16 * a, d), sb, dq[4 + d]);
+      }
+    }
+  }
+  if (qi < Lq) {
+    uint16_t* op = p.dq + ((int64_t)(u.r0 + qi) * p.H + head) * kQk + 4 * L.half;
+#pragma unroll
+    for (int d = 0; d < 6; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        bf16x4 b;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[j] = (__bf16)(dq[d][4 * i + j] * p.scale);
+        *reinterpret_cast<bf16x4*>(op + 32 * d + 8 * i) = b;
+      }
+  }
+}
+
+// dk_rope = sum of the heads' rotary gradients, in head order.
+__global__ __launch_bounds__(256) void mla_rope_sum_kernel(const MlaPrefill p) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, n = (int64_t)p.Tk * kRopeDim;
+  if (i >= n) return;
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+  for (int h = 0; h < p.H; ++h) sum += *reinterpret_cast<const f32x4*>(p.rope_part + h * n + i);
+  bf16x4 b;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) b[j] = (__bf16)sum[j];
+  *reinterpret_cast<bf16x4*>(p.dk_rope + i) = b;
+}
+
+// Blocks of a packed batch, at most: every request ends inside one.
+int64_t blocks(int64_t tokens, int B, int rows) { return (tokens + rows - 1) / rows + B; }
+
+}  // namespace
+
+hipError_t launch_mla_prefill(const MlaPrefill& p, hipStream_t stream) {
+  const int64_t units = blocks(p.Tq, p.B, 128);
+  hipLaunchKernelGGL(mla_fwd_kernel<4>, dim3(unit_grid(units, p.H)), dim3(256), 0, stream, p, (int)units);
+  return hipGetLastError();
+}
+
+hipError_t launch_mla_prefill_bwd(const MlaPrefill& p, hipStream_t stream) {
+  const int64_t rows = (int64_t)p.Tq * p.H;
+  if (p.Tq > 0) {
+    hipLaunchKernelGGL(mla_delta_kernel, dim3((unsigned)((rows + 15) / 16)), dim3(256), 0, stream, p);
+    const int64_t units = blocks(p.Tq, p.B, 128);
+    hipLaunchKernelGGL(mla_dq_kernel<4>, dim3(unit_grid(units, p.H)), dim3(256), 0, stream, p, (int)units);
+  }
+  if (p.Tk > 0) {
+    const int64_t units = blocks(p.Tk, p.B, 128);
+    hipLaunchKernelGGL(mla_dkv_kernel, dim3(unit_grid(units, p.H)), dim3(256), 0, stream, p, (int)units);
+    hipLaunchKernelGGL(mla_rope_sum_kernel, dim3((unsigned)(((int64_t)p.Tk * kRopeDim / 4 + 255) / 256)), dim3(256), 0,
+                       stream, p);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace fp8bs

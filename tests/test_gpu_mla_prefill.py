@@ -1,0 +1,172 @@
+"""Expanded latent attention on the GPU, forward and gradients, against the
+float64 oracle: every element inside the bound that follows from rounding the
+probabilities (and dS) and the outputs to BF16."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import attention as oa
+
+import fp8_block_scaled_x1_amd as fb
+
+pytestmark = pytest.mark.gpu
+SCALE = 192 ** -0.5
+
+
+def _f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _off(lens):
+    return np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+
+
+def _inputs(dev, lens, H, seed, std=1.5):
+    g = torch.Generator().manual_seed(seed)
+    cq, ck = _off([a for a, _ in lens]), _off([b for _, b in lens])
+    q = (torch.randn((cq[-1], H, 192), generator=g) * std).to(torch.bfloat16).to(dev)
+    kv = torch.randn((ck[-1], H, 256), generator=g).to(torch.bfloat16).to(dev)
+    kr = torch.randn((ck[-1], 64), generator=g).to(torch.bfloat16).to(dev)
+    dout = torch.randn((cq[-1], H, 128), generator=g).to(torch.bfloat16).to(dev)
+    return q, kv, kr, dout, cq, ck
+
+
+def _inside(got, ref, what):
+    want, bound = ref
+    got = _f64(got)
+    assert got.shape == want.shape, what
+    same_inf = np.isneginf(want) & np.isneginf(got)
+    with np.errstate(invalid="ignore"):
+        bad = ~(same_inf | (np.abs(got - want) <= bound))
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} outside, first at {tuple(np.argwhere(bad)[0])}: " \
+                          f"{got[bad][0]} against {want[bad][0]} +- {bound[bad][0]}"
+
+
+def _check(dev, lens, H, causal, seed=0, scale=SCALE, std=1.5):
+    q, kv, kr, dout, cq, ck = _inputs(dev, lens, H, seed, std)
+    tq, tk = torch.from_numpy(cq).to(dev), torch.from_numpy(ck).to(dev)
+    out, lse = fb.fp8bs_mla_prefill(q, kv, kr, tq, tk, scale, causal=causal)
+    grads = fb.fp8bs_mla_prefill_bwd(dout, q, kv, kr, out, lse, tq, tk, scale, causal=causal)
+    torch.cuda.synchronize()
+    ref = oa.mla_prefill(_f64(q), _f64(kv), _f64(kr), cq, ck, scale, causal, _f64(dout))
+    _inside(out, ref["out"], f"out {lens} {causal}")
+    _inside(lse, ref["lse"], f"lse {lens} {causal}")
+    for name, x in zip(("dq", "dkv", "dk_rope"), grads):
+        _inside(x, ref[name], f"{name} {lens} {causal}")
+
+
+LENS = [
+    [(1, 1)],
+    [(1, 200)],
+    [(64, 64), (65, 65), (63, 63)],
+    [(128, 128), (129, 129)],
+    [(33, 97), (1, 64), (127, 191)],                # chunks behind cached tokens, ends inside tiles
+    [(260, 260)],
+    [(5, 0), (0, 7), (3, 3), (0, 0)],               # no keys, no queries, neither
+    [(70, 20), (200, 130), (2, 1)],                 # causal rows that see nothing
+    [(40, 300), (150, 513)],
+]
+
+
+@pytest.mark.parametrize("lens", LENS, ids=str)
+@pytest.mark.parametrize("causal", [True, False])
+def test_against_oracle(dev, lens, causal):
+    _check(dev, lens, 3, causal, seed=len(lens))
+
+
+@pytest.mark.parametrize("H", [1, 2, 5, 8, 16, 24])
+def test_head_counts(dev, H):
+    _check(dev, [(77, 77), (1, 130)], H, True, seed=H)
+
+
+@pytest.mark.parametrize("std,scale", [(0.01, SCALE), (12.0, SCALE), (1.0, 1e-4), (1.0, 1.0)])
+def test_flat_and_peaked_scores(dev, std, scale):
+    _check(dev, [(90, 90), (40, 100)], 2, True, seed=7, scale=scale, std=std)
+
+
+def test_many_short_requests(dev):
+    rng = np.random.default_rng(2)
+    _check(dev, [(int(n), int(n + e)) for n, e in zip(rng.integers(0, 9, 150), rng.integers(0, 4, 150))], 2, True)
+
+
+def test_tokens_with_gaps(dev):
+    # q, kv and k_rope as slices of wider rows, as a fused projection leaves them
+    q, kv, kr, dout, cq, ck = _inputs(dev, [(50, 50), (90, 120)], 4, 3)
+    tq, tk = torch.from_numpy(cq).to(dev), torch.from_numpy(ck).to(dev)
+    ref = fb.fp8bs_mla_prefill(q, kv, kr, tq, tk, SCALE)
+    wide = torch.full((len(q), 4 * 192 + 64), float("nan"), dtype=torch.bfloat16, device=dev)
+    wide[:, 64:] = q.reshape(len(q), -1)
+    wkv = torch.full((len(kv), 4 * 256 + 8), float("nan"), dtype=torch.bfloat16, device=dev)
+    wkv[:, :-8] = kv.reshape(len(kv), -1)
+    lat = torch.full((len(kr), 576), float("nan"), dtype=torch.bfloat16, device=dev)
+    lat[:, 512:] = kr
+    views = wide[:, 64:].unflatten(1, (4, 192)), wkv[:, :-8].unflatten(1, (4, 256)), lat[:, 512:]
+    got = fb.fp8bs_mla_prefill(*views, tq, tk, SCALE)
+    for a, b in zip(got, ref):
+        assert torch.equal(a, b)
+    for a, b in zip(fb.fp8bs_mla_prefill_bwd(dout, *views, *got, tq, tk, SCALE),
+                    fb.fp8bs_mla_prefill_bwd(dout, q, kv, kr, *ref, tq, tk, SCALE)):
+        assert torch.equal(a, b)
+    with pytest.raises(fb.Fp8bsError):          # 193 numbers apart: not 16-byte aligned
+        fb.fp8bs_mla_prefill(torch.zeros(8, 193, dtype=torch.bfloat16, device=dev)[:, :192].unflatten(1, (1, 192)),
+                             kv[:8, :1].contiguous(), kr[:8], tq[:2] * 0, tk[:2] * 0, SCALE)
+    with pytest.raises(ValueError, match="contiguous"):
+        fb.fp8bs_mla_prefill(q.transpose(0, 1).contiguous().transpose(0, 1), kv, kr, tq, tk, SCALE)
+
+
+def test_requests_do_not_see_each_other(dev):
+    # a request's results do not depend on its neighbours in the batch, nor on their values
+    q, kv, kr, dout, cq, ck = _inputs(dev, [(60, 60), (61, 100), (200, 200)], 2, 4)
+    tq, tk = torch.from_numpy(cq).to(dev), torch.from_numpy(ck).to(dev)
+    out, lse = fb.fp8bs_mla_prefill(q, kv, kr, tq, tk, SCALE)
+    i, j = slice(cq[1], cq[2]), slice(ck[1], ck[2])
+    one = [torch.tensor([0, n], dtype=torch.int32, device=dev) for n in (61, 100)]
+    o1, l1 = fb.fp8bs_mla_prefill(q[i].contiguous(), kv[j].contiguous(), kr[j].contiguous(), *one, SCALE)
+    assert torch.equal(out[i], o1) and torch.equal(lse[:, i], l1)
+    q[:cq[1]] = float("nan")
+    kv[ck[2]:], kr[ck[2]:] = float("inf"), float("nan")
+    o2, l2 = fb.fp8bs_mla_prefill(q, kv, kr, tq, tk, SCALE)
+    assert torch.equal(o2[i], o1) and torch.equal(l2[:, i], l1)
+
+
+def test_long_rows_against_float32(dev):
+    # long enough to rescale often, with ends off every tile: the sampled rows of one head
+    lens = [(1500, 2777)]
+    q, kv, kr, dout, cq, ck = _inputs(dev, lens, 8, 6)
+    tq, tk = torch.from_numpy(cq).to(dev), torch.from_numpy(ck).to(dev)
+    out, lse = fb.fp8bs_mla_prefill(q, kv, kr, tq, tk, SCALE)
+    for h in (0, 7):
+        K = np.concatenate([_f64(kv[:, h, :128]), _f64(kr)], -1)
+        for row in (0, 1, 127, 128, 700, 1499):
+            n = row + 1 + 2777 - 1500
+            o, l, bo, bl = oa.mla_head(_f64(q[row:row + 1, h]), K[:n], _f64(kv[:n, h, 128:]), SCALE, False)
+            _inside(out[row:row + 1, h], (o, bo), f"row {row} head {h}")
+            _inside(lse[h, row:row + 1], (l, bl), f"lse {row} head {h}")
+
+
+def test_same_bits_every_time_and_in_a_graph(dev):
+    q, kv, kr, dout, cq, ck = _inputs(dev, [(130, 130), (70, 200)], 8, 9)
+    tq, tk = torch.from_numpy(cq).to(dev), torch.from_numpy(ck).to(dev)
+
+    def step():
+        out, lse = fb.fp8bs_mla_prefill(q, kv, kr, tq, tk, SCALE)
+        return (out, lse, *fb.fp8bs_mla_prefill_bwd(dout, q, kv, kr, out, lse, tq, tk, SCALE))
+
+    ref = [x.clone() for x in step()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for a, b in zip(step(), ref):
+            assert torch.equal(a, b)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        res = step()
+    for _ in range(3):
+        for x in res:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(res, ref):
+            assert torch.equal(a, b)
