@@ -39,44 +39,50 @@ int prefill_sizes(int B, int64_t Tq, int64_t Tk, int H, int64_t q_stride, int64_
 
 // ---- absorbed form ----
 
+// Sizes of one problem (the requests' own tokens, or the prefix) and its
+// share of the workspace.
 struct DecodeSizes {
-  int64_t rows, max_len, part_floats, ml_floats;
-  fp8bs::MlaDecode p;
+  int B;                        // requests
+  int64_t rows, all_rows;       // of a request, of all
+  int64_t max_len;
+  int block_rows, groups;
+  int64_t row_blocks;
+  int64_t pieces;               // partials of a request's rows
+  int64_t bytes_out() const { return align256(4 * pieces * rows * 512); }
+  int64_t bytes() const { return bytes_out() + align256(4 * pieces * rows * 2); }
 };
 
-// Sizes of one problem (the requests' own tokens, or the prefix's) and its
-// share of the workspace. joined: every piece is kept as a partial.
-int decode_sizes(int B, int64_t rows, int64_t width, int page, bool joined, DecodeSizes& s) {
+int decode_sizes(int B, int64_t rows, int64_t all_rows, int64_t width, int page, bool joined, DecodeSizes& s) {
   if (width > kI32 / page - kTile) return FP8BS_ERR_TOO_LARGE;
+  s.B = B;
   s.rows = rows;
+  s.all_rows = all_rows;
   s.max_len = width * page;
   const int64_t tiles = (int64_t)B * ((s.max_len + kTile - 1) / kTile);
   if (tiles >= kI32) return FP8BS_ERR_TOO_LARGE;
-  int64_t row_blocks = 0;
-  fp8bs::mla_decode_plan(rows, tiles, &s.p.block_rows, &row_blocks, &s.p.groups);
-  if (((int64_t)s.p.groups + 8) * row_blocks > kGridMax) return FP8BS_ERR_TOO_LARGE;
-  s.p.row_blocks = (int)row_blocks;
-  const int64_t pieces = 2 * (int64_t)s.p.groups + (joined ? B : 0);
-  s.part_floats = pieces * rows * 512;
-  s.ml_floats = pieces * rows * 2;
+  s.block_rows = fp8bs::mla_decode_block_rows(rows);
+  s.row_blocks = (rows + s.block_rows - 1) / s.block_rows;
+  s.groups = fp8bs::mla_decode_groups(s.row_blocks, tiles);
+  if (s.groups * s.row_blocks > kGridMax) return FP8BS_ERR_TOO_LARGE;
+  s.pieces = 2 * (int64_t)s.groups + (joined ? B : 0);
   return FP8BS_OK;
 }
-
-int64_t decode_bytes(const DecodeSizes& s) { return align256(4 * s.part_floats) + align256(4 * s.ml_floats); }
 
 int decode_plan(int B, int T, int H, int64_t width, int page, int64_t prefix_pages, DecodeSizes& own,
                 DecodeSizes& prefix) {
   if (B < 0 || T < 1 || H < 1 || width < 0 || page < 1 || prefix_pages < 0) return FP8BS_ERR_SHAPE;
-  const int64_t rows = (int64_t)T * H;
-  if (rows >= 1 << 24 || B * rows >= kI32 / 8) return FP8BS_ERR_TOO_LARGE;
-  int st = decode_sizes(B, rows, width, page, prefix_pages > 0, own);
-  if (st == FP8BS_OK && prefix_pages > 0) st = decode_sizes(1, B * rows, prefix_pages, page, true, prefix);
-  return st;
+  const int64_t rows = (int64_t)T * H, all = B * rows;
+  if (rows >= 1 << 24 || all >= kI32 / 8) return FP8BS_ERR_TOO_LARGE;
+  int st = decode_sizes(B, rows, all, width, page, prefix_pages > 0, own);
+  if (st != FP8BS_OK || prefix_pages == 0) return st;
+  // the prefix: every block of everyone's rows is a request over the same tokens
+  const int block = fp8bs::mla_decode_block_rows(all);
+  return decode_sizes((int)((all + block - 1) / block), block, all, prefix_pages, page, true, prefix);
 }
 
 void fill(fp8bs::MlaDecode& p, const uint16_t* q, const void* cache, const float* scales, const uint16_t* rope,
-          int64_t pages, int page, const int32_t* table, int64_t width, const int32_t* lens, int B, int tokens,
-          int heads, const DecodeSizes& s, float scale, uint16_t* out, float* lse, bool join, char*& ws) {
+          int64_t pages, int page, const int32_t* table, int64_t width, const int32_t* lens, const DecodeSizes& s,
+          float scale, uint16_t* out, float* lse, bool join, char*& ws) {
   p.q = q;
   p.cache = static_cast<const char*>(cache);
   p.scales = reinterpret_cast<const char*>(scales);
@@ -84,10 +90,10 @@ void fill(fp8bs::MlaDecode& p, const uint16_t* q, const void* cache, const float
   p.table = table;
   p.lens = lens;
   p.table_stride = width;
-  p.B = B;
+  p.len_stride = 1;
+  p.B = s.B;
   p.rows = (int)s.rows;
-  p.tokens = tokens;
-  p.heads = heads;
+  p.all_rows = s.all_rows;
   p.pages = (int)pages;
   p.page = page;
   p.max_len = (int)s.max_len;
@@ -98,16 +104,15 @@ void fill(fp8bs::MlaDecode& p, const uint16_t* q, const void* cache, const float
   p.page_shift = 31 + L;
   p.page_magic = (uint32_t)(((uint64_t)1 << (31 + L)) / (uint64_t)page + 1);
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.block_rows = s.p.block_rows;
-  p.row_blocks = s.p.row_blocks;
-  p.groups = s.p.groups;
+  p.block_rows = s.block_rows;
+  p.row_blocks = (int)s.row_blocks;
+  p.groups = s.groups;
   p.join = join;
   p.out = out;
   p.lse = lse;
   p.part = reinterpret_cast<float*>(ws);
-  ws += align256(4 * s.part_floats);
-  p.part_ml = reinterpret_cast<float*>(ws);
-  ws += align256(4 * s.ml_floats);
+  p.part_ml = reinterpret_cast<float*>(ws + s.bytes_out());
+  ws += s.bytes();
 }
 
 int decode(const uint16_t* q, int kind, const void* cache, const float* scales, const uint16_t* rope, int64_t pages,
@@ -134,11 +139,15 @@ int decode(const uint16_t* q, int kind, const void* cache, const float* scales, 
   char* ws = static_cast<char*>(workspace);
   fp8bs::MlaDecode a{}, b{};
   const bool join = prefix_pages > 0;
-  fill(a, q, cache, scales, rope, pages, page, table, width, lens, B, T, H, own, scale, out, lse, join, ws);
-  // the prefix: one request whose rows are everyone's, nothing hidden
-  if (join)
-    fill(b, q, cache, scales, rope, pages, page, prefix_table, prefix_pages, prefix_len, 1, 1, (int)prefix.rows, prefix,
-         scale, out, lse, true, ws);
+  fill(a, q, cache, scales, rope, pages, page, table, width, lens, own, scale, out, lse, join, ws);
+  a.tokens = T;
+  a.heads = H;
+  if (join) {
+    fill(b, q, cache, scales, rope, pages, page, prefix_table, 0, prefix_len, prefix, scale, out, lse, true, ws);
+    b.len_stride = 0;
+    b.tokens = 1;              // it hides nothing
+    b.heads = b.rows;
+  }
   return status_of(fp8bs::launch_mla_decode(a, join ? &b : nullptr, kind == FP8BS_CACHE_FP8, as_stream(stream)));
 }
 
@@ -211,7 +220,7 @@ int64_t fp8bs_mla_decode_workspace_bytes(int B, int T, int H, int64_t table_widt
   DecodeSizes own{}, prefix{};
   const int st = decode_plan(B, T, H, table_width, page, prefix_pages, own, prefix);
   if (st != FP8BS_OK) return st;
-  return decode_bytes(own) + (prefix_pages > 0 ? decode_bytes(prefix) : 0);
+  return own.bytes() + (prefix_pages > 0 ? prefix.bytes() : 0);
 }
 
 int fp8bs_mla_decode(const uint16_t* q, int cache_kind, const void* cache, const float* cache_scales,

@@ -66,6 +66,13 @@ __device__ __forceinline__ void attn_wait() {
 // loads in flight stay in flight.
 __device__ __forceinline__ void attn_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
+// Keeps the compiler from computing what follows from v ahead of the loop (one
+// XOR next to its use is cheaper than a register held for the whole loop).
+__device__ __forceinline__ int opaque(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 __device__ __forceinline__ bf16x8 lds_bf16x8(const char* p) { return *reinterpret_cast<const bf16x8*>(p); }
 
 // Transposing LDS read of 16-bit elements: each group of 16 lanes reads a

@@ -41,7 +41,9 @@ struct MlaDecode {
   const int32_t* table;   // [B][table_stride]
   const int32_t* lens;    // [B]
   int64_t table_stride;
-  int B, rows, tokens, heads;   // rows = tokens * heads
+  int len_stride;         // 0: one length (and, table_stride 0, one table) for all
+  int B, rows, tokens, heads;   // rows of a request: tokens * heads
+  int64_t all_rows;       // rows of all requests (the last may have fewer)
   int pages, page, max_len;
   uint32_t page_magic;    // tok / page = (tok * page_magic) >> page_shift
   int page_shift;
@@ -54,7 +56,8 @@ struct MlaDecode {
   float* part_ml;         // [2 groups + B][rows][2]
 };
 
-void mla_decode_plan(int64_t rows, int64_t max_tiles, int* block_rows, int64_t* row_blocks, int* groups);
+int mla_decode_block_rows(int64_t rows);
+int mla_decode_groups(int64_t row_blocks, int64_t max_tiles);
 hipError_t launch_mla_decode(const MlaDecode& own, const MlaDecode* prefix, bool fp8, hipStream_t stream);
 
 struct VerifyDrafts {

@@ -42,25 +42,34 @@ namespace {
 
 constexpr int kTile = 64;            // tokens per tile
 constexpr int kLatent = 512, kRope = 64, kKey = kLatent + kRope;
-constexpr int kThreads = 256;
+constexpr int kWaitVmcnt0 = 0x0F70;   // s_waitcnt vmcnt(0), the other counters left alone
+constexpr int kJoinThreads = 256;
+// The weights' reference only follows the running maximum once that is more
+// than 2^8 above it: weights up to 2^8 cost no precision in FP32 or BF16, and
+// the accumulators are rescaled a few times per request instead of per tile.
+constexpr float kSlack = 8.f;
 
-template <bool FP8>
+template <bool FP8, int NW>
 struct Tile {
   static constexpr int kRowBytes = FP8 ? kLatent : 2 * kLatent;
   static constexpr int kLatentBytes = kTile * kRowBytes;
   static constexpr int kRopeBytes = kTile * 2 * kRope;
   static constexpr int kScaleBytes = FP8 ? kTile * 16 : 0;
   static constexpr int kBytes = kLatentBytes + kRopeBytes + kScaleBytes;
-  static constexpr int kLoads = FP8 ? 8 + 2 + 1 : 16 + 2;   // per wave
+  static constexpr int kRows = kTile / NW;                  // that one wave loads
+  static constexpr int kLoads = FP8 ? kRows / 2 + kRows / 8 + 1 : kRows + kRows / 8;
 };
 
 // 16-byte chunk swizzles of LDS row r (the loads permute the source chunks, so
-// LDS itself is written linearly). Whole rows of 256 bytes and more: 16 rows
-// at one chunk (key reads), and rows 0..7 and 8..15 at a pair of chunks (value
-// reads) or, for bytes, rows 0..7 and 16..23 at one chunk, fall on distinct
-// banks. 128-byte rows: 16 rows at one chunk do.
-__device__ __forceinline__ int swz_bf16(int r) { return ((r & 7) << 1) | ((r >> 3) & 1); }
-__device__ __forceinline__ int swz_fp8(int r) { return (r & 7) | ((((r >> 3) ^ (r >> 4)) & 1) << 3); }
+// LDS itself is written linearly). The LDS serves a 16-byte read in groups of
+// 16 lanes, {0-3, 12-15, 20-27}, {4-11, 16-19, 28-31} and the same from 32, and
+// an 8-byte read in halves of the wave. A key read (lane: row lane%16, chunk
+// 4*ks + lane/16) thus meets rows 0-3, 12-15 at one chunk and 4-11 at its
+// neighbour; a value read rows 0-7 (8-15) at a pair of chunks, or, for bytes,
+// rows 0-7 and 16-23 (8-15, 24-31) at one chunk. All of these touch every bank
+// once. Rows of 128 bytes (rotary part): key reads do.
+__device__ __forceinline__ int swz_bf16(int r) { return (((r & 7) ^ ((r >> 1) & 4)) << 1) | ((r >> 3) & 1); }
+__device__ __forceinline__ int swz_fp8(int r) { return swz_bf16(r) ^ ((r >> 4) & 1); }
 __device__ __forceinline__ int swz_rope(int r) { return (r >> 1) & 7; }
 
 // The tiles of a request, and the request a tile belongs to.
@@ -72,7 +81,7 @@ struct Cursor {
   int left;     // tiles left in the group's range, this one included
 };
 
-__device__ __forceinline__ int clamp_len(const MlaDecode& p, int b) { return min(max(p.lens[b], 0), p.max_len); }
+__device__ __forceinline__ int clamp_len(const MlaDecode& p, int b) { return min(max(p.lens[b * p.len_stride], 0), p.max_len); }
 
 __device__ __forceinline__ void advance(const MlaDecode& p, Cursor& c) {
   --c.left;
@@ -137,149 +146,171 @@ __device__ __forceinline__ int page_of(const MlaDecode& p, int tok) {
   return (int)(((uint64_t)(uint32_t)tok * p.page_magic) >> p.page_shift);
 }
 
-// Wave w's token row of a tile for this lane: row 16w + lane%16. Tokens past
-// the end repeat the last one: always cached, and masked by its position.
-__device__ __forceinline__ int row_token(const Cursor& c, int w, int lane) {
-  return min(c.tile * kTile + 16 * w + (lane & 15), c.len - 1);
+// Token of row 16*rg + lane%16 of a tile. Tokens past the end repeat the last
+// one: always cached, and masked by its position.
+__device__ __forceinline__ int row_token(const Cursor& c, int rg, int lane) {
+  return min(c.tile * kTile + 16 * rg + (lane & 15), c.len - 1);
 }
 
-__device__ __forceinline__ void load_entries(const MlaDecode& p, const Cursor& c, int w, int lane, uint32_t lds) {
-  const int tok = row_token(c, w, lane);
+__device__ __forceinline__ void load_entries(const MlaDecode& p, const Cursor& c, int rg, int lane, uint32_t lds) {
+  const int tok = row_token(c, rg, lane);
   dma4(p.table + (int64_t)c.b * p.table_stride + page_of(p, tok), lds);
 }
 
-template <bool FP8>
+// The wave's kRows rows of a tile, whose block-table entries (of the 16-row
+// group they are in) lane%16 holds.
+template <bool FP8, int NW>
 __device__ __forceinline__ void load_tile(const MlaDecode& p, const Cursor& c, int w, int lane, int entry,
                                           uint32_t lds) {
-  using T = Tile<FP8>;
-  const int tok = row_token(c, w, lane);
+  using T = Tile<FP8, NW>;
+  const int rg = w * T::kRows / 16, r0 = w * T::kRows % 16;
+  const int tok = row_token(c, rg, lane);
   const int pg = min(max(entry, 0), p.pages - 1);
   const int64_t flat = (int64_t)pg * p.page + (tok - page_of(p, tok) * p.page);
   const int lo = (int)(uint32_t)flat, hi = (int)(flat >> 32);
   if constexpr (!FP8) {
-    // 16 rows of 1024 latent bytes, one per load: the row is wave-uniform
+    // rows of 1024 latent bytes, one per load: the row is wave-uniform
+    const int chunk = opaque((lane ^ swz_bf16(r0)) << 4);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int64_t f = ((int64_t)__builtin_amdgcn_readlane(hi, i) << 32) | (uint32_t)__builtin_amdgcn_readlane(lo, i);
-      dma16_s(p.cache + f * (2 * kKey), (uint32_t)((lane ^ swz_bf16(i)) << 4), lds + (16 * w + i) * T::kRowBytes);
+    for (int i = 0; i < T::kRows; ++i) {
+      const int64_t f = ((int64_t)__builtin_amdgcn_readlane(hi, r0 + i) << 32) |
+                        (uint32_t)__builtin_amdgcn_readlane(lo, r0 + i);
+      dma16_s(p.cache + f * (2 * kKey), (uint32_t)(chunk ^ (swz_bf16(i) << 4)),
+              lds + (16 * rg + r0 + i) * T::kRowBytes);
     }
   } else {
     // two rows of 512 code bytes per load
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t f0 = ((int64_t)__builtin_amdgcn_readlane(hi, 2 * i) << 32) | (uint32_t)__builtin_amdgcn_readlane(lo, 2 * i);
-      const int64_t f1 =
-          ((int64_t)__builtin_amdgcn_readlane(hi, 2 * i + 1) << 32) | (uint32_t)__builtin_amdgcn_readlane(lo, 2 * i + 1);
-      const int r = 16 * w + 2 * i + (lane >> 5);
+    for (int i = 0; i < T::kRows; i += 2) {
+      const int64_t f0 = ((int64_t)__builtin_amdgcn_readlane(hi, r0 + i) << 32) |
+                         (uint32_t)__builtin_amdgcn_readlane(lo, r0 + i);
+      const int64_t f1 = ((int64_t)__builtin_amdgcn_readlane(hi, r0 + i + 1) << 32) |
+                         (uint32_t)__builtin_amdgcn_readlane(lo, r0 + i + 1);
+      const int r = 16 * rg + r0 + i + (lane >> 5);
       dma16(p.cache + (lane < 32 ? f0 : f1) * kLatent + (((lane & 31) ^ swz_fp8(r)) << 4),
-            lds + (16 * w + 2 * i) * T::kRowBytes);
+            lds + (16 * rg + r0 + i) * T::kRowBytes);
     }
   }
   // rotary part: 8 rows of 128 bytes per load
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int src = 8 * i + (lane >> 3);
+  for (int i = 0; i < T::kRows; i += 8) {
+    const int src = r0 + i + (lane >> 3);
     const int64_t f = ((int64_t)__shfl(hi, src, 64) << 32) | (uint32_t)__shfl(lo, src, 64);
-    const int chunk = (lane & 7) ^ swz_rope(16 * w + src);
+    const int chunk = (lane & 7) ^ swz_rope(16 * rg + src);
     const char* row = FP8 ? p.rope + f * (2 * kRope) : p.cache + f * (2 * kKey) + 2 * kLatent;
-    dma16(row + (chunk << 4), lds + T::kLatentBytes + (16 * w + 8 * i) * (2 * kRope));
+    dma16(row + (chunk << 4), lds + T::kLatentBytes + (16 * rg + r0 + i) * (2 * kRope));
   }
   if constexpr (FP8) {
+    // the scales of the 16-row group (with 8 waves two of them load the same)
     const int src = lane >> 2;
     const int64_t f = ((int64_t)__shfl(hi, src, 64) << 32) | (uint32_t)__shfl(lo, src, 64);
-    dma4(p.scales + f * 16 + (lane & 3) * 4, lds + T::kLatentBytes + T::kRopeBytes + 16 * w * 16);
+    dma4(p.scales + f * 16 + (lane & 3) * 4, lds + T::kLatentBytes + T::kRopeBytes + 16 * rg * 16);
   }
 }
 
-template <int NR, bool FP8, int NBUF>
-__global__ __launch_bounds__(kThreads, 1) void mla_decode_kernel(const MlaDecode p) {
-  using T = Tile<FP8>;
-  constexpr int NB = NR / 16;                       // 16-row blocks
+// TEAMS teams of 4 waves, each with its own NR rows, share the tiles in LDS.
+template <int NR, int TEAMS, bool FP8, int NBUF>
+__global__ __launch_bounds__(256 * TEAMS) void mla_decode_kernel(const MlaDecode p) {
+  constexpr int NW = 4 * TEAMS;
+  using T = Tile<FP8, NW>;
+  constexpr int NB = NR / 16;                       // 16-row blocks of a team
   constexpr int kProbBytes = kTile * NR * (FP8 ? 4 : 2);
   __shared__ __align__(1024) char tiles[NBUF * T::kBytes];
-  __shared__ __align__(16) char probs[kProbBytes];
-  __shared__ __align__(16) float stat[4 * NR];
-  __shared__ __align__(16) int entries[4][64];
+  __shared__ __align__(16) char team_probs[TEAMS * kProbBytes];
+  __shared__ __align__(16) float team_stat[TEAMS * 4 * NR];
+  __shared__ __align__(16) int entries[NW][64];
 
   const int lane = threadIdx.x & 63, n16 = lane & 15, g4 = lane >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int w = wave & 3, team = wave >> 2, rg = wave * T::kRows / 16;
+  char* const probs = team_probs + team * kProbBytes;
+  float* const stat = team_stat + team * 4 * NR;
 
-  // workgroup -> (group, row block), the row blocks of a group on one XCD
-  const int xcd = blockIdx.x % kAttnXcds, slot = blockIdx.x / kAttnXcds;
-  const int g = (slot / p.row_blocks) * kAttnXcds + xcd, rb = slot % p.row_blocks;
-  if (g >= p.groups) return;
+  // workgroup -> (group, row block): workgroups are dealt over the XCDs one by
+  // one; renumbered so that an XCD's are consecutive, row blocks of a group first
+  const int per = gridDim.x / kAttnXcds, rest = gridDim.x % kAttnXcds;
+  const int xcd = blockIdx.x % kAttnXcds;
+  const int wg = xcd * per + min(xcd, rest) + blockIdx.x / kAttnXcds;
+  const int g = wg / p.row_blocks;
+  const int row0 = ((wg - g * p.row_blocks) * TEAMS + team) * NR;      // the team's first row
   const int total = total_tiles(p);
   const int t0 = range_start(g, total, p.groups), t1 = range_start(g + 1, total, p.groups);
   if (t0 >= t1) return;
 
-  const uint32_t lds_tiles = lds_offset(tiles), lds_entries = lds_offset(entries[w]);
+  const uint32_t lds_tiles = lds_offset(tiles), lds_entries = lds_offset(entries[wave]);
   Cursor cur = locate(p, t0, t1 - t0);
   Cursor nxt = cur;      // the tile that is loaded next
   Cursor ent = cur;      // the tile whose block-table entries are fetched next
 #pragma unroll
   for (int i = 0; i < NBUF - 1; ++i) {
     if (nxt.left > 0) {
-      load_entries(p, ent, w, lane, lds_entries);
+      load_entries(p, ent, rg, lane, lds_entries);
       advance(p, ent);
       attn_wait<0>();
-      load_tile<FP8>(p, nxt, w, lane, entries[w][lane & 15], lds_tiles + i * T::kBytes);
+      load_tile<FP8, NW>(p, nxt, wave, lane, entries[wave][lane & 15], lds_tiles + i * T::kBytes);
       advance(p, nxt);
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
   }
   if (ent.left > 0) {
-    load_entries(p, ent, w, lane, lds_entries);
+    load_entries(p, ent, rg, lane, lds_entries);
     advance(p, ent);
   }
 
-  // loop-invariant LDS offsets of this lane
+  // LDS offsets of this lane: the swizzles only touch bits that the row and
+  // tile offsets leave free, so the chunk is picked by an XOR
   const int krow = 16 * w + n16;                                   // key reads: the wave's token n16
-  const int kx = FP8 ? swz_fp8(krow) : swz_bf16(krow);
+  const int key0 = krow * T::kRowBytes + ((g4 ^ (FP8 ? swz_fp8(krow) : swz_bf16(krow))) << 4);
+  const int rope0 = T::kLatentBytes + krow * (2 * kRope) + ((g4 ^ swz_rope(krow)) << 4);
   const int vrow = FP8 ? ((n16 >> 1) & 3) + 4 * g4 + 16 * (n16 >> 3) : 4 * g4 + (n16 >> 2);
-  const int vx = FP8 ? swz_fp8(vrow) : swz_bf16(vrow);
+  const int val0 = vrow * T::kRowBytes + 8 * (n16 & 1) +
+                   (FP8 ? 256 * (w >> 1) + ((8 * (w & 1) ^ swz_fp8(vrow)) << 4)
+                        : 256 * w + ((((n16 >> 1) & 1) ^ swz_bf16(vrow)) << 4));
 
   bf16x8 qf[NB][kKey / 32];
   f32x4 acc[8][NB];
   float m[NB], l[NB];
   int limit[NB];
-  bool fresh = true, whole = false, first = true;
+  bool first = true;
   int buf = 0;
 
-  while (cur.left > 0) {
-    if (fresh) {      // a new request's rows
-      whole = cur.tile == 0 && cur.left >= cur.tiles;
+  while (cur.left > 0) {      // a request's part of the range
+    const bool whole = cur.tile == 0 && cur.left >= cur.tiles;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        const int row = min(rb * NR + nb * 16 + n16, p.rows - 1);
-        const uint16_t* qr = p.q + ((int64_t)cur.b * p.rows + row) * kKey;
+    for (int nb = 0; nb < NB; ++nb) {
+      const int row = min(row0 + nb * 16 + n16, p.rows - 1);
+      const uint16_t* qr = p.q + min((int64_t)cur.b * p.rows + row, p.all_rows - 1) * kKey;
 #pragma unroll
-        for (int ks = 0; ks < kKey / 32; ++ks) {
-          // FP8: a lane reads 16 codes at a time, the slots of two k steps
-          const int col = FP8 && ks < 16 ? 64 * (ks >> 1) + 16 * g4 + 8 * (ks & 1) : 32 * ks + 8 * g4;
-          qf[nb][ks] = *reinterpret_cast<const bf16x8*>(qr + col);
-        }
-        limit[nb] = cur.len - (p.tokens - 1 - row / p.heads);
-        m[nb] = neg_inf();
-        l[nb] = 0.f;
-#pragma unroll
-        for (int d = 0; d < 8; ++d) acc[d][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int ks = 0; ks < kKey / 32; ++ks) {
+        // FP8: a lane reads 16 codes at a time, the slots of two k steps
+        const int col = FP8 && ks < 16 ? 64 * (ks >> 1) + 16 * g4 + 8 * (ks & 1) : 32 * ks + 8 * g4;
+        qf[nb][ks] = *reinterpret_cast<const bf16x8*>(qr + col);
       }
-      fresh = false;
+      limit[nb] = cur.len - (p.tokens - 1 - row / p.heads);
+      m[nb] = neg_inf();
+      l[nb] = 0.f;
+#pragma unroll
+      for (int d = 0; d < 8; ++d) acc[d][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
+    // said to the compiler, which would otherwise wait for the queries inside
+    // the tile loop and with them for the tiles in flight
+    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+
+    for (bool last = false; !last;) {
     if (nxt.left > 0 && NBUF > 2 && cur.left > 1)
       attn_wait<(NBUF - 2) * (T::kLoads + 1)>();
     else
       attn_wait<0>();
     attn_barrier();
     if (nxt.left > 0) {
-      const int entry = entries[w][lane & 15];
+      const int entry = entries[wave][lane & 15];
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       if (ent.left > 0) {
-        load_entries(p, ent, w, lane, lds_entries);
+        load_entries(p, ent, rg, lane, lds_entries);
         advance(p, ent);
       }
       const int nbuf = buf == 0 ? NBUF - 1 : buf - 1;
-      load_tile<FP8>(p, nxt, w, lane, entry, lds_tiles + nbuf * T::kBytes);
+      load_tile<FP8, NW>(p, nxt, wave, lane, entry, lds_tiles + nbuf * T::kBytes);
       advance(p, nxt);
     }
     const char* tl = tiles + buf * T::kBytes;
@@ -289,15 +320,15 @@ __global__ __launch_bounds__(kThreads, 1) void mla_decode_kernel(const MlaDecode
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) s[nb] = f32x4{0.f, 0.f, 0.f, 0.f};
     if constexpr (!FP8) {
-      const char* kp = tl + krow * T::kRowBytes;
+      const int key = opaque(key0);
 #pragma unroll
       for (int ks = 0; ks < 16; ++ks) {
-        const bf16x8 a = lds_bf16x8(kp + (ks >> 2) * 256 + (((4 * (ks & 3) + g4) ^ kx) << 4));
+        const bf16x8 a = lds_bf16x8(tl + (key ^ ((ks & 3) << 6)) + (ks >> 2) * 256);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) s[nb] = mfma16(a, qf[nb][ks], s[nb]);
       }
     } else {
-      const char* kp = tl + krow * T::kRowBytes;
+      const int key = opaque(key0);
       const char* sp = tl + T::kLatentBytes + T::kRopeBytes + (16 * w + 4 * g4) * 16;
       float sc[4][4];     // [token i][group]
 #pragma unroll
@@ -314,7 +345,7 @@ __global__ __launch_bounds__(kThreads, 1) void mla_decode_kernel(const MlaDecode
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int kp2 = 2 * q + h;      // 64 columns
-          const uint4 c = *reinterpret_cast<const uint4*>(kp + (kp2 >> 2) * 256 + (((4 * (kp2 & 3) + g4) ^ kx) << 4));
+          const uint4 c = *reinterpret_cast<const uint4*>(tl + (key ^ ((kp2 & 3) << 6)) + (kp2 >> 2) * 256);
           const bf16x8 a0 = e4m3_to_bf16(c.x, c.y), a1 = e4m3_to_bf16(c.z, c.w);
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) part[nb] = mfma16(a0, qf[nb][2 * kp2], part[nb]);
@@ -328,10 +359,9 @@ __global__ __launch_bounds__(kThreads, 1) void mla_decode_kernel(const MlaDecode
       }
     }
     {
-      const char* rp = tl + T::kLatentBytes + krow * (2 * kRope);
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        const bf16x8 a = lds_bf16x8(rp + (((4 * ks + g4) ^ swz_rope(krow)) << 4));
+        const bf16x8 a = lds_bf16x8(tl + (rope0 ^ (ks << 6)));
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) s[nb] = mfma16(a, qf[nb][16 + ks], s[nb]);
       }
@@ -355,19 +385,32 @@ __global__ __launch_bounds__(kThreads, 1) void mla_decode_kernel(const MlaDecode
     attn_barrier();
 
     // probabilities against the new maxima, into LDS as the value product's operand
-    float alpha[NB];
+    float ref[NB];
+    bool grown = false;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int n = nb * 16 + n16;
-      const float mt = fmaxf(fmaxf(stat[n], stat[NR + n]), fmaxf(stat[2 * NR + n], stat[3 * NR + n]));
-      const float mn = fmaxf(m[nb], mt);
-      const float ref = mn == neg_inf() ? 0.f : mn;      // nothing visible yet: every weight is 0
-      alpha[nb] = exp2_fast(m[nb] - ref);
-      m[nb] = mn;
+      ref[nb] = fmaxf(fmaxf(stat[n], stat[NR + n]), fmaxf(stat[2 * NR + n], stat[3 * NR + n]));
+      grown |= ref[nb] > m[nb] + kSlack;
+    }
+    if (__any(grown)) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const float mn = fmaxf(m[nb], ref[nb]);
+        const float alpha = mn == neg_inf() ? 1.f : exp2_fast(m[nb] - mn);
+        m[nb] = mn;
+        l[nb] *= alpha;
+#pragma unroll
+        for (int d = 0; d < 8; ++d) acc[d][nb] *= alpha;
+      }
+    }
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      ref[nb] = m[nb] == neg_inf() ? 0.f : m[nb];      // nothing visible yet: every weight is 0
       f32x4 e;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) e[i] = exp2_fast(s[nb][i] - ref);
-      l[nb] = fmaf(l[nb], alpha[nb], (e[0] + e[1]) + (e[2] + e[3]));
+      for (int i = 0; i < 4; ++i) e[i] = exp2_fast(s[nb][i] - ref[nb]);
+      l[nb] += (e[0] + e[1]) + (e[2] + e[3]);
       // [32-token step w/2][row block][lane], half w%2 of the lane's 8 slots
       const int at = (((w >> 1) * NB + nb) * 64 + lane) * 2 + (w & 1);
       if constexpr (FP8) {
@@ -383,11 +426,8 @@ __global__ __launch_bounds__(kThreads, 1) void mla_decode_kernel(const MlaDecode
 
     // output columns 128w .. +127: D[column 4*g4 + i][row n16]
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-      for (int d = 0; d < 8; ++d) acc[d][nb] *= alpha[nb];
-#pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
+      const int val = opaque(val0);
       bf16x8 pb[NB];
       if constexpr (FP8) {
         const float* sp = reinterpret_cast<const float*>(tl + T::kLatentBytes + T::kRopeBytes) + w;
@@ -412,13 +452,10 @@ __global__ __launch_bounds__(kThreads, 1) void mla_decode_kernel(const MlaDecode
       for (int d = 0; d < 8; ++d) {
         bf16x8 a;
         if constexpr (FP8) {
-          const int chunk = 8 * w + d;
-          const i32x2 c = lds_tr8(tl + (32 * kk + vrow) * T::kRowBytes + (((chunk & ~15) | ((chunk & 15) ^ vx)) << 4) +
-                                  8 * (n16 & 1));
+          const i32x2 c = lds_tr8(tl + (val ^ (d << 4)) + 32 * kk * T::kRowBytes);
           a = e4m3_to_bf16((uint32_t)c[0], (uint32_t)c[1]);
         } else {
-          const char* vp = tl + (32 * kk + vrow) * T::kRowBytes + 256 * w + (((2 * d + ((n16 >> 1) & 1)) ^ vx) << 4) +
-                           8 * (n16 & 1);
+          const char* vp = tl + (val ^ (d << 5)) + 32 * kk * T::kRowBytes;
           a = join(lds_tr16(vp), lds_tr16(vp + 16 * T::kRowBytes));
         }
 #pragma unroll
@@ -426,7 +463,7 @@ __global__ __launch_bounds__(kThreads, 1) void mla_decode_kernel(const MlaDecode
       }
     }
 
-    const bool last = cur.tile + 1 == cur.tiles || cur.left == 1;
+    last = cur.tile + 1 == cur.tiles || cur.left == 1;
     if (last) {
       // sums over the lanes' and waves' tokens
 #pragma unroll
@@ -441,9 +478,9 @@ __global__ __launch_bounds__(kThreads, 1) void mla_decode_kernel(const MlaDecode
       const int64_t part = whole ? 2 * p.groups + cur.b : 2 * g + (first ? 0 : 1);
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        const int n = nb * 16 + n16, row = rb * NR + n;
+        const int n = nb * 16 + n16, row = row0 + n;
         const float sum = (stat[n] + stat[NR + n]) + (stat[2 * NR + n] + stat[3 * NR + n]);
-        if (row < p.rows) {
+        if (row < p.rows && (int64_t)cur.b * p.rows + row < p.all_rows) {
           if (final) {
             const int64_t o = (int64_t)cur.b * p.rows + row;
             const float inv = sum > 0.f ? 1.f / sum : 0.f;
@@ -466,10 +503,10 @@ __global__ __launch_bounds__(kThreads, 1) void mla_decode_kernel(const MlaDecode
         }
       }
       first = false;
-      fresh = true;
     }
     advance(p, cur);
     buf = buf + 1 == NBUF ? 0 : buf + 1;
+    }
   }
 }
 
@@ -496,10 +533,8 @@ struct Joiner {
   }
 };
 
-__global__ __launch_bounds__(kThreads) void mla_join_kernel(const MlaDecode p, const MlaDecode prefix) {
-  const int lane = threadIdx.x & 63;
-  const int64_t o = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (o >= (int64_t)p.B * p.rows) return;
+// Adds the partials of one row; false if the row's result is written already.
+__device__ __forceinline__ bool add_pieces(const MlaDecode& p, int64_t o, int lane, Joiner& j) {
   const int b = (int)(o / p.rows), row = (int)(o - (int64_t)b * p.rows);
   // tiles before the request, its own and all
   int before = 0, all = 0;
@@ -511,35 +546,35 @@ __global__ __launch_bounds__(kThreads) void mla_join_kernel(const MlaDecode p, c
   all = wave_sum(all);
   before = wave_sum(before);
   const int own = (clamp_len(p, b) + kTile - 1) / kTile;
+  if (own == 0) return true;
+  // the group of tile t is the last whose range starts at or before it
+  auto group_of = [&](int t) {
+    int g = (int)((int64_t)t * p.groups / all);
+    while (g + 1 < p.groups && range_start(g + 1, all, p.groups) <= t) ++g;
+    while (range_start(g, all, p.groups) > t) --g;
+    return g;
+  };
+  const int g0 = group_of(before), g1 = group_of(before + own - 1);
+  if (g0 == g1) {
+    if (!p.join) return false;
+    j.add(p, 2 * (int64_t)p.groups + b, row, lane);
+    return true;
+  }
+  for (int g = g0; g <= g1; ++g) {
+    const int start = range_start(g, all, p.groups);
+    if (start == range_start(g + 1, all, p.groups)) continue;     // an empty range
+    j.add(p, 2 * (int64_t)g + (start >= before ? 0 : 1), row, lane);
+  }
+  return true;
+}
+
+__global__ __launch_bounds__(kJoinThreads) void mla_join_kernel(const MlaDecode p, const MlaDecode prefix) {
+  const int lane = threadIdx.x & 63;
+  const int64_t o = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (o >= p.all_rows) return;
   Joiner j;
-  if (own > 0) {
-    // the group of tile t is the last whose range starts at or before it
-    auto group_of = [&](int t) {
-      int g = (int)((int64_t)t * p.groups / all);
-      while (g + 1 < p.groups && range_start(g + 1, all, p.groups) <= t) ++g;
-      while (range_start(g, all, p.groups) > t) --g;
-      return g;
-    };
-    const int g0 = group_of(before), g1 = group_of(before + own - 1);
-    if (g0 == g1) {
-      if (!p.join) return;      // one group held all of it and wrote the result
-      j.add(p, 2 * (int64_t)p.groups + b, row, lane);
-    } else {
-      for (int g = g0; g <= g1; ++g) {
-        const int start = range_start(g, all, p.groups);
-        if (start == range_start(g + 1, all, p.groups)) continue;     // an empty range
-        j.add(p, 2 * (int64_t)g + (start >= before ? 0 : 1), row, lane);
-      }
-    }
-  }
-  if (p.join) {
-    const int tiles = (clamp_len(prefix, 0) + kTile - 1) / kTile;
-    for (int g = 0; g < prefix.groups; ++g) {
-      const int a = range_start(g, tiles, prefix.groups), e = range_start(g + 1, tiles, prefix.groups);
-      if (a == e) continue;
-      j.add(prefix, a == 0 && e == tiles ? 2 * (int64_t)prefix.groups : 2 * (int64_t)g, (int)o, lane);
-    }
-  }
+  if (!add_pieces(p, o, lane, j)) return;
+  if (p.join) add_pieces(prefix, o, lane, j);
   const float inv = j.l > 0.f ? 1.f / j.l : 0.f;
   bf16x8 v;
 #pragma unroll
@@ -560,42 +595,40 @@ int compute_units() {
   return cached[dev];
 }
 
-template <int NR>
+template <int NR, int TEAMS>
 void launch_rows(const MlaDecode& p, bool fp8, hipStream_t stream) {
-  const int per_xcd = (p.groups + kAttnXcds - 1) / kAttnXcds;
-  const dim3 grid((unsigned)((int64_t)per_xcd * kAttnXcds * p.row_blocks));
+  const dim3 grid((unsigned)((int64_t)p.groups * p.row_blocks)), block(256 * TEAMS);
   if (fp8)
-    hipLaunchKernelGGL((mla_decode_kernel<NR, true, 2>), grid, dim3(kThreads), 0, stream, p);
+    hipLaunchKernelGGL((mla_decode_kernel<NR, TEAMS, true, NR * TEAMS == 16 ? 3 : 2>), grid, block, 0, stream, p);
   else
-    hipLaunchKernelGGL((mla_decode_kernel<NR, false, 2>), grid, dim3(kThreads), 0, stream, p);
+    hipLaunchKernelGGL((mla_decode_kernel<NR, TEAMS, false, 2>), grid, block, 0, stream, p);
 }
 
 void launch_tiles(const MlaDecode& p, bool fp8, hipStream_t stream) {
   if (p.block_rows == 16)
-    launch_rows<16>(p, fp8, stream);
+    launch_rows<16, 1>(p, fp8, stream);
   else if (p.block_rows == 32)
-    launch_rows<32>(p, fp8, stream);
+    launch_rows<32, 1>(p, fp8, stream);
   else
-    launch_rows<64>(p, fp8, stream);
+    launch_rows<32, 2>(p, fp8, stream);
 }
 
 }  // namespace
 
-// Rows per workgroup and how many groups share the tiles (max_tiles: the most
-// tiles there can be, from the sizes the host knows).
-void mla_decode_plan(int64_t rows, int64_t max_tiles, int* block_rows, int64_t* row_blocks, int* groups) {
-  *block_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-  *row_blocks = rows > 0 ? (rows + *block_rows - 1) / *block_rows : 1;
-  int64_t g = (compute_units() + *row_blocks - 1) / *row_blocks;
+int mla_decode_block_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+// Groups that share the tiles (max_tiles: the most there can be, from the
+// sizes the host knows), so that groups times row blocks fill the device once.
+int mla_decode_groups(int64_t row_blocks, int64_t max_tiles) {
+  int64_t g = (compute_units() + row_blocks - 1) / row_blocks;
   if (g > max_tiles) g = max_tiles;
-  *groups = (int)(g < 1 ? 1 : g);
+  return (int)(g < 1 ? 1 : g);
 }
 
 hipError_t launch_mla_decode(const MlaDecode& own, const MlaDecode* prefix, bool fp8, hipStream_t stream) {
   if (prefix) launch_tiles(*prefix, fp8, stream);
   if (own.max_len > 0) launch_tiles(own, fp8, stream);
-  const int64_t rows = (int64_t)own.B * own.rows;
-  hipLaunchKernelGGL(mla_join_kernel, dim3((unsigned)((rows + 3) / 4)), dim3(kThreads), 0, stream, own,
+  hipLaunchKernelGGL(mla_join_kernel, dim3((unsigned)((own.all_rows + 3) / 4)), dim3(kJoinThreads), 0, stream, own,
                      prefix ? *prefix : own);
   return hipGetLastError();
 }
