@@ -17,24 +17,30 @@
 // rows in one group; the row blocks of a group sit on one XCD, next to each
 // other in time, so the L2 serves the tiles to all but the first.
 //
-// Tile loop (4 waves): wave w forms the scores of its 16 tokens for all NR
-// rows, the waves meet over the row maxima and exchange probabilities through
-// LDS, then wave w adds the 64 tokens' values into its 128 output columns. So
-// a tile is read from LDS once as keys and once as values whatever NR is (a
-// split of the rows over the waves would read it four times).
+// RT teams (1 or 2) of four waves, 32 rows each, share the tiles in LDS. A
+// wave forms the partial scores of 32 tokens over half of the key's columns
+// (so it holds 32 x 288 query numbers only), trades one half of them for its
+// partner's (the same tokens, the other columns), and has the scores of 16
+// tokens and 32 rows. It turns them into weights, writes them to LDS in the
+// order in which the value product's operand wants them, and adds the 64
+// tokens' values into its 32 x 128 part of the output. No product is formed
+// twice, and 72 + 64 + 16 registers of queries, output and scores leave room
+// for operands to be fetched ahead, with two waves per SIMD for RT = 2. The
+// row maxima need no exchange of their own: the weights are taken against a
+// reference that the team shares and that is only raised (a second exchange,
+// for all) when some wave finds a score 2^8 above it.
 //
 // FP8 cache: codes become BF16 exactly; a group's scale multiplies the partial
 // score of its 128 columns (FP32) and the probability that meets its 128
-// output columns (wave w's columns are group w), so the latent vector itself
-// is never rounded.
+// output columns, so the latent vector itself is never rounded.
 //
 // Roundings below 32 bits: probabilities (times the scale, FP8) to BF16 for
 // the matrix unit (relative 2^-8 at most each, on the terms of a mean), and the output.
 
 #include <atomic>
 
-#include "attn_common.h"
 #include "attn_internal.h"
+#include "mla_tiles.h"
 
 namespace fp8bs {
 
@@ -43,34 +49,20 @@ namespace {
 constexpr int kTile = 64;            // tokens per tile
 constexpr int kLatent = 512, kRope = 64, kKey = kLatent + kRope;
 constexpr int kWaitVmcnt0 = 0x0F70;   // s_waitcnt vmcnt(0), the other counters left alone
-constexpr int kJoinThreads = 256;
+constexpr int kThreads = 256;
 // The weights' reference only follows the running maximum once that is more
 // than 2^8 above it: weights up to 2^8 cost no precision in FP32 or BF16, and
 // the accumulators are rescaled a few times per request instead of per tile.
 constexpr float kSlack = 8.f;
 
-template <bool FP8, int NW>
+template <bool FP8>
 struct Tile {
   static constexpr int kRowBytes = FP8 ? kLatent : 2 * kLatent;
   static constexpr int kLatentBytes = kTile * kRowBytes;
   static constexpr int kRopeBytes = kTile * 2 * kRope;
-  static constexpr int kScaleBytes = FP8 ? kTile * 16 : 0;
+  static constexpr int kScaleBytes = FP8 ? kTile * 16 : 0;        // [group][token]
   static constexpr int kBytes = kLatentBytes + kRopeBytes + kScaleBytes;
-  static constexpr int kRows = kTile / NW;                  // that one wave loads
-  static constexpr int kLoads = FP8 ? kRows / 2 + kRows / 8 + 1 : kRows + kRows / 8;
 };
-
-// 16-byte chunk swizzles of LDS row r (the loads permute the source chunks, so
-// LDS itself is written linearly). The LDS serves a 16-byte read in groups of
-// 16 lanes, {0-3, 12-15, 20-27}, {4-11, 16-19, 28-31} and the same from 32, and
-// an 8-byte read in halves of the wave. A key read (lane: row lane%16, chunk
-// 4*ks + lane/16) thus meets rows 0-3, 12-15 at one chunk and 4-11 at its
-// neighbour; a value read rows 0-7 (8-15) at a pair of chunks, or, for bytes,
-// rows 0-7 and 16-23 (8-15, 24-31) at one chunk. All of these touch every bank
-// once. Rows of 128 bytes (rotary part): key reads do.
-__device__ __forceinline__ int swz_bf16(int r) { return (((r & 7) ^ ((r >> 1) & 4)) << 1) | ((r >> 3) & 1); }
-__device__ __forceinline__ int swz_fp8(int r) { return swz_bf16(r) ^ ((r >> 4) & 1); }
-__device__ __forceinline__ int swz_rope(int r) { return (r >> 1) & 7; }
 
 // The tiles of a request, and the request a tile belongs to.
 struct Cursor {
@@ -146,85 +138,85 @@ __device__ __forceinline__ int page_of(const MlaDecode& p, int tok) {
   return (int)(((uint64_t)(uint32_t)tok * p.page_magic) >> p.page_shift);
 }
 
-// Token of row 16*rg + lane%16 of a tile. Tokens past the end repeat the last
-// one: always cached, and masked by its position.
-__device__ __forceinline__ int row_token(const Cursor& c, int rg, int lane) {
-  return min(c.tile * kTile + 16 * rg + (lane & 15), c.len - 1);
+// Token of the tile's row `lane`. Tokens past the end repeat the last one:
+// always cached, and masked by its position.
+__device__ __forceinline__ int row_token(const Cursor& c, int lane) { return min(c.tile * kTile + lane, c.len - 1); }
+
+__device__ __forceinline__ const char* lane_ptr(const char* base, int64_t off, int from) {
+  const uint64_t a = (uint64_t)(base + off);
+  return (const char*)(((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(a >> 32), from) << 32) |
+                       (uint32_t)__builtin_amdgcn_readlane((int)a, from));
 }
 
-__device__ __forceinline__ void load_entries(const MlaDecode& p, const Cursor& c, int rg, int lane, uint32_t lds) {
-  const int tok = row_token(c, rg, lane);
-  dma4(p.table + (int64_t)c.b * p.table_stride + page_of(p, tok), lds);
-}
-
-// The wave's kRows rows of a tile, whose block-table entries (of the 16-row
-// group they are in) lane%16 holds.
-template <bool FP8, int NW>
-__device__ __forceinline__ void load_tile(const MlaDecode& p, const Cursor& c, int w, int lane, int entry,
+// The wave's ROWS rows of a tile, from row r0; lane l holds row l's block-table
+// entry. The 16-byte chunks are permuted by swz256 (swz128) of the row in
+// groups of 16 (8), see mla_tiles.h; LDS itself is written linearly.
+template <bool FP8, int ROWS>
+__device__ __forceinline__ void load_tile(const MlaDecode& p, const Cursor& c, int r0, int lane, int entry,
                                           uint32_t lds) {
-  using T = Tile<FP8, NW>;
-  const int rg = w * T::kRows / 16, r0 = w * T::kRows % 16;
-  const int tok = row_token(c, rg, lane);
+  using T = Tile<FP8>;
+  const int tok = row_token(c, lane);
   const int pg = min(max(entry, 0), p.pages - 1);
   const int64_t flat = (int64_t)pg * p.page + (tok - page_of(p, tok) * p.page);
-  const int lo = (int)(uint32_t)flat, hi = (int)(flat >> 32);
   if constexpr (!FP8) {
     // rows of 1024 latent bytes, one per load: the row is wave-uniform
-    const int chunk = opaque((lane ^ swz_bf16(r0)) << 4);
+    const int64_t off = flat * (2 * kKey);
+    const int chunk = opaque((lane << 4) ^ (swz256(r0) << 4));
 #pragma unroll
-    for (int i = 0; i < T::kRows; ++i) {
-      const int64_t f = ((int64_t)__builtin_amdgcn_readlane(hi, r0 + i) << 32) |
-                        (uint32_t)__builtin_amdgcn_readlane(lo, r0 + i);
-      dma16_s(p.cache + f * (2 * kKey), (uint32_t)(chunk ^ (swz_bf16(i) << 4)),
-              lds + (16 * rg + r0 + i) * T::kRowBytes);
-    }
+    for (int i = 0; i < ROWS; ++i)
+      dma16_s(lane_ptr(p.cache, off, r0 + i), (uint32_t)(chunk ^ (swz256(i) << 4)), lds + (r0 + i) * T::kRowBytes);
   } else {
     // two rows of 512 code bytes per load
+    const int64_t off = flat * kLatent;
+    const int chunk = opaque(((lane & 31) << 4) ^ (swz256(r0) << 4));
 #pragma unroll
-    for (int i = 0; i < T::kRows; i += 2) {
-      const int64_t f0 = ((int64_t)__builtin_amdgcn_readlane(hi, r0 + i) << 32) |
-                         (uint32_t)__builtin_amdgcn_readlane(lo, r0 + i);
-      const int64_t f1 = ((int64_t)__builtin_amdgcn_readlane(hi, r0 + i + 1) << 32) |
-                         (uint32_t)__builtin_amdgcn_readlane(lo, r0 + i + 1);
-      const int r = 16 * rg + r0 + i + (lane >> 5);
-      dma16(p.cache + (lane < 32 ? f0 : f1) * kLatent + (((lane & 31) ^ swz_fp8(r)) << 4),
-            lds + (16 * rg + r0 + i) * T::kRowBytes);
+    for (int i = 0; i < ROWS; i += 2) {
+      const char* a = lane_ptr(p.cache, off, r0 + i);
+      const char* b = lane_ptr(p.cache, off, r0 + i + 1);
+      dma16((lane < 32 ? a : b) + (chunk ^ ((lane < 32 ? swz256(i) : swz256(i + 1)) << 4)),
+            lds + (r0 + i) * T::kRowBytes);
     }
   }
   // rotary part: 8 rows of 128 bytes per load
 #pragma unroll
-  for (int i = 0; i < T::kRows; i += 8) {
-    const int src = r0 + i + (lane >> 3);
-    const int64_t f = ((int64_t)__shfl(hi, src, 64) << 32) | (uint32_t)__shfl(lo, src, 64);
-    const int chunk = (lane & 7) ^ swz_rope(16 * rg + src);
-    const char* row = FP8 ? p.rope + f * (2 * kRope) : p.cache + f * (2 * kKey) + 2 * kLatent;
-    dma16(row + (chunk << 4), lds + T::kLatentBytes + (16 * rg + r0 + i) * (2 * kRope));
+  for (int i = 0; i < ROWS; i += 8) {
+    const int row = r0 + i + (lane >> 3);
+    const int64_t f = ((int64_t)__shfl((int)(flat >> 32), row, 64) << 32) | (uint32_t)__shfl((int)flat, row, 64);
+    const int chunk = (lane & 7) ^ swz128(row);
+    const char* src = FP8 ? p.rope + f * (2 * kRope) : p.cache + f * (2 * kKey) + 2 * kLatent;
+    dma16(src + (chunk << 4), lds + T::kLatentBytes + (r0 + i) * (2 * kRope));
   }
+  // the 64 tokens' scales of one group (with 8 waves two of them load the same)
   if constexpr (FP8) {
-    // the scales of the 16-row group (with 8 waves two of them load the same)
-    const int src = lane >> 2;
-    const int64_t f = ((int64_t)__shfl(hi, src, 64) << 32) | (uint32_t)__shfl(lo, src, 64);
-    dma4(p.scales + f * 16 + (lane & 3) * 4, lds + T::kLatentBytes + T::kRopeBytes + 16 * rg * 16);
+    const int q = r0 >> 4;
+    dma4(p.scales + flat * 16 + 4 * q, lds + T::kLatentBytes + T::kRopeBytes + q * 4 * kTile);
   }
 }
 
-// TEAMS teams of 4 waves, each with its own NR rows, share the tiles in LDS.
-template <int NR, int TEAMS, bool FP8, int NBUF>
-__global__ __launch_bounds__(256 * TEAMS) void mla_decode_kernel(const MlaDecode p) {
-  constexpr int NW = 4 * TEAMS;
-  using T = Tile<FP8, NW>;
-  constexpr int NB = NR / 16;                       // 16-row blocks of a team
-  constexpr int kProbBytes = kTile * NR * (FP8 ? 4 : 2);
-  __shared__ __align__(1024) char tiles[NBUF * T::kBytes];
-  __shared__ __align__(16) char team_probs[TEAMS * kProbBytes];
-  __shared__ __align__(16) float team_stat[TEAMS * 4 * NR];
-  __shared__ __align__(16) int entries[NW][64];
+template <int RT, bool FP8, int NBUF>
+__global__ __launch_bounds__(256 * RT) __attribute__((amdgpu_waves_per_eu(2))) void mla_decode_kernel(
+    const MlaDecode p) {
+  static_assert(RT == 1 || RT == 2, "row teams");
+  using T = Tile<FP8>;
+  constexpr int NW = 4 * RT, kRows = kTile / NW;        // waves; rows of a tile that each loads
+  constexpr int kLoads = (FP8 ? kRows / 2 + 1 : kRows) + kRows / 8;
+  // A wave's slot: the partial scores that its partner sends, then its weights
+  // (BF16, or FP32 to meet the scales first); behind them its row maxima and
+  // its wish to raise the reference. With NBUF = 2 the entries of the next
+  // tile wait in a register instead of in LDS.
+  constexpr int kProbBytes = 64 * 8 * (FP8 ? 4 : 2), kSlot = FP8 ? 2048 + 256 : 2048;
+  static_assert(NBUF == 2 || NBUF == 3, "tiles in flight");
+  __shared__ __align__(1024) char lds_mem[NBUF * T::kBytes + NW * kSlot + (NBUF > 2 ? NW * 256 : 0)];
+  char* const tiles = lds_mem;
+  char* const slots = lds_mem + NBUF * T::kBytes;
 
-  const int lane = threadIdx.x & 63, n16 = lane & 15, g4 = lane >> 4;
+  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int w = wave & 3, team = wave >> 2, rg = wave * T::kRows / 16;
-  char* const probs = team_probs + team * kProbBytes;
-  float* const stat = team_stat + team * 4 * NR;
+  const int rt = wave >> 2, quarter = wave & 3;     // team; 16 tokens (weights) and 128 columns (output) of the wave
+  const int th = quarter >> 1, kh = quarter & 1;    // 32 tokens and half of the key's columns (scores)
+  char* const slot = slots + wave * kSlot;
+  float* const my_stat = reinterpret_cast<float*>(slot + kProbBytes);
+  const char* const team = slots + rt * 4 * kSlot;
 
   // workgroup -> (group, row block): workgroups are dealt over the XCDs one by
   // one; renumbered so that an XCD's are consecutive, row blocks of a group first
@@ -232,281 +224,283 @@ __global__ __launch_bounds__(256 * TEAMS) void mla_decode_kernel(const MlaDecode
   const int xcd = blockIdx.x % kAttnXcds;
   const int wg = xcd * per + min(xcd, rest) + blockIdx.x / kAttnXcds;
   const int g = wg / p.row_blocks;
-  const int row0 = ((wg - g * p.row_blocks) * TEAMS + team) * NR;      // the team's first row
   const int total = total_tiles(p);
   const int t0 = range_start(g, total, p.groups), t1 = range_start(g + 1, total, p.groups);
   if (t0 >= t1) return;
 
-  const uint32_t lds_tiles = lds_offset(tiles), lds_entries = lds_offset(entries[wave]);
+  const uint32_t lds_tiles = lds_offset(tiles);
+  const int* const entries = reinterpret_cast<const int*>(slots + NW * kSlot + wave * 256);
+  const uint32_t lds_entries = lds_offset(entries);
+  int entry = 0;         // of row `lane` of the tile that is loaded next (NBUF == 2)
   Cursor cur = locate(p, t0, t1 - t0);
   Cursor nxt = cur;      // the tile that is loaded next
   Cursor ent = cur;      // the tile whose block-table entries are fetched next
-#pragma unroll
-  for (int i = 0; i < NBUF - 1; ++i) {
-    if (nxt.left > 0) {
-      load_entries(p, ent, rg, lane, lds_entries);
-      advance(p, ent);
-      attn_wait<0>();
-      load_tile<FP8, NW>(p, nxt, wave, lane, entries[wave][lane & 15], lds_tiles + i * T::kBytes);
-      advance(p, nxt);
+  auto fetch_entries = [&] {
+    const int* src = p.table + (int64_t)ent.b * p.table_stride + page_of(p, row_token(ent, lane));
+    if constexpr (NBUF == 2)
+      entry = *src;
+    else
+      dma4(src, lds_entries);
+    advance(p, ent);
+  };
+  auto load_next = [&](int to) {
+    if constexpr (NBUF > 2) {
+      entry = entries[lane];
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
-  }
-  if (ent.left > 0) {
-    load_entries(p, ent, rg, lane, lds_entries);
-    advance(p, ent);
+    const int e = opaque(entry);      // waited for here, before the next fetch is under way
+    const Cursor c = nxt;
+    advance(p, nxt);
+    if (ent.left > 0) fetch_entries();
+    load_tile<FP8, kRows>(p, c, wave * kRows, lane, e, lds_tiles + to * T::kBytes);
+  };
+  fetch_entries();
+#pragma unroll
+  for (int i = 0; i < NBUF - 1; ++i) {
+    attn_wait<0>();
+    if (nxt.left > 0) load_next(i);
   }
 
   // LDS offsets of this lane: the swizzles only touch bits that the row and
   // tile offsets leave free, so the chunk is picked by an XOR
-  const int krow = 16 * w + n16;                                   // key reads: the wave's token n16
-  const int key0 = krow * T::kRowBytes + ((g4 ^ (FP8 ? swz_fp8(krow) : swz_bf16(krow))) << 4);
-  const int rope0 = T::kLatentBytes + krow * (2 * kRope) + ((g4 ^ swz_rope(krow)) << 4);
-  const int vrow = FP8 ? ((n16 >> 1) & 3) + 4 * g4 + 16 * (n16 >> 3) : 4 * g4 + (n16 >> 2);
-  const int val0 = vrow * T::kRowBytes + 8 * (n16 & 1) +
-                   (FP8 ? 256 * (w >> 1) + ((8 * (w & 1) ^ swz_fp8(vrow)) << 4)
-                        : 256 * w + ((((n16 >> 1) & 1) ^ swz_bf16(vrow)) << 4));
+  const TileLane L(lane);
+  const int key0 = (32 * th + L.row) * T::kRowBytes + kh * (T::kRowBytes / 2) + ((L.half ^ L.x256) << 4);
+  const int rope0 = T::kLatentBytes + (32 * th + L.row) * (2 * kRope) + ((L.half ^ L.x128 ^ (4 * kh)) << 4);
+  int val0;
+  if constexpr (FP8) {
+    const int i = (lane & 15) >> 1, row = 4 * L.half + (i & 3) + 8 * (i >> 2);
+    val0 = row * T::kRowBytes + 256 * (quarter >> 1) + 8 * (lane & 1) +
+           (((8 * (quarter & 1) + ((lane >> 4) & 1)) ^ swz256(row)) << 4);
+  } else {
+    val0 = L.trow * T::kRowBytes + 256 * quarter + L.tbyte + ((L.tchunk ^ L.tx256) << 4);
+  }
+  const int scale0 = T::kLatentBytes + T::kRopeBytes + 16 * L.half;      // [group][token]
 
-  bf16x8 qf[NB][kKey / 32];
-  f32x4 acc[8][NB];
-  float m[NB], l[NB];
-  int limit[NB];
+  const int row = ((wg - g * p.row_blocks) * RT + rt) * 32 + L.row;      // this lane's row
+  const int late = p.tokens - 1 - min(row, p.rows - 1) / p.heads;        // newest tokens hidden from it
+
+  bf16x8 qf[18];
+  f32x16 acc[4];
+  float m, l;
   bool first = true;
   int buf = 0;
 
   while (cur.left > 0) {      // a request's part of the range
     const bool whole = cur.tile == 0 && cur.left >= cur.tiles;
+    const uint16_t* qr = p.q + min((int64_t)cur.b * p.rows + min(row, p.rows - 1), p.all_rows - 1) * kKey;
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const int row = min(row0 + nb * 16 + n16, p.rows - 1);
-      const uint16_t* qr = p.q + min((int64_t)cur.b * p.rows + row, p.all_rows - 1) * kKey;
-#pragma unroll
-      for (int ks = 0; ks < kKey / 32; ++ks) {
-        // FP8: a lane reads 16 codes at a time, the slots of two k steps
-        const int col = FP8 && ks < 16 ? 64 * (ks >> 1) + 16 * g4 + 8 * (ks & 1) : 32 * ks + 8 * g4;
-        qf[nb][ks] = *reinterpret_cast<const bf16x8*>(qr + col);
-      }
-      limit[nb] = cur.len - (p.tokens - 1 - row / p.heads);
-      m[nb] = neg_inf();
-      l[nb] = 0.f;
-#pragma unroll
-      for (int d = 0; d < 8; ++d) acc[d][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int ks = 0; ks < 16; ++ks) {
+      // FP8: a lane reads 16 codes at a time, the slots of two k steps
+      const int col = FP8 ? 32 * (ks >> 1) + 16 * L.half + 8 * (ks & 1) : 16 * ks + 8 * L.half;
+      qf[ks] = *reinterpret_cast<const bf16x8*>(qr + 256 * kh + col);
     }
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+      qf[16 + ks] = *reinterpret_cast<const bf16x8*>(qr + kLatent + 32 * kh + 16 * ks + 8 * L.half);
+    m = neg_inf();
+    l = 0.f;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) acc[d] = zero16();
     // said to the compiler, which would otherwise wait for the queries inside
     // the tile loop and with them for the tiles in flight
     __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
 
     for (bool last = false; !last;) {
-    if (nxt.left > 0 && NBUF > 2 && cur.left > 1)
-      attn_wait<(NBUF - 2) * (T::kLoads + 1)>();
-    else
-      attn_wait<0>();
-    attn_barrier();
-    if (nxt.left > 0) {
-      const int entry = entries[wave][lane & 15];
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      if (ent.left > 0) {
-        load_entries(p, ent, rg, lane, lds_entries);
-        advance(p, ent);
-      }
-      const int nbuf = buf == 0 ? NBUF - 1 : buf - 1;
-      load_tile<FP8, NW>(p, nxt, wave, lane, entry, lds_tiles + nbuf * T::kBytes);
-      advance(p, nxt);
-    }
-    const char* tl = tiles + buf * T::kBytes;
+      if (nxt.left > 0 && NBUF > 2)
+        attn_wait<kLoads>();
+      else
+        attn_wait<0>();
+      attn_barrier();
+      if (nxt.left > 0) load_next(buf == 0 ? NBUF - 1 : buf - 1);
+      const char* tl = tiles + buf * T::kBytes;
 
-    // scores of this wave's 16 tokens: D[token 4*g4 + i][row n16]
-    f32x4 s[NB];
+      // partial scores: D[token drow(i)][row lane%32] of 32 tokens
+      f32x16 x = zero16(), y = zero16();
+      {
+        const int key = opaque(key0);
+        if constexpr (!FP8) {
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) s[nb] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if constexpr (!FP8) {
-      const int key = opaque(key0);
-#pragma unroll
-      for (int ks = 0; ks < 16; ++ks) {
-        const bf16x8 a = lds_bf16x8(tl + (key ^ ((ks & 3) << 6)) + (ks >> 2) * 256);
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) s[nb] = mfma16(a, qf[nb][ks], s[nb]);
-      }
-    } else {
-      const int key = opaque(key0);
-      const char* sp = tl + T::kLatentBytes + T::kRopeBytes + (16 * w + 4 * g4) * 16;
-      float sc[4][4];     // [token i][group]
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f32x4 v = *reinterpret_cast<const f32x4*>(sp + 16 * i);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) sc[i][q] = v[q];
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        f32x4 part[NB];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) part[nb] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int kp2 = 2 * q + h;      // 64 columns
-          const uint4 c = *reinterpret_cast<const uint4*>(tl + (key ^ ((kp2 & 3) << 6)) + (kp2 >> 2) * 256);
-          const bf16x8 a0 = e4m3_to_bf16(c.x, c.y), a1 = e4m3_to_bf16(c.z, c.w);
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) part[nb] = mfma16(a0, qf[nb][2 * kp2], part[nb]);
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) part[nb] = mfma16(a1, qf[nb][2 * kp2 + 1], part[nb]);
-        }
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[nb][i] = fmaf(sc[i][q], part[nb][i], s[nb][i]);
-      }
-    }
-    {
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        const bf16x8 a = lds_bf16x8(tl + (rope0 ^ (ks << 6)));
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) s[nb] = mfma16(a, qf[nb][16 + ks], s[nb]);
-      }
-    }
-
-    // row maxima over the tile
-    const int tok0 = cur.tile * kTile + 16 * w + 4 * g4;
-    const bool edge = (cur.tile + 1) * kTile > cur.len - (p.tokens - 1);
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s[nb][i] *= p.scale_log2;
-        if (edge && tok0 + i >= limit[nb]) s[nb][i] = neg_inf();
-      }
-      float v = fmaxf(fmaxf(s[nb][0], s[nb][1]), fmaxf(s[nb][2], s[nb][3]));
-      v = fmaxf(v, __shfl_xor(v, 16, 64));
-      v = fmaxf(v, __shfl_xor(v, 32, 64));
-      if (g4 == 0) stat[w * NR + nb * 16 + n16] = v;
-    }
-    attn_barrier();
-
-    // probabilities against the new maxima, into LDS as the value product's operand
-    float ref[NB];
-    bool grown = false;
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const int n = nb * 16 + n16;
-      ref[nb] = fmaxf(fmaxf(stat[n], stat[NR + n]), fmaxf(stat[2 * NR + n], stat[3 * NR + n]));
-      grown |= ref[nb] > m[nb] + kSlack;
-    }
-    if (__any(grown)) {
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        const float mn = fmaxf(m[nb], ref[nb]);
-        const float alpha = mn == neg_inf() ? 1.f : exp2_fast(m[nb] - mn);
-        m[nb] = mn;
-        l[nb] *= alpha;
-#pragma unroll
-        for (int d = 0; d < 8; ++d) acc[d][nb] *= alpha;
-      }
-    }
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      ref[nb] = m[nb] == neg_inf() ? 0.f : m[nb];      // nothing visible yet: every weight is 0
-      f32x4 e;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) e[i] = exp2_fast(s[nb][i] - ref[nb]);
-      l[nb] += (e[0] + e[1]) + (e[2] + e[3]);
-      // [32-token step w/2][row block][lane], half w%2 of the lane's 8 slots
-      const int at = (((w >> 1) * NB + nb) * 64 + lane) * 2 + (w & 1);
-      if constexpr (FP8) {
-        *reinterpret_cast<f32x4*>(probs + 16 * at) = e;
-      } else {
-        bf16x4 b;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) b[i] = (__bf16)e[i];
-        *reinterpret_cast<bf16x4*>(probs + 8 * at) = b;
-      }
-    }
-    attn_barrier();
-
-    // output columns 128w .. +127: D[column 4*g4 + i][row n16]
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      const int val = opaque(val0);
-      bf16x8 pb[NB];
-      if constexpr (FP8) {
-        const float* sp = reinterpret_cast<const float*>(tl + T::kLatentBytes + T::kRopeBytes) + w;
-        float sc[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sc[j] = sp[4 * (32 * kk + 16 * (j >> 2) + 4 * g4 + (j & 3))];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          const f32x4* e = reinterpret_cast<const f32x4*>(probs + ((kk * NB + nb) * 64 + lane) * 32);
-          const f32x4 e0 = e[0], e1 = e[1];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            pb[nb][j] = (__bf16)(e0[j] * sc[j]);
-            pb[nb][4 + j] = (__bf16)(e1[j] * sc[4 + j]);
+          for (int ks = 0; ks < 16; ks += 2) {      // two chains: an MFMA need not wait for the one before
+            x = mfma32(lds_bf16x8(tl + (key ^ ((ks & 7) << 5)) + (ks >> 3) * 256), qf[ks], x);
+            y = mfma32(lds_bf16x8(tl + (key ^ (((ks + 1) & 7) << 5)) + (ks >> 3) * 256), qf[ks + 1], y);
           }
-        }
-      } else {
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) pb[nb] = lds_bf16x8(probs + ((kk * NB + nb) * 64 + lane) * 16);
-      }
-#pragma unroll
-      for (int d = 0; d < 8; ++d) {
-        bf16x8 a;
-        if constexpr (FP8) {
-          const i32x2 c = lds_tr8(tl + (val ^ (d << 4)) + 32 * kk * T::kRowBytes);
-          a = e4m3_to_bf16((uint32_t)c[0], (uint32_t)c[1]);
+          x = mfma32(lds_bf16x8(tl + rope0), qf[16], x);
+          y = mfma32(lds_bf16x8(tl + (rope0 ^ 32)), qf[17], y);
+          x += y;
         } else {
-          const char* vp = tl + (val ^ (d << 5)) + 32 * kk * T::kRowBytes;
-          a = join(lds_tr16(vp), lds_tr16(vp + 16 * T::kRowBytes));
+          f32x16 z[2];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {             // 128 columns with one scale a token
+            z[q] = zero16();
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {           // 32 columns
+              const uint4 c = *reinterpret_cast<const uint4*>(tl + (key ^ ((4 * q + h) << 5)));
+              z[q] = mfma32(e4m3_to_bf16(c.x, c.y), qf[8 * q + 2 * h], z[q]);
+              z[q] = mfma32(e4m3_to_bf16(c.z, c.w), qf[8 * q + 2 * h + 1], z[q]);
+            }
+          }
+          x = mfma32(lds_bf16x8(tl + rope0), qf[16], x);
+          x = mfma32(lds_bf16x8(tl + (rope0 ^ 32)), qf[17], x);
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i4 = 0; i4 < 4; ++i4) {
+              const f32x4 sc =
+                  *reinterpret_cast<const f32x4*>(tl + scale0 + 4 * kTile * (2 * kh + q) + 4 * (32 * th + 8 * i4));
+#pragma unroll
+              for (int j = 0; j < 4; ++j) x[4 * i4 + j] = fmaf(sc[j], z[q][4 * i4 + j], x[4 * i4 + j]);
+            }
         }
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) acc[d][nb] = mfma16(a, pb[nb], acc[d][nb]);
       }
-    }
-
-    last = cur.tile + 1 == cur.tiles || cur.left == 1;
-    if (last) {
-      // sums over the lanes' and waves' tokens
+      // the partner's half of them to its slot, this wave's kept
+      f32x4 s[2];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        float v = l[nb];
-        v += __shfl_xor(v, 16, 64);
-        v += __shfl_xor(v, 32, 64);
-        if (g4 == 0) stat[w * NR + nb * 16 + n16] = v;
+      for (int i = 0; i < 2; ++i) {
+        f32x4 give;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float lo = x[4 * i + j], hi = x[8 + 4 * i + j];
+          give[j] = kh ? lo : hi;
+          s[i][j] = kh ? hi : lo;
+        }
+        *reinterpret_cast<f32x4*>(slots + (wave ^ 1) * kSlot + 1024 * i + 16 * lane) = give;
       }
       attn_barrier();
-      const bool final = whole && !p.join;
-      const int64_t part = whole ? 2 * p.groups + cur.b : 2 * g + (first ? 0 : 1);
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        const int n = nb * 16 + n16, row = row0 + n;
-        const float sum = (stat[n] + stat[NR + n]) + (stat[2 * NR + n] + stat[3 * NR + n]);
-        if (row < p.rows && (int64_t)cur.b * p.rows + row < p.all_rows) {
-          if (final) {
-            const int64_t o = (int64_t)cur.b * p.rows + row;
-            const float inv = sum > 0.f ? 1.f / sum : 0.f;
-            uint16_t* op = p.out + o * kLatent + 128 * w + 4 * g4;
+      for (int i = 0; i < 2; ++i) s[i] += *reinterpret_cast<const f32x4*>(slot + 1024 * i + 16 * lane);
+
+      // weights of 16 tokens against the team's reference
+      const int tok0 = cur.tile * kTile + 16 * quarter + 4 * L.half, seen = cur.len - late;
+      if ((cur.tile + 1) * kTile > cur.len - (p.tokens - 1)) {
 #pragma unroll
-            for (int d = 0; d < 8; ++d) {
-              bf16x4 b;
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) b[i] = (__bf16)(acc[d][nb][i] * inv);
-              *reinterpret_cast<bf16x4*>(op + 16 * d) = b;
-            }
-            if (w == 0 && g4 == 0) p.lse[o] = sum > 0.f ? (m[nb] + __builtin_log2f(sum)) * kLn2 : neg_inf();
+          for (int j = 0; j < 4; ++j)
+            if (tok0 + 8 * i + j >= seen) s[i][j] = neg_inf();
+      }
+      float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
+                        fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
+      top = half_max(top) * p.scale_log2;
+      float sum;
+      auto weigh = [&] {
+        const float ref = m == neg_inf() ? 0.f : m;      // nothing visible yet: every weight is 0
+        f32x4 e[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) e[i][j] = exp2_fast(fmaf(s[i][j], p.scale_log2, -ref));
+        sum = ((e[0][0] + e[0][1]) + (e[0][2] + e[0][3])) + ((e[1][0] + e[1][1]) + (e[1][2] + e[1][3]));
+        if constexpr (FP8) {
+          *reinterpret_cast<f32x4*>(slot + 16 * lane) = e[0];
+          *reinterpret_cast<f32x4*>(slot + 1024 + 16 * lane) = e[1];
+        } else {
+          bf16x8 b;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            b[j] = (__bf16)e[0][j];
+            b[4 + j] = (__bf16)e[1][j];
+          }
+          *reinterpret_cast<bf16x8*>(slot + 16 * lane) = b;
+        }
+      };
+      weigh();
+      if (L.half == 0) my_stat[L.row] = top;
+      const bool grown = __any(top > m + kSlack);
+      if (lane == 0) my_stat[32] = grown ? 1.f : 0.f;
+      attn_barrier();
+      // every wave's wish: the answer is the same for all
+      if (__any(*reinterpret_cast<const float*>(slots + (lane % NW) * kSlot + kProbBytes + 128) != 0.f)) {
+        float mn = m;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mn = fmaxf(mn, reinterpret_cast<const float*>(team + k * kSlot + kProbBytes)[L.row]);
+        const float alpha = mn == neg_inf() ? 1.f : exp2_fast(m - mn);
+        m = mn;
+        l *= alpha;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) acc[d] *= alpha;
+        weigh();
+        attn_barrier();
+      }
+      l += sum;
+
+      // output: D[column drow(i)][row lane%32] of each 32-column block
+      const int val = opaque(val0);
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        const char* vt = tl + 16 * a * T::kRowBytes;
+        bf16x8 pb;
+        if constexpr (!FP8) {
+          pb = lds_bf16x8(team + a * kSlot + 16 * lane);
+        } else {
+          const f32x4 e0 = *reinterpret_cast<const f32x4*>(team + a * kSlot + 16 * lane);
+          const f32x4 e1 = *reinterpret_cast<const f32x4*>(team + a * kSlot + 1024 + 16 * lane);
+          const char* sp = tl + scale0 + 4 * kTile * quarter + 4 * 16 * a;
+          const f32x4 c0 = *reinterpret_cast<const f32x4*>(sp), c1 = *reinterpret_cast<const f32x4*>(sp + 32);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            pb[j] = (__bf16)(e0[j] * c0[j]);
+            pb[4 + j] = (__bf16)(e1[j] * c1[j]);
+          }
+        }
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          if constexpr (!FP8) {
+            const int at = val ^ (d << 6);
+            acc[d] = mfma32(join(lds_tr16(vt + at), lds_tr16(vt + (at ^ 32) + 8 * T::kRowBytes)), pb, acc[d]);
           } else {
-            const int64_t o = part * p.rows + row;
-            float* op = p.part + o * kLatent + 128 * w + 4 * g4;
-#pragma unroll
-            for (int d = 0; d < 8; ++d) *reinterpret_cast<f32x4*>(op + 16 * d) = acc[d][nb];
-            if (w == 0 && g4 == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * o) = make_float2(m[nb], sum);
+            const i32x2 c = lds_tr8(vt + (val ^ (d << 5)));
+            acc[d] = mfma32(e4m3_to_bf16((uint32_t)c[0], (uint32_t)c[1]), pb, acc[d]);
           }
         }
       }
-      first = false;
+      last = cur.tile + 1 == cur.tiles || cur.left == 1;
+      if (!last) {
+        advance(p, cur);
+        buf = buf + 1 == NBUF ? 0 : buf + 1;
+      }
     }
+
+    // sums over the lanes' and the waves' tokens
+    l = half_sum(l);
+    if (L.half == 0) my_stat[L.row] = l;
+    attn_barrier();
+    l = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) l += reinterpret_cast<const float*>(team + k * kSlot + kProbBytes)[L.row];
+    if (row < p.rows && (int64_t)cur.b * p.rows + row < p.all_rows) {
+      if (whole && !p.join) {
+        const int64_t o = (int64_t)cur.b * p.rows + row;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        uint16_t* op = p.out + o * kLatent + 128 * quarter + 4 * L.half;
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            bf16x4 b;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) b[j] = (__bf16)(acc[d][4 * i + j] * inv);
+            *reinterpret_cast<bf16x4*>(op + 32 * d + 8 * i) = b;
+          }
+        if (quarter == 0 && L.half == 0) p.lse[o] = l > 0.f ? (m + __builtin_log2f(l)) * kLn2 : neg_inf();
+      } else {
+        const int64_t o = (whole ? 2 * (int64_t)p.groups + cur.b : 2 * (int64_t)g + (first ? 0 : 1)) * p.rows + row;
+        float* op = p.part + o * kLatent + 128 * quarter + 4 * L.half;
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            f32x4 v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = acc[d][4 * i + j];
+            *reinterpret_cast<f32x4*>(op + 32 * d + 8 * i) = v;
+          }
+        if (quarter == 0 && L.half == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * o) = make_float2(m, l);
+      }
+    }
+    first = false;
     advance(p, cur);
     buf = buf + 1 == NBUF ? 0 : buf + 1;
-    }
   }
 }
 
@@ -568,7 +562,7 @@ __device__ __forceinline__ bool add_pieces(const MlaDecode& p, int64_t o, int la
   return true;
 }
 
-__global__ __launch_bounds__(kJoinThreads) void mla_join_kernel(const MlaDecode p, const MlaDecode prefix) {
+__global__ __launch_bounds__(kThreads) void mla_join_kernel(const MlaDecode p, const MlaDecode prefix) {
   const int lane = threadIdx.x & 63;
   const int64_t o = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (o >= p.all_rows) return;
@@ -595,27 +589,25 @@ int compute_units() {
   return cached[dev];
 }
 
-template <int NR, int TEAMS>
+template <int RT>
 void launch_rows(const MlaDecode& p, bool fp8, hipStream_t stream) {
-  const dim3 grid((unsigned)((int64_t)p.groups * p.row_blocks)), block(256 * TEAMS);
+  const dim3 grid((unsigned)((int64_t)p.groups * p.row_blocks));
   if (fp8)
-    hipLaunchKernelGGL((mla_decode_kernel<NR, TEAMS, true, NR * TEAMS == 16 ? 3 : 2>), grid, block, 0, stream, p);
+    hipLaunchKernelGGL((mla_decode_kernel<RT, true, 3>), grid, dim3(256 * RT), 0, stream, p);
   else
-    hipLaunchKernelGGL((mla_decode_kernel<NR, TEAMS, false, 2>), grid, block, 0, stream, p);
+    hipLaunchKernelGGL((mla_decode_kernel<RT, false, 2>), grid, dim3(256 * RT), 0, stream, p);
 }
 
 void launch_tiles(const MlaDecode& p, bool fp8, hipStream_t stream) {
-  if (p.block_rows == 16)
-    launch_rows<16, 1>(p, fp8, stream);
-  else if (p.block_rows == 32)
-    launch_rows<32, 1>(p, fp8, stream);
+  if (p.block_rows == 32)
+    launch_rows<1>(p, fp8, stream);
   else
-    launch_rows<32, 2>(p, fp8, stream);
+    launch_rows<2>(p, fp8, stream);
 }
 
 }  // namespace
 
-int mla_decode_block_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+int mla_decode_block_rows(int64_t rows) { return rows <= 32 ? 32 : 64; }
 
 // Groups that share the tiles (max_tiles: the most there can be, from the
 // sizes the host knows), so that groups times row blocks fill the device once.
@@ -628,7 +620,7 @@ int mla_decode_groups(int64_t row_blocks, int64_t max_tiles) {
 hipError_t launch_mla_decode(const MlaDecode& own, const MlaDecode* prefix, bool fp8, hipStream_t stream) {
   if (prefix) launch_tiles(*prefix, fp8, stream);
   if (own.max_len > 0) launch_tiles(own, fp8, stream);
-  hipLaunchKernelGGL(mla_join_kernel, dim3((unsigned)((own.all_rows + 3) / 4)), dim3(kJoinThreads), 0, stream, own,
+  hipLaunchKernelGGL(mla_join_kernel, dim3((unsigned)((own.all_rows + 3) / 4)), dim3(kThreads), 0, stream, own,
                      prefix ? *prefix : own);
   return hipGetLastError();
 }
