@@ -148,50 +148,81 @@ __device__ __forceinline__ const char* lane_ptr(const char* base, int64_t off, i
                        (uint32_t)__builtin_amdgcn_readlane((int)a, from));
 }
 
-// The wave's ROWS rows of a tile, from row r0; lane l holds row l's block-table
-// entry. The 16-byte chunks are permuted by swz256 (swz128) of the row in
-// groups of 16 (8), see mla_tiles.h; LDS itself is written linearly.
+// The wave's ROWS rows of a tile, from row r0, load by load (kLoads of them), so
+// that they can be issued between the matrix instructions: a wave that issues
+// its loads in one go stands still until the address unit has taken them all.
+// Lane l holds row l's block-table entry. The 16-byte chunks are permuted by
+// swz256 (swz128) of the row in groups of 16 (8), see mla_tiles.h; LDS itself
+// is written linearly.
 template <bool FP8, int ROWS>
-__device__ __forceinline__ void load_tile(const MlaDecode& p, const Cursor& c, int r0, int lane, int entry,
-                                          uint32_t lds) {
+struct Loader {
   using T = Tile<FP8>;
-  const int tok = row_token(c, lane);
-  const int pg = min(max(entry, 0), p.pages - 1);
-  const int64_t flat = (int64_t)pg * p.page + (tok - page_of(p, tok) * p.page);
-  if constexpr (!FP8) {
-    // rows of 1024 latent bytes, one per load: the row is wave-uniform
-    const int64_t off = flat * (2 * kKey);
-    const int chunk = opaque((lane << 4) ^ (swz256(r0) << 4));
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i)
-      dma16_s(lane_ptr(p.cache, off, r0 + i), (uint32_t)(chunk ^ (swz256(i) << 4)), lds + (r0 + i) * T::kRowBytes);
-  } else {
-    // two rows of 512 code bytes per load
-    const int64_t off = flat * kLatent;
-    const int chunk = opaque(((lane & 31) << 4) ^ (swz256(r0) << 4));
-#pragma unroll
-    for (int i = 0; i < ROWS; i += 2) {
-      const char* a = lane_ptr(p.cache, off, r0 + i);
-      const char* b = lane_ptr(p.cache, off, r0 + i + 1);
-      dma16((lane < 32 ? a : b) + (chunk ^ ((lane < 32 ? swz256(i) : swz256(i + 1)) << 4)),
-            lds + (r0 + i) * T::kRowBytes);
+  static constexpr int kMain = FP8 ? ROWS / 2 : ROWS, kRopes = ROWS / 8, kLoads = kMain + kRopes + (FP8 ? 1 : 0);
+  const MlaDecode& p;
+  const int r0, lane;
+  const uint32_t lds;
+  const int64_t flat;
+  const int chunk;
+  __device__ __forceinline__ static int64_t flat_of(const MlaDecode& p, const Cursor& c, int lane, int entry) {
+    const int tok = row_token(c, lane);
+    return (int64_t)min(max(entry, 0), p.pages - 1) * p.page + (tok - page_of(p, tok) * p.page);
+  }
+  __device__ __forceinline__ Loader(const MlaDecode& p_, const Cursor& c, int r0_, int lane_, int entry, uint32_t lds_)
+      : p(p_), r0(r0_), lane(lane_), lds(lds_), flat(flat_of(p_, c, lane_, entry)),
+        chunk(opaque(((FP8 ? lane_ & 31 : lane_) << 4) ^ (swz256(r0_) << 4))) {}
+  __device__ __forceinline__ void issue(int n) const {
+    if (n < kMain) {
+      if constexpr (!FP8) {      // a row of 1024 latent bytes: the row is wave-uniform
+        dma16_s(lane_ptr(p.cache, flat * (2 * kKey), r0 + n), (uint32_t)(chunk ^ (swz256(n) << 4)),
+                lds + (r0 + n) * T::kRowBytes);
+      } else {                   // two rows of 512 code bytes
+        const char* a = lane_ptr(p.cache, flat * kLatent, r0 + 2 * n);
+        const char* b = lane_ptr(p.cache, flat * kLatent, r0 + 2 * n + 1);
+        dma16((lane < 32 ? a : b) + (chunk ^ ((lane < 32 ? swz256(2 * n) : swz256(2 * n + 1)) << 4)),
+              lds + (r0 + 2 * n) * T::kRowBytes);
+      }
+    } else if (n < kMain + kRopes) {      // rotary part: 8 rows of 128 bytes
+      const int i = 8 * (n - kMain), row = r0 + i + (lane >> 3);
+      const int64_t f = ((int64_t)__shfl((int)(flat >> 32), row, 64) << 32) | (uint32_t)__shfl((int)flat, row, 64);
+      const int c = (lane & 7) ^ swz128(row);
+      const char* src = FP8 ? p.rope + f * (2 * kRope) : p.cache + f * (2 * kKey) + 2 * kLatent;
+      dma16(src + (c << 4), lds + T::kLatentBytes + (r0 + i) * (2 * kRope));
+    } else if constexpr (FP8) {           // 64 tokens' scales of one group (with 8 waves two load the same)
+      const int q = r0 >> 4;
+      dma4(p.scales + flat * 16 + 4 * q, lds + T::kLatentBytes + T::kRopeBytes + q * 4 * kTile);
     }
   }
-  // rotary part: 8 rows of 128 bytes per load
-#pragma unroll
-  for (int i = 0; i < ROWS; i += 8) {
-    const int row = r0 + i + (lane >> 3);
-    const int64_t f = ((int64_t)__shfl((int)(flat >> 32), row, 64) << 32) | (uint32_t)__shfl((int)flat, row, 64);
-    const int chunk = (lane & 7) ^ swz128(row);
-    const char* src = FP8 ? p.rope + f * (2 * kRope) : p.cache + f * (2 * kKey) + 2 * kLatent;
-    dma16(src + (chunk << 4), lds + T::kLatentBytes + (r0 + i) * (2 * kRope));
+};
+
+// Operands of the value product, kAhead steps ahead: step i is the 16 tokens
+// i/4 and the wave's 32-column block i%4. at: the lane's LDS address in step 0.
+template <bool FP8>
+struct ValueFeed {
+  static constexpr int kAhead = 4;
+  const char* at;
+  bf16x8 v[FP8 ? 1 : kAhead];
+  i32x2 c[FP8 ? kAhead : 1];
+  __device__ __forceinline__ explicit ValueFeed(const char* at_) : at(at_) {}
+  __device__ __forceinline__ const char* xored(int bits) const {
+    return at + (((int)(uintptr_t)(lds_void)at ^ bits) - (int)(uintptr_t)(lds_void)at);
   }
-  // the 64 tokens' scales of one group (with 8 waves two of them load the same)
-  if constexpr (FP8) {
-    const int q = r0 >> 4;
-    dma4(p.scales + flat * 16 + 4 * q, lds + T::kLatentBytes + T::kRopeBytes + q * 4 * kTile);
+  __device__ __forceinline__ void fetch(int i) {
+    const int row = 16 * (i >> 2), d = i & 3;
+    if constexpr (FP8) {
+      c[i % kAhead] = lds_tr8(xored(d << 5) + row * Tile<FP8>::kRowBytes);
+    } else {
+      const char* a = xored(d << 6) + row * Tile<FP8>::kRowBytes;
+      const char* b = xored((d << 6) ^ 32) + (row + 8) * Tile<FP8>::kRowBytes;
+      v[i % kAhead] = join(lds_tr16(a), lds_tr16(b));
+    }
   }
-}
+  __device__ __forceinline__ bf16x8 get(int i) const {
+    if constexpr (FP8)
+      return e4m3_to_bf16((uint32_t)c[i % kAhead][0], (uint32_t)c[i % kAhead][1]);
+    else
+      return v[i % kAhead];
+  }
+};
 
 template <int RT, bool FP8, int NBUF>
 __global__ __launch_bounds__(256 * RT) __attribute__((amdgpu_waves_per_eu(2))) void mla_decode_kernel(
@@ -199,7 +230,9 @@ __global__ __launch_bounds__(256 * RT) __attribute__((amdgpu_waves_per_eu(2))) v
   static_assert(RT == 1 || RT == 2, "row teams");
   using T = Tile<FP8>;
   constexpr int NW = 4 * RT, kRows = kTile / NW;        // waves; rows of a tile that each loads
-  constexpr int kLoads = (FP8 ? kRows / 2 + 1 : kRows) + kRows / 8;
+  using Load = Loader<FP8, kRows>;
+  using Values = ValueFeed<FP8>;
+  constexpr int kLoads = Load::kLoads;
   // A wave's slot: the partial scores that its partner sends, then its weights
   // (BF16, or FP32 to meet the scales first); behind them its row maxima and
   // its wish to raise the reference. With NBUF = 2 the entries of the next
@@ -243,7 +276,7 @@ __global__ __launch_bounds__(256 * RT) __attribute__((amdgpu_waves_per_eu(2))) v
       dma4(src, lds_entries);
     advance(p, ent);
   };
-  auto load_next = [&](int to) {
+  auto start_next = [&](int to) {      // the loads of the tile `nxt`, into buffer `to`
     if constexpr (NBUF > 2) {
       entry = entries[lane];
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -252,13 +285,17 @@ __global__ __launch_bounds__(256 * RT) __attribute__((amdgpu_waves_per_eu(2))) v
     const Cursor c = nxt;
     advance(p, nxt);
     if (ent.left > 0) fetch_entries();
-    load_tile<FP8, kRows>(p, c, wave * kRows, lane, e, lds_tiles + to * T::kBytes);
+    return Load(p, c, wave * kRows, lane, e, lds_tiles + to * T::kBytes);
   };
   fetch_entries();
 #pragma unroll
   for (int i = 0; i < NBUF - 1; ++i) {
     attn_wait<0>();
-    if (nxt.left > 0) load_next(i);
+    if (nxt.left > 0) {
+      const Load ld = start_next(i);
+#pragma unroll
+      for (int n = 0; n < kLoads; ++n) ld.issue(n);
+    }
   }
 
   // LDS offsets of this lane: the swizzles only touch bits that the row and
@@ -311,36 +348,55 @@ __global__ __launch_bounds__(256 * RT) __attribute__((amdgpu_waves_per_eu(2))) v
       else
         attn_wait<0>();
       attn_barrier();
-      if (nxt.left > 0) load_next(buf == 0 ? NBUF - 1 : buf - 1);
       const char* tl = tiles + buf * T::kBytes;
 
-      // partial scores: D[token drow(i)][row lane%32] of 32 tokens
-      f32x16 x = zero16(), y = zero16();
-      {
-        const int key = opaque(key0);
+      // partial scores: D[token drow(i)][row lane%32] of 32 tokens, operands
+      // fetched kAhead steps ahead, the next tile's loads in between
+      f32x16 x;
+      const int key = opaque(key0);
+      auto partial = [&](auto&& between) {
         if constexpr (!FP8) {
+          constexpr int kAhead = 6;
+          bf16x8 kf[kAhead];
+          auto fetch = [&](int ks) {
+            return lds_bf16x8(ks < 16 ? tl + (key ^ ((ks & 7) << 5)) + (ks >> 3) * 256 : tl + (rope0 ^ ((ks & 1) << 5)));
+          };
+          f32x16 y[2] = {zero16(), zero16()};      // two chains: an MFMA need not wait for the one before
 #pragma unroll
-          for (int ks = 0; ks < 16; ks += 2) {      // two chains: an MFMA need not wait for the one before
-            x = mfma32(lds_bf16x8(tl + (key ^ ((ks & 7) << 5)) + (ks >> 3) * 256), qf[ks], x);
-            y = mfma32(lds_bf16x8(tl + (key ^ (((ks + 1) & 7) << 5)) + (ks >> 3) * 256), qf[ks + 1], y);
+          for (int ks = 0; ks < kAhead; ++ks) kf[ks] = fetch(ks);
+#pragma unroll
+          for (int ks = 0; ks < 18; ++ks) {
+            __builtin_amdgcn_sched_barrier(0);
+            y[ks & 1] = mfma32(kf[ks % kAhead], qf[ks], y[ks & 1]);
+            if (ks + kAhead < 18) kf[ks % kAhead] = fetch(ks + kAhead);
+            between(ks);
           }
-          x = mfma32(lds_bf16x8(tl + rope0), qf[16], x);
-          y = mfma32(lds_bf16x8(tl + (rope0 ^ 32)), qf[17], y);
-          x += y;
+          __builtin_amdgcn_sched_barrier(0);
+          x = y[0] + y[1];
         } else {
-          f32x16 z[2];
+          constexpr int kAhead = 3;
+          uint4 kc[kAhead];
+          auto fetch = [&](int h) { return *reinterpret_cast<const uint4*>(tl + (key ^ (h << 5))); };
+          f32x16 z[2] = {zero16(), zero16()};      // 128 columns with one scale a token each
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {             // 128 columns with one scale a token
-            z[q] = zero16();
+          for (int h = 0; h < kAhead; ++h) kc[h] = fetch(h);
+          const bf16x8 r0 = lds_bf16x8(tl + rope0), r1 = lds_bf16x8(tl + (rope0 ^ 32));
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {           // 32 columns
-              const uint4 c = *reinterpret_cast<const uint4*>(tl + (key ^ ((4 * q + h) << 5)));
-              z[q] = mfma32(e4m3_to_bf16(c.x, c.y), qf[8 * q + 2 * h], z[q]);
-              z[q] = mfma32(e4m3_to_bf16(c.z, c.w), qf[8 * q + 2 * h + 1], z[q]);
-            }
+          for (int h = 0; h < 8; ++h) {            // 32 columns
+            __builtin_amdgcn_sched_barrier(0);
+            const uint4 c = kc[h % kAhead];
+            const bf16x8 a0 = e4m3_to_bf16(c.x, c.y), a1 = e4m3_to_bf16(c.z, c.w);
+            if (h + kAhead < 8) kc[h % kAhead] = fetch(h + kAhead);
+            z[h >> 2] = mfma32(a0, qf[2 * h], z[h >> 2]);
+            between(2 * h);
+            z[h >> 2] = mfma32(a1, qf[2 * h + 1], z[h >> 2]);
+            between(2 * h + 1);
           }
-          x = mfma32(lds_bf16x8(tl + rope0), qf[16], x);
-          x = mfma32(lds_bf16x8(tl + (rope0 ^ 32)), qf[17], x);
+          x = mfma32(r0, qf[16], zero16());
+          between(16);
+          x = mfma32(r1, qf[17], x);
+          between(17);
+          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
           for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -351,6 +407,14 @@ __global__ __launch_bounds__(256 * RT) __attribute__((amdgpu_waves_per_eu(2))) v
               for (int j = 0; j < 4; ++j) x[4 * i4 + j] = fmaf(sc[j], z[q][4 * i4 + j], x[4 * i4 + j]);
             }
         }
+      };
+      if (nxt.left > 0) {
+        const Load ld = start_next(buf == 0 ? NBUF - 1 : buf - 1);
+        partial([&](int i) {
+          if (i * kLoads / 18 != (i + 1) * kLoads / 18) ld.issue(i * kLoads / 18);
+        });
+      } else {
+        partial([](int) {});
       }
       // the partner's half of them to its slot, this wave's kept
       f32x4 s[2];
@@ -404,6 +468,10 @@ __global__ __launch_bounds__(256 * RT) __attribute__((amdgpu_waves_per_eu(2))) v
         }
       };
       weigh();
+      // the first values are on their way before the waves meet
+      Values vf(tl + opaque(val0));
+#pragma unroll
+      for (int i = 0; i < Values::kAhead; ++i) vf.fetch(i);
       if (L.half == 0) my_stat[L.row] = top;
       const bool grown = __any(top > m + kSlack);
       if (lane == 0) my_stat[32] = grown ? 1.f : 0.f;
@@ -425,13 +493,11 @@ __global__ __launch_bounds__(256 * RT) __attribute__((amdgpu_waves_per_eu(2))) v
       l += sum;
 
       // output: D[column drow(i)][row lane%32] of each 32-column block
-      const int val = opaque(val0);
+      bf16x8 pb[4];
 #pragma unroll
       for (int a = 0; a < 4; ++a) {
-        const char* vt = tl + 16 * a * T::kRowBytes;
-        bf16x8 pb;
         if constexpr (!FP8) {
-          pb = lds_bf16x8(team + a * kSlot + 16 * lane);
+          pb[a] = lds_bf16x8(team + a * kSlot + 16 * lane);
         } else {
           const f32x4 e0 = *reinterpret_cast<const f32x4*>(team + a * kSlot + 16 * lane);
           const f32x4 e1 = *reinterpret_cast<const f32x4*>(team + a * kSlot + 1024 + 16 * lane);
@@ -439,21 +505,18 @@ __global__ __launch_bounds__(256 * RT) __attribute__((amdgpu_waves_per_eu(2))) v
           const f32x4 c0 = *reinterpret_cast<const f32x4*>(sp), c1 = *reinterpret_cast<const f32x4*>(sp + 32);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            pb[j] = (__bf16)(e0[j] * c0[j]);
-            pb[4 + j] = (__bf16)(e1[j] * c1[j]);
-          }
-        }
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          if constexpr (!FP8) {
-            const int at = val ^ (d << 6);
-            acc[d] = mfma32(join(lds_tr16(vt + at), lds_tr16(vt + (at ^ 32) + 8 * T::kRowBytes)), pb, acc[d]);
-          } else {
-            const i32x2 c = lds_tr8(vt + (val ^ (d << 5)));
-            acc[d] = mfma32(e4m3_to_bf16((uint32_t)c[0], (uint32_t)c[1]), pb, acc[d]);
+            pb[a][j] = (__bf16)(e0[j] * c0[j]);
+            pb[a][4 + j] = (__bf16)(e1[j] * c1[j]);
           }
         }
       }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
+        acc[i & 3] = mfma32(vf.get(i), pb[i >> 2], acc[i & 3]);
+        if (i + Values::kAhead < 16) vf.fetch(i + Values::kAhead);
+      }
+      __builtin_amdgcn_sched_barrier(0);
       last = cur.tile + 1 == cur.tiles || cur.left == 1;
       if (!last) {
         advance(p, cur);
