@@ -195,25 +195,22 @@ struct Loader {
 };
 
 // Operands of the value product, kAhead steps ahead: step i is the 16 tokens
-// i/4 and the wave's 32-column block i%4. at: the lane's LDS address in step 0.
+// i/4 and the wave's 32-column block i%4. at: the lane's offset in step 0.
 template <bool FP8>
 struct ValueFeed {
   static constexpr int kAhead = 4;
-  const char* at;
+  const char* base;
+  int at;
   bf16x8 v[FP8 ? 1 : kAhead];
   i32x2 c[FP8 ? kAhead : 1];
-  __device__ __forceinline__ explicit ValueFeed(const char* at_) : at(at_) {}
-  __device__ __forceinline__ const char* xored(int bits) const {
-    return at + (((int)(uintptr_t)(lds_void)at ^ bits) - (int)(uintptr_t)(lds_void)at);
-  }
+  __device__ __forceinline__ ValueFeed(const char* base_, int at_) : base(base_), at(at_) {}
   __device__ __forceinline__ void fetch(int i) {
     const int row = 16 * (i >> 2), d = i & 3;
     if constexpr (FP8) {
-      c[i % kAhead] = lds_tr8(xored(d << 5) + row * Tile<FP8>::kRowBytes);
+      c[i % kAhead] = lds_tr8(base + (at ^ (d << 5)) + row * Tile<FP8>::kRowBytes);
     } else {
-      const char* a = xored(d << 6) + row * Tile<FP8>::kRowBytes;
-      const char* b = xored((d << 6) ^ 32) + (row + 8) * Tile<FP8>::kRowBytes;
-      v[i % kAhead] = join(lds_tr16(a), lds_tr16(b));
+      v[i % kAhead] = join(lds_tr16(base + (at ^ (d << 6)) + row * Tile<FP8>::kRowBytes),
+                           lds_tr16(base + (at ^ (d << 6) ^ 32) + (row + 8) * Tile<FP8>::kRowBytes));
     }
   }
   __device__ __forceinline__ bf16x8 get(int i) const {
@@ -301,8 +298,10 @@ __global__ __launch_bounds__(256 * RT) __attribute__((amdgpu_waves_per_eu(2))) v
   // LDS offsets of this lane: the swizzles only touch bits that the row and
   // tile offsets leave free, so the chunk is picked by an XOR
   const TileLane L(lane);
-  const int key0 = (32 * th + L.row) * T::kRowBytes + kh * (T::kRowBytes / 2) + ((L.half ^ L.x256) << 4);
-  const int rope0 = T::kLatentBytes + (32 * th + L.row) * (2 * kRope) + ((L.half ^ L.x128 ^ (4 * kh)) << 4);
+  // key reads: the 16 tokens whose scores the wave keeps come first
+  const int krow = 32 * th + (L.row ^ (16 * kh));
+  const int key0 = krow * T::kRowBytes + kh * (T::kRowBytes / 2) + ((L.half ^ L.x256) << 4);
+  const int rope0 = T::kLatentBytes + krow * (2 * kRope) + ((L.half ^ L.x128 ^ (4 * kh)) << 4);
   int val0;
   if constexpr (FP8) {
     const int i = (lane & 15) >> 1, row = 4 * L.half + (i & 3) + 8 * (i >> 2);
@@ -348,39 +347,39 @@ __global__ __launch_bounds__(256 * RT) __attribute__((amdgpu_waves_per_eu(2))) v
       else
         attn_wait<0>();
       attn_barrier();
-      const char* tl = tiles + buf * T::kBytes;
+      const int at = buf * T::kBytes;      // of the tile in LDS
+      const char* tl = tiles + at;
 
-      // partial scores: D[token drow(i)][row lane%32] of 32 tokens, operands
-      // fetched kAhead steps ahead, the next tile's loads in between
+      // partial scores: D[token drow(i) ^ 16 kh][row lane%32] of 32 tokens,
+      // operands fetched kAhead steps ahead, the next tile's loads in between
       f32x16 x;
-      const int key = opaque(key0);
+      const int key = opaque(key0 + at), rope = rope0 + at;
       auto partial = [&](auto&& between) {
         if constexpr (!FP8) {
           constexpr int kAhead = 6;
           bf16x8 kf[kAhead];
           auto fetch = [&](int ks) {
-            return lds_bf16x8(ks < 16 ? tl + (key ^ ((ks & 7) << 5)) + (ks >> 3) * 256 : tl + (rope0 ^ ((ks & 1) << 5)));
+            return lds_bf16x8(ks < 16 ? tiles + (key ^ ((ks & 7) << 5)) + (ks >> 3) * 256 : tiles + (rope ^ ((ks & 1) << 5)));
           };
-          f32x16 y[2] = {zero16(), zero16()};      // two chains: an MFMA need not wait for the one before
+          x = zero16();
 #pragma unroll
           for (int ks = 0; ks < kAhead; ++ks) kf[ks] = fetch(ks);
 #pragma unroll
           for (int ks = 0; ks < 18; ++ks) {
             __builtin_amdgcn_sched_barrier(0);
-            y[ks & 1] = mfma32(kf[ks % kAhead], qf[ks], y[ks & 1]);
+            x = mfma32(kf[ks % kAhead], qf[ks], x);
             if (ks + kAhead < 18) kf[ks % kAhead] = fetch(ks + kAhead);
             between(ks);
           }
           __builtin_amdgcn_sched_barrier(0);
-          x = y[0] + y[1];
         } else {
           constexpr int kAhead = 3;
           uint4 kc[kAhead];
-          auto fetch = [&](int h) { return *reinterpret_cast<const uint4*>(tl + (key ^ (h << 5))); };
+          auto fetch = [&](int h) { return *reinterpret_cast<const uint4*>(tiles + (key ^ (h << 5))); };
           f32x16 z[2] = {zero16(), zero16()};      // 128 columns with one scale a token each
 #pragma unroll
           for (int h = 0; h < kAhead; ++h) kc[h] = fetch(h);
-          const bf16x8 r0 = lds_bf16x8(tl + rope0), r1 = lds_bf16x8(tl + (rope0 ^ 32));
+          const bf16x8 r0 = lds_bf16x8(tiles + rope), r1 = lds_bf16x8(tiles + (rope ^ 32));
 #pragma unroll
           for (int h = 0; h < 8; ++h) {            // 32 columns
             __builtin_amdgcn_sched_barrier(0);
@@ -402,7 +401,7 @@ __global__ __launch_bounds__(256 * RT) __attribute__((amdgpu_waves_per_eu(2))) v
 #pragma unroll
             for (int i4 = 0; i4 < 4; ++i4) {
               const f32x4 sc =
-                  *reinterpret_cast<const f32x4*>(tl + scale0 + 4 * kTile * (2 * kh + q) + 4 * (32 * th + 8 * i4));
+                  *reinterpret_cast<const f32x4*>(tl + scale0 + 4 * kTile * (2 * kh + q) + 4 * (32 * th + ((8 * i4) ^ (16 * kh))));
 #pragma unroll
               for (int j = 0; j < 4; ++j) x[4 * i4 + j] = fmaf(sc[j], z[q][4 * i4 + j], x[4 * i4 + j]);
             }
@@ -423,9 +422,8 @@ __global__ __launch_bounds__(256 * RT) __attribute__((amdgpu_waves_per_eu(2))) v
         f32x4 give;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float lo = x[4 * i + j], hi = x[8 + 4 * i + j];
-          give[j] = kh ? lo : hi;
-          s[i][j] = kh ? hi : lo;
+          s[i][j] = x[4 * i + j];
+          give[j] = x[8 + 4 * i + j];
         }
         *reinterpret_cast<f32x4*>(slots + (wave ^ 1) * kSlot + 1024 * i + 16 * lane) = give;
       }
@@ -469,7 +467,7 @@ __global__ __launch_bounds__(256 * RT) __attribute__((amdgpu_waves_per_eu(2))) v
       };
       weigh();
       // the first values are on their way before the waves meet
-      Values vf(tl + opaque(val0));
+      Values vf(tiles, opaque(val0 + at));
 #pragma unroll
       for (int i = 0; i < Values::kAhead; ++i) vf.fetch(i);
       if (L.half == 0) my_stat[L.row] = top;
