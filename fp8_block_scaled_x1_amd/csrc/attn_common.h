@@ -63,6 +63,10 @@ template <int N>
 __device__ __forceinline__ void attn_wait() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
+// Every vector-memory operation done, said to the compiler too: placed after
+// the loads of operands that a loop keeps, it leaves no wait for them (and with
+// them for the tiles in flight) inside the loop.
+__device__ __forceinline__ void operands_loaded() { __builtin_amdgcn_s_waitcnt(0x0F70); }   // vmcnt(0) alone
 // All LDS accesses of the wave done, then meet the other waves. Vector-memory
 // loads in flight stay in flight.
 __device__ __forceinline__ void attn_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }

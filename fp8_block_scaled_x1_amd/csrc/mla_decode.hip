@@ -48,7 +48,6 @@ namespace {
 
 constexpr int kTile = 64;            // tokens per tile
 constexpr int kLatent = 512, kRope = 64, kKey = kLatent + kRope;
-constexpr int kWaitVmcnt0 = 0x0F70;   // s_waitcnt vmcnt(0), the other counters left alone
 constexpr int kThreads = 256;
 // The weights' reference only follows the running maximum once that is more
 // than 2^8 above it: weights up to 2^8 cost no precision in FP32 or BF16, and
@@ -337,9 +336,7 @@ __global__ __launch_bounds__(256 * RT) __attribute__((amdgpu_waves_per_eu(2))) v
     l = 0.f;
 #pragma unroll
     for (int d = 0; d < 4; ++d) acc[d] = zero16();
-    // said to the compiler, which would otherwise wait for the queries inside
-    // the tile loop and with them for the tiles in flight
-    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+    operands_loaded();
 
     for (bool last = false; !last;) {
       if (nxt.left > 0 && NBUF > 2)

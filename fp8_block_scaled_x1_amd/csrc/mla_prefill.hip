@@ -70,11 +70,38 @@ __device__ __forceinline__ f32x16 scores(const char* t, const TileLane& L, int k
   return s;
 }
 
-// Forward: NW waves of 32 queries, key tiles of 64 in two LDS buffers.
+// The weights' reference follows the running maximum only once that is more
+// than 2^8 above it: weights up to 2^8 cost no precision in FP32 or BF16, and
+// the output is rescaled a few times per row instead of per tile.
+constexpr float kSlack = 8.f;
+
+// The wave's share of a key tile's loads, one by one.
 template <int NW>
-__global__ __launch_bounds__(64 * NW, 2) void mla_fwd_kernel(const MlaPrefill p, int units) {
+struct KeyLoader {
+  static constexpr int kRows = kBn / NW, kWide = kRows / 4, kLoads = 2 * kWide + kRows / 8;
+  static_assert(kRows % 8 == 0, "whole loads per wave");
+  const MlaPrefill& p;
+  const uint16_t *kv, *kr;
+  int row0, last, w, lane;
+  uint32_t lds;
+  __device__ __forceinline__ void issue(int n) const {
+    if (n < kWide)
+      load_rows256(kv, p.kv_stride, row0, last, kRows * w + 4 * n, lane, lds);
+    else if (n < 2 * kWide)
+      load_rows256(kv + kNope, p.kv_stride, row0, last, kRows * w + 4 * (n - kWide), lane, lds + kNopeTile + kRopeTile);
+    else
+      load_rows128(kr, p.rope_stride, row0, last, kRows * w + 8 * (n - 2 * kWide), lane, lds + kNopeTile);
+  }
+};
+
+// Forward: NW waves of 32 queries; key tiles of 64 in NBUF LDS buffers, NBUF - 1
+// of them on their way while one is used.
+template <int NW, int NBUF>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) void mla_fwd_kernel(const MlaPrefill p,
+                                                                                                 int units) {
   constexpr int BM = 32 * NW;
-  __shared__ __align__(1024) char tiles[2 * kFwdTile];
+  using Load = KeyLoader<NW>;
+  __shared__ __align__(1024) char tiles[NBUF * kFwdTile];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int unit, head;
@@ -100,7 +127,7 @@ __global__ __launch_bounds__(64 * NW, 2) void mla_fwd_kernel(const MlaPrefill p,
   const uint16_t* kv = p.kv + (int64_t)k0 * p.kv_stride + head * (kNope + kVDim);
   const uint16_t* kr = p.k_rope + (int64_t)k0 * p.rope_stride;
   const uint32_t lds = lds_offset(tiles);
-  if (nt > 0) load_keys<NW>(p, kv, kr, 0, Lk - 1, w, lane, lds);
+  auto loader = [&](int t, int to) { return Load{p, kv, kr, t * kBn, Lk - 1, w, lane, lds + to * kFwdTile}; };
 
   bf16x8 qf[12];
   load_operand(qf, p.q + (int64_t)(u.r0 + qc) * p.q_stride + head * kQk, L.half);
@@ -108,17 +135,62 @@ __global__ __launch_bounds__(64 * NW, 2) void mla_fwd_kernel(const MlaPrefill p,
   f32x16 o[4];
 #pragma unroll
   for (int d = 0; d < 4; ++d) o[d] = zero16();
-  float m = neg_inf(), l = 0.f;      // m: of the raw scores
-
-  for (int t = 0; t < nt; ++t) {
-    attn_wait<0>();
-    attn_barrier();
-    if (t + 1 < nt) load_keys<NW>(p, kv, kr, (t + 1) * kBn, Lk - 1, w, lane, lds + ((t + 1) & 1) * kFwdTile);
-    if (t * kBn >= wave_any) continue;
-    const char* tl = tiles + (t & 1) * kFwdTile;
-    f32x16 s[2];
+  float m = neg_inf(), l = 0.f;      // m: in units of log2
+  operands_loaded();
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) s[kb] = scores(tl, L, 32 * kb, qf);
+  for (int i = 0; i < NBUF - 1; ++i)
+    if (i < nt) {
+      const Load ld = loader(i, i);
+#pragma unroll
+      for (int n = 0; n < Load::kLoads; ++n) ld.issue(n);
+    }
+  const int key0 = at256(L), rope0 = kNopeTile + at128(L), val0 = kNopeTile + kRopeTile + at256t(L);
+
+  int buf = 0;
+  for (int t = 0; t < nt; ++t, buf = buf + 1 == NBUF ? 0 : buf + 1) {
+    if (NBUF > 2 && t + NBUF - 2 < nt)
+      attn_wait<(NBUF - 2) * Load::kLoads>();
+    else
+      attn_wait<0>();
+    attn_barrier();
+    const int more = t + NBUF - 1;
+    const Load ld = loader(more, buf == 0 ? NBUF - 1 : buf - 1);
+    if (t * kBn >= wave_any) {      // nothing here for this wave: only its share of the loads
+      if (more < nt) {
+#pragma unroll
+        for (int n = 0; n < Load::kLoads; ++n) ld.issue(n);
+      }
+      continue;
+    }
+    const int at = buf * kFwdTile;
+    f32x16 s[2];
+    // S^T, operands fetched kAhead steps ahead, the loads of a later tile in between
+    auto products = [&](auto&& between) {
+      constexpr int kAhead = 6;
+      const int key = opaque(key0 + at), rope = opaque(rope0 + at);
+      bf16x8 kf[kAhead];
+      auto fetch = [&](int i) {      // step i: k step i/2 of key block i%2
+        return i < 16 ? get256(tiles, key, 32 * (i & 1), i >> 1) : get128(tiles, rope, 32 * (i & 1), (i >> 1) - 8);
+      };
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) kf[i] = fetch(i);
+      s[0] = zero16();
+      s[1] = zero16();
+#pragma unroll
+      for (int i = 0; i < 24; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
+        s[i & 1] = mfma32(kf[i % kAhead], qf[i >> 1], s[i & 1]);
+        if (i + kAhead < 24) kf[i % kAhead] = fetch(i + kAhead);
+        between(i);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    if (more < nt)
+      products([&](int i) {
+        if (i * Load::kLoads / 24 != (i + 1) * Load::kLoads / 24) ld.issue(i * Load::kLoads / 24);
+      });
+    else
+      products([](int) {});
     if ((t + 1) * kBn > wave_all) {
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
@@ -126,21 +198,28 @@ __global__ __launch_bounds__(64 * NW, 2) void mla_fwd_kernel(const MlaPrefill p,
         for (int i = 0; i < 16; ++i)
           if (t * kBn + 32 * kb + drow(i, L.half) >= see) s[kb][i] = neg_inf();
     }
+    // the first values are on their way during the softmax
+    constexpr int kAhead = 4;
+    const int val = opaque(val0 + at);
+    bf16x8 vf[kAhead];
+    auto fetch = [&](int i) { return get256t(tiles, val, 16 * (i >> 2), i & 3); };      // 16 keys i/4, columns i%4
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) vf[i] = fetch(i);
     float mt = s[0][0];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
       for (int i = 0; i < 16; ++i) mt = fmaxf(mt, s[kb][i]);
-    mt = fmaxf(mt, __shfl_xor(mt, 32, 64));
-    const float mn = fmaxf(m, mt);
-    const float ref = mn == neg_inf() ? 0.f : mn * c;
-    if (__any(mn > m)) {
-      const float alpha = exp2_fast(m * c - ref);
+    mt = half_max(mt) * c;
+    if (__any(mt > m + kSlack)) {
+      const float mn = fmaxf(m, mt);
+      const float alpha = mn == neg_inf() ? 1.f : exp2_fast(m - mn);
+      m = mn;
       l *= alpha;
 #pragma unroll
       for (int d = 0; d < 4; ++d) o[d] *= alpha;
-      m = mn;
     }
+    const float ref = m == neg_inf() ? 0.f : m;      // nothing visible yet: every weight is 0
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       float sum = 0.f;
@@ -151,18 +230,19 @@ __global__ __launch_bounds__(64 * NW, 2) void mla_fwd_kernel(const MlaPrefill p,
       }
       l += sum;
     }
-    const char* vt = tl + kNopeTile + kRopeTile;
+    bf16x8 pb[4];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+    for (int a = 0; a < 4; ++a) pb[a] = pack8(s[a >> 1], a & 1);
 #pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        const bf16x8 pb = pack8(s[kb], a);
-#pragma unroll
-        for (int d = 0; d < 4; ++d) o[d] = mfma32(cols256(vt, L, 32 * kb + 16 * a, d), pb, o[d]);
-      }
+    for (int i = 0; i < 16; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      o[i & 3] = mfma32(vf[i % kAhead], pb[i >> 2], o[i & 3]);
+      if (i + kAhead < 16) vf[i % kAhead] = fetch(i + kAhead);
+    }
+    __builtin_amdgcn_sched_barrier(0);
   }
 
-  l += __shfl_xor(l, 32, 64);
+  l = half_sum(l);
   if (qi < Lq) {
     const float inv = l > 0.f ? 1.f / l : 0.f;
     uint16_t* op = p.out + ((int64_t)(u.r0 + qi) * p.H + head) * kVDim + 4 * L.half;
@@ -176,7 +256,7 @@ __global__ __launch_bounds__(64 * NW, 2) void mla_fwd_kernel(const MlaPrefill p,
         *reinterpret_cast<bf16x4*>(op + 32 * d + 8 * i) = b;
       }
     if (L.half == 0)
-      p.lse[(int64_t)head * p.Tq + u.r0 + qi] = l > 0.f ? (m * c + __builtin_log2f(l)) * kLn2 : neg_inf();
+      p.lse[(int64_t)head * p.Tq + u.r0 + qi] = l > 0.f ? (m + __builtin_log2f(l)) * kLn2 : neg_inf();
   }
 }
 
@@ -250,6 +330,7 @@ __global__ __launch_bounds__(256, 1) void mla_dkv_kernel(const MlaPrefill p, int
   };
   if (nt > 0) load(0);
   const float c = p.scale * kLog2e;
+  operands_loaded();
 
   for (int t = 0; t < nt; ++t) {
     attn_wait<0>();
@@ -364,6 +445,7 @@ __global__ __launch_bounds__(64 * NW, 2) void mla_dq_kernel(const MlaPrefill p, 
   f32x16 dq[6];
 #pragma unroll
   for (int d = 0; d < 6; ++d) dq[d] = zero16();
+  operands_loaded();
 
   for (int t = 0; t < nt; ++t) {
     attn_wait<0>();
@@ -427,8 +509,11 @@ int64_t blocks(int64_t tokens, int B, int rows) { return (tokens + rows - 1) / r
 }  // namespace
 
 hipError_t launch_mla_prefill(const MlaPrefill& p, hipStream_t stream) {
-  const int64_t units = blocks(p.Tq, p.B, 128);
-  hipLaunchKernelGGL(mla_fwd_kernel<4>, dim3(unit_grid(units, p.H)), dim3(256), 0, stream, p, (int)units);
+  const int64_t wide = blocks(p.Tq, p.B, 256), units = blocks(p.Tq, p.B, 128);
+  if (wide * p.H >= 1024)
+    hipLaunchKernelGGL((mla_fwd_kernel<8, 3>), dim3(unit_grid(wide, p.H)), dim3(512), 0, stream, p, (int)wide);
+  else
+    hipLaunchKernelGGL((mla_fwd_kernel<4, 2>), dim3(unit_grid(units, p.H)), dim3(256), 0, stream, p, (int)units);
   return hipGetLastError();
 }
 
