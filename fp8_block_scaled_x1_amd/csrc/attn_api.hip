@@ -28,9 +28,11 @@ int prefill_sizes(int B, int64_t Tq, int64_t Tk, int H, int64_t q_stride, int64_
                   float scale) {
   if (B < 0 || Tq < 0 || Tk < 0 || H < 1) return FP8BS_ERR_SHAPE;
   if (B == 0 && (Tq > 0 || Tk > 0)) return FP8BS_ERR_SHAPE;      // tokens of no request
-  if (H > 65536 || Tq >= kI32 - 65536 || Tk >= kI32 - 65536) return FP8BS_ERR_TOO_LARGE;
+  if (H > 32768 || Tq >= kI32 - 65536 || Tk >= kI32 - 65536) return FP8BS_ERR_TOO_LARGE;
   if (q_stride < (int64_t)H * 192 || kv_stride < (int64_t)H * 256 || rope_stride < 64) return FP8BS_ERR_SHAPE;
   if (q_stride % 8 || kv_stride % 8 || rope_stride % 8) return FP8BS_ERR_ALIGN;
+  // a tile's rows are addressed by 32-bit byte offsets from its first
+  if (q_stride >= 1 << 24 || kv_stride >= 1 << 24 || rope_stride >= 1 << 24) return FP8BS_ERR_TOO_LARGE;
   const int64_t most = Tq > Tk ? Tq : Tk;
   if ((most / 32 + 1 + B) * H > kGridMax || most * H > kGridMax * 8) return FP8BS_ERR_TOO_LARGE;
   if (bad_scale(scale)) return FP8BS_ERR_VALUE;
@@ -181,7 +183,7 @@ int fp8bs_mla_prefill(const uint16_t* q, int64_t q_stride, const uint16_t* kv, i
 
 int64_t fp8bs_mla_prefill_bwd_workspace_bytes(int64_t Tq, int64_t Tk, int H) {
   if (Tq < 0 || Tk < 0 || H < 1) return FP8BS_ERR_SHAPE;
-  if (Tq >= kI32 || Tk >= kI32 || H > 65536) return FP8BS_ERR_TOO_LARGE;
+  if (Tq >= kI32 || Tk >= kI32 || H > 32768) return FP8BS_ERR_TOO_LARGE;
   return align256(4 * Tq * H) + 4 * Tk * H * 64;
 }
 

@@ -75,31 +75,46 @@ __device__ __forceinline__ f32x16 scores(const char* t, const TileLane& L, int k
 // the output is rescaled a few times per row instead of per tile.
 constexpr float kSlack = 8.f;
 
-// The wave's share of a key tile's loads, one by one.
+// The wave's share of a key tile's loads, one by one: each lane's offsets from
+// the tile's first token stay in registers, the tile's base is wave-uniform.
 template <int NW>
 struct KeyLoader {
   static constexpr int kRows = kBn / NW, kWide = kRows / 4, kLoads = 2 * kWide + kRows / 8;
   static_assert(kRows % 8 == 0, "whole loads per wave");
-  const MlaPrefill& p;
-  const uint16_t *kv, *kr;
-  int row0, last, w, lane;
-  uint32_t lds;
-  __device__ __forceinline__ void issue(int n) const {
+  uint32_t off[kWide + kRows / 8];
+  // last: the tile's last row that exists (rows past it repeat it)
+  __device__ __forceinline__ void place(const MlaPrefill& p, int last, int w, int lane) {
+#pragma unroll
+    for (int n = 0; n < kWide; ++n) {
+      const int r = kRows * w + 4 * n + (lane >> 4);
+      off[n] = (uint32_t)(min(r, last) * (int)p.kv_stride + (((lane & 15) ^ swz256(r)) << 3)) * 2;
+    }
+#pragma unroll
+    for (int n = 0; n < kRows / 8; ++n) {
+      const int r = kRows * w + 8 * n + (lane >> 3);
+      off[kWide + n] = (uint32_t)(min(r, last) * (int)p.rope_stride + (((lane & 7) ^ swz128(r)) << 3)) * 2;
+    }
+  }
+  __device__ __forceinline__ void issue(int n, const uint16_t* kv, const uint16_t* kr, int w, uint32_t lds) const {
     if (n < kWide)
-      load_rows256(kv, p.kv_stride, row0, last, kRows * w + 4 * n, lane, lds);
+      dma16_s(kv, off[n], lds + (kRows * w + 4 * n) * 256);
     else if (n < 2 * kWide)
-      load_rows256(kv + kNope, p.kv_stride, row0, last, kRows * w + 4 * (n - kWide), lane, lds + kNopeTile + kRopeTile);
+      dma16_s(kv + kNope, off[n - kWide], lds + kNopeTile + kRopeTile + (kRows * w + 4 * (n - kWide)) * 256);
     else
-      load_rows128(kr, p.rope_stride, row0, last, kRows * w + 8 * (n - 2 * kWide), lane, lds + kNopeTile);
+      dma16_s(kr, off[n - kWide], lds + kNopeTile + (kRows * w + 8 * (n - 2 * kWide)) * 128);
   }
 };
 
-// Forward: NW waves of 32 queries; key tiles of 64 in NBUF LDS buffers, NBUF - 1
-// of them on their way while one is used.
-template <int NW, int NBUF>
+// Forward: NW waves of 32 queries; key tiles of 64 in three LDS buffers. The
+// loop is staggered by one tile: the scores of tile t+1 are formed (matrix
+// unit) while the weights of tile t are (vector unit: 32 exponentials a lane,
+// about as long as the tile's products), and the values of tile t are added
+// while the maxima of tile t+1 are found; so one wave alone keeps both units
+// busy, and what it waits for is bridged by the SIMD's second wave.
+template <int NW>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) void mla_fwd_kernel(const MlaPrefill p,
                                                                                                  int units) {
-  constexpr int BM = 32 * NW;
+  constexpr int BM = 32 * NW, NBUF = 3;
   using Load = KeyLoader<NW>;
   __shared__ __align__(1024) char tiles[NBUF * kFwdTile];
   const int lane = threadIdx.x & 63;
@@ -122,12 +137,25 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
   const int qc = min(qi, Lq - 1);
   const int see = p.causal ? min(Lk, qi + off + 1) : Lk;                   // keys it sees
   const int wave_all = p.causal ? min(Lk, first + 32 * w + off + 1) : Lk;  // keys all the wave's queries see
-  const int wave_any = p.causal ? min(Lk, first + 32 * w + 32 + off) : Lk;
+  const int wave_any = p.causal ? min(kend, max(first + 32 * w + 32 + off, 0)) : Lk;
+  const int wave_nt = first + 32 * w < Lq ? (wave_any + kBn - 1) / kBn : 0;      // its tiles: the first ones
 
   const uint16_t* kv = p.kv + (int64_t)k0 * p.kv_stride + head * (kNope + kVDim);
   const uint16_t* kr = p.k_rope + (int64_t)k0 * p.rope_stride;
   const uint32_t lds = lds_offset(tiles);
-  auto loader = [&](int t, int to) { return Load{p, kv, kr, t * kBn, Lk - 1, w, lane, lds + to * kFwdTile}; };
+  Load ld;
+  ld.place(p, min(Lk, kBn) - 1, w, lane);
+  int loaded = 0;      // tiles whose loads are under way
+  // the next tile's loads: `kvt`, `krt` its first token
+  const uint16_t *kvt = kv, *krt = kr;
+  auto loads_begin = [&] {
+    if (loaded > 0 && (loaded + 1) * kBn > Lk) ld.place(p, Lk - 1 - loaded * kBn, w, lane);
+  };
+  auto loads_end = [&] {
+    ++loaded;
+    kvt += (int64_t)kBn * p.kv_stride;
+    krt += (int64_t)kBn * p.rope_stride;
+  };
 
   bf16x8 qf[12];
   load_operand(qf, p.q + (int64_t)(u.r0 + qc) * p.q_stride + head * kQk, L.half);
@@ -140,106 +168,140 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
 #pragma unroll
   for (int i = 0; i < NBUF - 1; ++i)
     if (i < nt) {
-      const Load ld = loader(i, i);
+      loads_begin();
 #pragma unroll
-      for (int n = 0; n < Load::kLoads; ++n) ld.issue(n);
+      for (int n = 0; n < Load::kLoads; ++n) ld.issue(n, kvt, krt, w, lds + i * kFwdTile);
+      loads_end();
     }
   const int key0 = at256(L), rope0 = kNopeTile + at128(L), val0 = kNopeTile + kRopeTile + at256t(L);
 
-  int buf = 0;
-  for (int t = 0; t < nt; ++t, buf = buf + 1 == NBUF ? 0 : buf + 1) {
-    if (NBUF > 2 && t + NBUF - 2 < nt)
-      attn_wait<(NBUF - 2) * Load::kLoads>();
-    else
-      attn_wait<0>();
-    attn_barrier();
-    const int more = t + NBUF - 1;
-    const Load ld = loader(more, buf == 0 ? NBUF - 1 : buf - 1);
-    if (t * kBn >= wave_any) {      // nothing here for this wave: only its share of the loads
-      if (more < nt) {
-#pragma unroll
-        for (int n = 0; n < Load::kLoads; ++n) ld.issue(n);
-      }
-      continue;
-    }
-    const int at = buf * kFwdTile;
-    f32x16 s[2];
-    // S^T, operands fetched kAhead steps ahead, the loads of a later tile in between
-    auto products = [&](auto&& between) {
-      constexpr int kAhead = 6;
-      const int key = opaque(key0 + at), rope = opaque(rope0 + at);
-      bf16x8 kf[kAhead];
-      auto fetch = [&](int i) {      // step i: k step i/2 of key block i%2
-        return i < 16 ? get256(tiles, key, 32 * (i & 1), i >> 1) : get128(tiles, rope, 32 * (i & 1), (i >> 1) - 8);
-      };
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) kf[i] = fetch(i);
-      s[0] = zero16();
-      s[1] = zero16();
-#pragma unroll
-      for (int i = 0; i < 24; ++i) {
-        __builtin_amdgcn_sched_barrier(0);
-        s[i & 1] = mfma32(kf[i % kAhead], qf[i >> 1], s[i & 1]);
-        if (i + kAhead < 24) kf[i % kAhead] = fetch(i + kAhead);
-        between(i);
-      }
-      __builtin_amdgcn_sched_barrier(0);
+  // S^T of the tile at LDS offset `at`, operands fetched kAhead steps ahead
+  constexpr int kAhead = 4;
+  auto products = [&](f32x16 (&s)[2], int at, auto&& between) {
+    const int key = opaque(key0 + at), rope = opaque(rope0 + at);
+    bf16x8 kf[kAhead];
+    auto fetch = [&](int i) {      // step i: k step i/2 of key block i%2
+      return i < 16 ? get256(tiles, key, 32 * (i & 1), i >> 1) : get128(tiles, rope, 32 * (i & 1), (i >> 1) - 8);
     };
-    if (more < nt)
-      products([&](int i) {
-        if (i * Load::kLoads / 24 != (i + 1) * Load::kLoads / 24) ld.issue(i * Load::kLoads / 24);
-      });
-    else
-      products([](int) {});
-    if ((t + 1) * kBn > wave_all) {
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
+    for (int i = 0; i < kAhead; ++i) kf[i] = fetch(i);
+    s[0] = zero16();
+    s[1] = zero16();
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (t * kBn + 32 * kb + drow(i, L.half) >= see) s[kb][i] = neg_inf();
+    for (int i = 0; i < 24; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      s[i & 1] = mfma32(kf[i % kAhead], qf[i >> 1], s[i & 1]);
+      if (i + kAhead < 24) kf[i % kAhead] = fetch(i + kAhead);
+      between(i);
     }
-    // the first values are on their way during the softmax
-    constexpr int kAhead = 4;
-    const int val = opaque(val0 + at);
-    bf16x8 vf[kAhead];
-    auto fetch = [&](int i) { return get256t(tiles, val, 16 * (i >> 2), i & 3); };      // 16 keys i/4, columns i%4
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) vf[i] = fetch(i);
-    float mt = s[0][0];
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto mask = [&](f32x16 (&s)[2], int t) {
+    if ((t + 1) * kBn <= wave_all) return;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) mt = fmaxf(mt, s[kb][i]);
-    mt = half_max(mt) * c;
-    if (__any(mt > m + kSlack)) {
-      const float mn = fmaxf(m, mt);
+      for (int i = 0; i < 16; ++i)
+        if (t * kBn + 32 * kb + drow(i, L.half) >= see) s[kb][i] = neg_inf();
+  };
+  // Raises the weights' reference where a tile's maximum asks for it.
+  auto raise = [&](float top) {
+    top = half_max(top) * c;
+    if (__any(top > m + kSlack)) {
+      const float mn = fmaxf(m, top);
       const float alpha = mn == neg_inf() ? 1.f : exp2_fast(m - mn);
       m = mn;
       l *= alpha;
 #pragma unroll
       for (int d = 0; d < 4; ++d) o[d] *= alpha;
     }
-    const float ref = m == neg_inf() ? 0.f : m;      // nothing visible yet: every weight is 0
+  };
+  auto max4 = [](const f32x16& v, int i) { return fmaxf(fmaxf(v[4 * i], v[4 * i + 1]), fmaxf(v[4 * i + 2], v[4 * i + 3])); };
+
+  int buf = 0;
+  // Tile t, whose scores are in s; those of tile t+1 go to sn.
+  auto step = [&](int t, f32x16 (&s)[2], f32x16 (&sn)[2]) {
+    if (t + NBUF - 1 < nt)
+      attn_wait<(NBUF - 3) * Load::kLoads>();
+    else
+      attn_wait<0>();
+    attn_barrier();
+    const int at = buf * kFwdTile, next = buf + 1 == NBUF ? 0 : buf + 1, prev = buf == 0 ? NBUF - 1 : buf - 1;
+    const bool load = loaded < nt;
+    if (load) loads_begin();
+    auto issue = [&](int n) { ld.issue(n, kvt, krt, w, lds + prev * kFwdTile); };
+    if (t < wave_nt) {
+      const float ref = m == neg_inf() ? 0.f : m;      // nothing visible yet: every weight is 0
+      bf16x8 pb[4];
+      float sum[2] = {0.f, 0.f};
+      auto weigh = [&](int i) {      // element i of the lane's 32
+        const float e = exp2_fast(fmaf(s[i >> 4][i & 15], c, -ref));
+        sum[i & 1] += e;
+        pb[i >> 3][i & 7] = (__bf16)e;
+      };
+      auto weigh_at = [&](int i) {      // 32 elements over 24 steps
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      float sum = 0.f;
+        for (int e = i * 32 / 24; e < (i + 1) * 32 / 24; ++e) weigh(e);
+      };
+      const bool more = t + 1 < wave_nt;
+      if (more && load) {
+        products(sn, next * kFwdTile, [&](int i) {
+          weigh_at(i);
+          if (i * Load::kLoads / 24 != (i + 1) * Load::kLoads / 24) issue(i * Load::kLoads / 24);
+        });
+      } else {
+        if (load) {
+#pragma unroll
+          for (int n = 0; n < Load::kLoads; ++n) issue(n);
+        }
+        if (more)
+          products(sn, next * kFwdTile, weigh_at);
+        else {
+#pragma unroll
+          for (int i = 0; i < 24; ++i) weigh_at(i);
+        }
+      }
+      l += sum[0] + sum[1];
+      if (more) mask(sn, t + 1);
+      const int val = opaque(val0 + at);
+      bf16x8 vf[kAhead];
+      auto fetch = [&](int i) { return get256t(tiles, val, 16 * (i >> 2), i & 3); };      // 16 keys i/4, columns i%4
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) vf[i] = fetch(i);
+      float top[2] = {neg_inf(), neg_inf()};
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        s[kb][i] = exp2_fast(fmaf(s[kb][i], c, -ref));
-        sum += s[kb][i];
+        __builtin_amdgcn_sched_barrier(0);
+        o[i & 3] = mfma32(vf[i % kAhead], pb[i >> 2], o[i & 3]);
+        if (i + kAhead < 16) vf[i % kAhead] = fetch(i + kAhead);
+        if (i & 1) top[(i >> 1) & 1] = fmaxf(top[(i >> 1) & 1], max4(sn[i >> 3], (i >> 1) & 3));
       }
-      l += sum;
-    }
-    bf16x8 pb[4];
-#pragma unroll
-    for (int a = 0; a < 4; ++a) pb[a] = pack8(s[a >> 1], a & 1);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
       __builtin_amdgcn_sched_barrier(0);
-      o[i & 3] = mfma32(vf[i % kAhead], pb[i >> 2], o[i & 3]);
-      if (i + kAhead < 16) vf[i % kAhead] = fetch(i + kAhead);
+      if (more) raise(fmaxf(top[0], top[1]));
+    } else if (load) {      // nothing here for this wave: only its share of the loads
+#pragma unroll
+      for (int n = 0; n < Load::kLoads; ++n) issue(n);
     }
-    __builtin_amdgcn_sched_barrier(0);
+    if (load) loads_end();
+    buf = next;
+  };
+
+  f32x16 sa[2], sb[2];
+  if (nt > 0) {
+    attn_wait<0>();
+    attn_barrier();
+    if (wave_nt > 0) {
+      products(sa, 0, [](int) {});
+      mask(sa, 0);
+      float top = neg_inf();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, max4(sa[i >> 2], i & 3));
+      raise(top);
+    }
+  }
+  for (int t = 0; t < nt; t += 2) {
+    step(t, sa, sb);
+    if (t + 1 < nt) step(t + 1, sb, sa);
   }
 
   l = half_sum(l);
@@ -511,9 +573,9 @@ int64_t blocks(int64_t tokens, int B, int rows) { return (tokens + rows - 1) / r
 hipError_t launch_mla_prefill(const MlaPrefill& p, hipStream_t stream) {
   const int64_t wide = blocks(p.Tq, p.B, 256), units = blocks(p.Tq, p.B, 128);
   if (wide * p.H >= 1024)
-    hipLaunchKernelGGL((mla_fwd_kernel<8, 3>), dim3(unit_grid(wide, p.H)), dim3(512), 0, stream, p, (int)wide);
+    hipLaunchKernelGGL(mla_fwd_kernel<8>, dim3(unit_grid(wide, p.H)), dim3(512), 0, stream, p, (int)wide);
   else
-    hipLaunchKernelGGL((mla_fwd_kernel<4, 2>), dim3(unit_grid(units, p.H)), dim3(256), 0, stream, p, (int)units);
+    hipLaunchKernelGGL(mla_fwd_kernel<4>, dim3(unit_grid(units, p.H)), dim3(256), 0, stream, p, (int)units);
   return hipGetLastError();
 }
 

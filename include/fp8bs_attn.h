@@ -54,7 +54,7 @@ enum fp8bs_cache { FP8BS_CACHE_BF16 = 0, FP8BS_CACHE_FP8 = 1 };
  *   cu_q, cu_k [B+1]      int32: first is 0, non-decreasing, last is Tq (Tk)
  *                         (precondition; the kernels clamp them into range)
  *   out     [Tq][H][128]  BF16      lse [H][Tq] float32
- * Strides: multiples of 8, at least a token's numbers. Scores, statistics and
+ * Strides: multiples of 8, at least a token's numbers, below 2^24. Scores, statistics and
  * sums are FP32; probabilities are rounded to BF16 for the matrix unit.
  * scale finite and > 0 (else FP8BS_ERR_VALUE); H >= 1.
  */
