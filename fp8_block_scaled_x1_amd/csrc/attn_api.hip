@@ -184,7 +184,7 @@ int fp8bs_mla_prefill(const uint16_t* q, int64_t q_stride, const uint16_t* kv, i
 int64_t fp8bs_mla_prefill_bwd_workspace_bytes(int64_t Tq, int64_t Tk, int H) {
   if (Tq < 0 || Tk < 0 || H < 1) return FP8BS_ERR_SHAPE;
   if (Tq >= kI32 || Tk >= kI32 || H > 32768) return FP8BS_ERR_TOO_LARGE;
-  return align256(4 * Tq * H) + 4 * Tk * H * 64;
+  return 2 * align256(4 * Tq * H) + 4 * Tk * H * 64;
 }
 
 int fp8bs_mla_prefill_bwd(const uint16_t* dout, const uint16_t* q, int64_t q_stride, const uint16_t* kv,
@@ -213,7 +213,8 @@ int fp8bs_mla_prefill_bwd(const uint16_t* dout, const uint16_t* q, int64_t q_str
   p.lse = const_cast<float*>(lse);
   p.dout = dout;
   p.delta = static_cast<float*>(workspace);
-  p.rope_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(4 * Tq * H));
+  p.lse2 = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(4 * Tq * H));
+  p.rope_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + 2 * align256(4 * Tq * H));
   p.dq = dq; p.dkv = dkv; p.dk_rope = dk_rope;
   return status_of(fp8bs::launch_mla_prefill_bwd(p, as_stream(stream)));
 }

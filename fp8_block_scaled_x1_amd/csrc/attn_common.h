@@ -56,6 +56,9 @@ __device__ __forceinline__ void dma16_s(const void* base, uint32_t voff, uint32_
 __device__ __forceinline__ void dma4(const void* src, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(lds) : "m0");
 }
+__device__ __forceinline__ void dma4_s(const void* base, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "s"(lds) : "m0");
+}
 
 // At most N of the wave's vector-memory operations stay pending (they complete
 // in issue order).

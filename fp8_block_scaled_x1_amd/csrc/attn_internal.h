@@ -23,6 +23,7 @@ struct MlaPrefill {
   // backward only
   const uint16_t* dout;   // [Tq][H][128]
   float* delta;           // [H][Tq]
+  float* lse2;            // [H][Tq]
   float* rope_part;       // [H][Tk][64]
   uint16_t* dq;           // [Tq][H][192]
   uint16_t* dkv;          // [Tk][H][256]

@@ -322,7 +322,8 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
   }
 }
 
-// D[h][t] = dO . O: 16 lanes per (token, head) row of 128.
+// D[h][t] = dO . O, and lse in units of log2 (0 for a query that sees no key,
+// whose scores are all masked): 16 lanes per (token, head) row of 128.
 __global__ __launch_bounds__(256) void mla_delta_kernel(const MlaPrefill p) {
   const int64_t r = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 4;
   const int part = threadIdx.x & 15;
@@ -334,18 +335,27 @@ __global__ __launch_bounds__(256) void mla_delta_kernel(const MlaPrefill p) {
   for (int i = 0; i < 8; ++i) v = fmaf((float)a[i], (float)b[i], v);
 #pragma unroll
   for (int d = 1; d < 16; d <<= 1) v += __shfl_xor(v, d, 64);
-  if (part == 0) p.delta[(r % p.H) * p.Tq + r / p.H] = v;
+  if (part == 0) {
+    const int64_t at = (r % p.H) * p.Tq + r / p.H;
+    const float lse = p.lse[at];
+    p.delta[at] = v;
+    p.lse2[at] = lse == neg_inf() ? 0.f : lse * kLog2e;
+  }
 }
 
 // Gradients of keys and values: 4 waves of 32 keys each, whose dK and dV stay
-// in registers while the tiles of 64 queries (Q, dO, lse, D) pass.
+// in registers (160 a lane, next to 80 of the keys and values themselves: one
+// wave per SIMD) while 32 queries at a time pass, in tiles of 64 (Q, dO, lse,
+// D) of which one is used and two are on their way. Staggered by one step: the
+// scores and dP of the next 32 queries are formed while the weights and dS of
+// these are, then dK and dV take these.
 constexpr int kBq = 64;
 constexpr int kQNope = kBq * 256, kQRope = kBq * 128, kDo = kBq * 256;
 constexpr int kBwdTile = kQNope + kQRope + kDo + 2 * kBq * 4;
 
 __global__ __launch_bounds__(256, 1) void mla_dkv_kernel(const MlaPrefill p, int units) {
-  constexpr int NW = 4, BK = 32 * NW;
-  __shared__ __align__(1024) char tiles[2 * kBwdTile];
+  constexpr int NW = 4, BK = 32 * NW, NBUF = 3, kLoads = 4 + 2 + 4 + 1;
+  __shared__ __align__(1024) char tiles[NBUF * kBwdTile];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int unit, head;
@@ -358,7 +368,7 @@ __global__ __launch_bounds__(256, 1) void mla_dkv_kernel(const MlaPrefill p, int
   const int kb0 = (unit - u.base) * BK;
   const int key0 = kb0 + 32 * w;
   const int start = p.causal ? max(0, kb0 - off) : 0;        // first query that sees the block's first key
-  const int nt = Lq > start ? (Lq - start + kBq - 1) / kBq : 0;
+  const int steps = Lq > start ? (Lq - start + 31) / 32 : 0, nt = (steps + 1) / 2;
 
   const TileLane L(lane);
   const int key = key0 + L.row, kc = min(key, Lk - 1);
@@ -380,64 +390,161 @@ __global__ __launch_bounds__(256, 1) void mla_dkv_kernel(const MlaPrefill p, int
 
   const uint16_t* qb = p.q + (int64_t)q0 * p.q_stride + head * kQk;
   const uint16_t* db = p.dout + ((int64_t)q0 * p.H + head) * kVDim;
-  const float* stat = (w == 0 ? p.lse : p.delta) + (int64_t)head * p.Tq + q0;
+  const float* stat = (w & 1 ? p.delta : p.lse2) + (int64_t)head * p.Tq + q0;      // (twice each, alike)
   const uint32_t lds = lds_offset(tiles);
-  auto load = [&](int t) {
-    const uint32_t at = lds + (t & 1) * kBwdTile;
-    const int row0 = start + t * kBq;
-    load_tile256<kBq, NW>(qb, p.q_stride, row0, Lq - 1, w, lane, at);
-    load_tile128<kBq, NW>(qb + kNope, p.q_stride, row0, Lq - 1, w, lane, at + kQNope);
-    load_tile256<kBq, NW>(db, (int64_t)p.H * kVDim, row0, Lq - 1, w, lane, at + kQNope + kQRope);
-    if (w < 2) dma4(stat + min(row0 + lane, Lq - 1), at + kQNope + kQRope + kDo + w * kBq * 4);
+  // A tile's loads: offsets from its first query in registers, clamped to the
+  // last query where the tile has fewer than 64.
+  uint32_t off_q[4], off_d[4], off_r[2], off_s;
+  auto place = [&](int last) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const int r = 16 * w + 4 * n + (lane >> 4), x = ((lane & 15) ^ swz256(r)) << 3;
+      off_q[n] = (uint32_t)(min(r, last) * (int)p.q_stride + x) * 2;
+      off_d[n] = (uint32_t)(min(r, last) * p.H * kVDim + x) * 2;
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int r = 16 * w + 8 * n + (lane >> 3);
+      off_r[n] = (uint32_t)(min(r, last) * (int)p.q_stride + (((lane & 7) ^ swz128(r)) << 3)) * 2;
+    }
+    off_s = (uint32_t)min(lane, last) * 4;
   };
-  if (nt > 0) load(0);
+  auto tile_begin = [&](int t) { place(min(kBq, Lq - start - t * kBq) - 1); };
+  auto issue = [&](int t, int n, uint32_t at) {
+    const int64_t row0 = start + t * kBq;
+    if (n < 4)
+      dma16_s(qb + row0 * p.q_stride, off_q[n], at + (16 * w + 4 * n) * 256);
+    else if (n < 8)
+      dma16_s(db + row0 * (p.H * kVDim), off_d[n - 4], at + kQNope + kQRope + (16 * w + 4 * (n - 4)) * 256);
+    else if (n < 10)
+      dma16_s(qb + row0 * p.q_stride + kNope, off_r[n - 8], at + kQNope + (16 * w + 8 * (n - 8)) * 128);
+    else
+      dma4_s(stat + row0, off_s, at + kQNope + kQRope + kDo + (w & 1) * kBq * 4);
+  };
   const float c = p.scale * kLog2e;
   operands_loaded();
-
-  for (int t = 0; t < nt; ++t) {
-    attn_wait<0>();
-    attn_barrier();
-    if (t + 1 < nt) load(t + 1);
-    const char* tl = tiles + (t & 1) * kBwdTile;
-    const char* dot = tl + kQNope + kQRope;
-    const float* st = reinterpret_cast<const float*>(dot + kDo);
 #pragma unroll
-    for (int sub = 0; sub < 2; ++sub) {
-      const int qr = start + t * kBq + 32 * sub;          // first query of the 32
-      if (qr >= Lq || (p.causal && qr + 31 + off < key0)) continue;
-      // S and dP of 32 queries (rows) by the wave's 32 keys (columns)
-      f32x16 s = zero16(), dp = zero16();
+  for (int i = 0; i < 2; ++i)
+    if (i < nt) {
+      if (i == 0 || i == nt - 1) tile_begin(i);
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks) s = mfma32(rows256(tl, L, 32 * sub, ks), kf[ks], s);
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) s = mfma32(rows128(tl + kQNope, L, 32 * sub, ks), kf[8 + ks], s);
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks) dp = mfma32(rows256(dot, L, 32 * sub, ks), vf[ks], dp);
-      const bool edge = qr + 32 > Lq || (p.causal && qr + off < key0 + 31);
-#pragma unroll
-      for (int i4 = 0; i4 < 4; ++i4) {
-        const f32x4 ls = *reinterpret_cast<const f32x4*>(st + 32 * sub + 8 * i4 + 4 * L.half);
-        const f32x4 de = *reinterpret_cast<const f32x4*>(st + kBq + 32 * sub + 8 * i4 + 4 * L.half);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int i = 4 * i4 + j, qi = qr + drow(i, L.half);
-          float e = exp2_fast(fmaf(s[i], c, -ls[j] * kLog2e));
-          if (edge && (qi >= Lq || (p.causal && qi + off < key))) e = 0.f;
-          s[i] = e;
-          dp[i] = e * (dp[i] - de[j]);
-        }
-      }
-#pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        const bf16x8 pb = pack8(s, a), sb = pack8(dp, a);
-#pragma unroll
-        for (int d = 0; d < 4; ++d) dv[d] = mfma32(cols256(dot, L, 32 * sub + 16 * a, d), pb, dv[d]);
-#pragma unroll
-        for (int d = 0; d < 4; ++d) dk[d] = mfma32(cols256(tl, L, 32 * sub + 16 * a, d), sb, dk[d]);
-#pragma unroll
-        for (int d = 0; d < 2; ++d) dk[4 + d] = mfma32(cols128(tl + kQNope, L, 32 * sub + 16 * a, d), sb, dk[4 + d]);
-      }
+      for (int n = 0; n < kLoads; ++n) issue(i, n, lds + i * kBwdTile);
     }
+  const int q_at = at256(L), qr_at = kQNope + at128(L), do_at = kQNope + kQRope + at256(L);
+  const int qt_at = at256t(L), qrt_at = kQNope + at128t(L), dot_at = kQNope + kQRope + at256t(L);
+  constexpr int kAhead = 4;
+
+  // S and dP of 32 queries (rows: sub * 32 of the tile at LDS offset `at`) by the wave's keys (columns)
+  auto products = [&](f32x16& s, f32x16& dp, int at, int sub, auto&& between) {
+    const int qa = opaque(q_at + at + sub * 32 * 256), ra = opaque(qr_at + at + sub * 32 * 128),
+              da = opaque(do_at + at + sub * 32 * 256);
+    bf16x8 f[kAhead];
+    auto fetch = [&](int i) {
+      return i < 8 ? get256(tiles, qa, 0, i) : i < 12 ? get128(tiles, ra, 0, i - 8) : get256(tiles, da, 0, i - 12);
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) f[i] = fetch(i);
+    s = zero16();
+    dp = zero16();
+#pragma unroll
+    for (int i = 0; i < 20; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (i < 12)
+        s = mfma32(f[i % kAhead], kf[i], s);
+      else
+        dp = mfma32(f[i % kAhead], vf[i - 12], dp);
+      if (i + kAhead < 20) f[i % kAhead] = fetch(i + kAhead);
+      between(i);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  // Hides what a query must not see, and rows past the last query.
+  auto mask = [&](f32x16& s, int j) {
+    const int qr = start + 32 * j;
+    if (qr + 32 <= Lq && !(p.causal && qr + off < key0 + 31)) return;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int qi = qr + drow(i, L.half);
+      if (qi >= Lq || (p.causal && qi + off < key)) s[i] = neg_inf();
+    }
+  };
+
+  f32x16 s, dp;
+  if (nt > 0) {
+    if (nt > 1)
+      attn_wait<kLoads>();
+    else
+      attn_wait<0>();
+    attn_barrier();
+    products(s, dp, 0, 0, [](int) {});
+    mask(s, 0);
+  }
+  int buf = 0;      // of step j's tile
+  for (int j = 0; j < steps; ++j) {
+    const int sub = j & 1, t = j >> 1, next = buf + 1 == NBUF ? 0 : buf + 1, prev = buf == 0 ? NBUF - 1 : buf - 1;
+    const int at = buf * kBwdTile;
+    bool load = false;
+    if (sub == 1) {      // the next step's tile is in LDS for everyone, and the one before this is free
+      attn_wait<0>();
+      attn_barrier();
+      load = t + 2 < nt;
+      if (t + 2 == nt - 1) tile_begin(nt - 1);
+    }
+    f32x16 sn, dpn;
+    bf16x8 pb[2], sb[2];
+    const float* st = reinterpret_cast<const float*>(tiles + at + kQNope + kQRope + kDo) + 32 * sub + 4 * L.half;
+    f32x4 ls[4], de[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ls[i] = *reinterpret_cast<const f32x4*>(st + 8 * i);
+      de[i] = *reinterpret_cast<const f32x4*>(st + kBq + 8 * i);
+    }
+    auto weigh = [&](int i) {      // element i of the lane's 16
+      const float e = exp2_fast(fmaf(s[i], c, -ls[i >> 2][i & 3]));
+      pb[i >> 3][i & 7] = (__bf16)e;
+      sb[i >> 3][i & 7] = (__bf16)(e * (dp[i] - de[i >> 2][i & 3]));
+    };
+    const int nat = sub ? next * kBwdTile : at;
+    if (j + 1 < steps) {
+      if (load)
+        products(sn, dpn, nat, sub ^ 1, [&](int i) {
+          if (i < 16) weigh(i);
+          if (i * kLoads / 20 != (i + 1) * kLoads / 20) issue(t + 2, i * kLoads / 20, lds + prev * kBwdTile);
+        });
+      else
+        products(sn, dpn, nat, sub ^ 1, [&](int i) {
+          if (i < 16) weigh(i);
+        });
+      mask(sn, j + 1);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) weigh(i);
+    }
+    // dV and dK: D[column drow(i)][key lane%32]
+    const int qt = opaque(qt_at + at + sub * 32 * 256), rt = opaque(qrt_at + at + sub * 32 * 128),
+              dt = opaque(dot_at + at + sub * 32 * 256);
+    bf16x8 f[kAhead];
+    auto fetch = [&](int i) {      // step i: 16 queries i/10; dV columns, dK columns, rotary ones
+      const int a = 16 * (i / 10), k = i % 10;
+      return k < 4 ? get256t(tiles, dt, a, k) : k < 8 ? get256t(tiles, qt, a, k - 4) : get128t(tiles, rt, a, k - 8);
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) f[i] = fetch(i);
+#pragma unroll
+    for (int i = 0; i < 20; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      const int a = i / 10, k = i % 10;
+      if (k < 4)
+        dv[k] = mfma32(f[i % kAhead], pb[a], dv[k]);
+      else
+        dk[k - 4] = mfma32(f[i % kAhead], sb[a], dk[k - 4]);
+      if (i + kAhead < 20) f[i % kAhead] = fetch(i + kAhead);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    s = sn;
+    dp = dpn;
+    if (sub == 1) buf = next;
   }
 
   if (key < Lk) {
@@ -467,12 +574,14 @@ __global__ __launch_bounds__(256, 1) void mla_dkv_kernel(const MlaPrefill p, int
   }
 }
 
-// Gradient of the queries: the forward's loop with dS in place of P, so it
-// needs no sums between workgroups.
-template <int NW>
-__global__ __launch_bounds__(64 * NW, 2) void mla_dq_kernel(const MlaPrefill p, int units) {
-  constexpr int BM = 32 * NW;
-  __shared__ __align__(1024) char tiles[2 * kFwdTile];
+// Gradient of the queries: 4 waves of 32 queries over tiles of 64 keys,
+// staggered by 32 keys as the keys' gradient is; dS needs no sums between
+// workgroups (S and dP are formed a second time instead, 320 of its 512
+// multiplications per query and key, so no result depends on any order).
+__global__ __launch_bounds__(256, 1) void mla_dq_kernel(const MlaPrefill p, int units) {
+  constexpr int NW = 4, BM = 32 * NW, NBUF = 3;
+  using Load = KeyLoader<NW>;
+  __shared__ __align__(1024) char tiles[NBUF * kFwdTile];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int unit, head;
@@ -485,59 +594,158 @@ __global__ __launch_bounds__(64 * NW, 2) void mla_dq_kernel(const MlaPrefill p, 
   const int first = (units - 1 - unit - u.base) * BM;
   const int end = min(first + BM, Lq);
   const int kend = p.causal ? min(Lk, max(end + off, 0)) : Lk;
-  const int nt = (kend + kBn - 1) / kBn;
+  const int steps = (kend + 31) / 32, nt = (steps + 1) / 2;
 
   const TileLane L(lane);
   const int qi = first + 32 * w + L.row, qc = min(qi, Lq - 1);
   const int see = p.causal ? min(Lk, qi + off + 1) : Lk;
   const int wave_all = p.causal ? min(Lk, first + 32 * w + off + 1) : Lk;
-  const int wave_any = p.causal ? min(Lk, first + 32 * w + 32 + off) : Lk;
+  const int wave_any = first + 32 * w >= Lq ? 0 : p.causal ? min(kend, max(first + 32 * w + 32 + off, 0)) : Lk;
+  const int wave_steps = (wave_any + 31) / 32;
 
-  const uint16_t* kv = p.kv + (int64_t)k0 * p.kv_stride + head * (kNope + kVDim);
-  const uint16_t* kr = p.k_rope + (int64_t)k0 * p.rope_stride;
+  const uint16_t* kvt = p.kv + (int64_t)k0 * p.kv_stride + head * (kNope + kVDim);      // of the next tile to load
+  const uint16_t* krt = p.k_rope + (int64_t)k0 * p.rope_stride;
   const uint32_t lds = lds_offset(tiles);
-  if (nt > 0) load_keys<NW>(p, kv, kr, 0, Lk - 1, w, lane, lds);
+  Load ld;
+  ld.place(p, min(Lk, kBn) - 1, w, lane);
+  int loaded = 0;
+  auto loads_begin = [&] {
+    if (loaded > 0 && (loaded + 1) * kBn > Lk) ld.place(p, Lk - 1 - loaded * kBn, w, lane);
+  };
+  auto loads_end = [&] {
+    ++loaded;
+    kvt += (int64_t)kBn * p.kv_stride;
+    krt += (int64_t)kBn * p.rope_stride;
+  };
 
   bf16x8 qf[12], df[8];
   load_operand(qf, p.q + (int64_t)(u.r0 + qc) * p.q_stride + head * kQk, L.half);
   load_operand(df, p.dout + ((int64_t)(u.r0 + qc) * p.H + head) * kVDim, L.half);
-  const float lse = p.lse[(int64_t)head * p.Tq + u.r0 + qc] * kLog2e;
+  const float lse = p.lse2[(int64_t)head * p.Tq + u.r0 + qc];
   const float delta = p.delta[(int64_t)head * p.Tq + u.r0 + qc];
   const float c = p.scale * kLog2e;
   f32x16 dq[6];
 #pragma unroll
   for (int d = 0; d < 6; ++d) dq[d] = zero16();
   operands_loaded();
-
-  for (int t = 0; t < nt; ++t) {
-    attn_wait<0>();
-    attn_barrier();
-    if (t + 1 < nt) load_keys<NW>(p, kv, kr, (t + 1) * kBn, Lk - 1, w, lane, lds + ((t + 1) & 1) * kFwdTile);
-    const char* tl = tiles + (t & 1) * kFwdTile;
-    const char* vt = tl + kNopeTile + kRopeTile;
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      const int key0 = t * kBn + 32 * kb;
-      if (key0 >= wave_any) continue;
-      f32x16 s = scores(tl, L, 32 * kb, qf), dp = zero16();
+  for (int i = 0; i < NBUF - 1; ++i)
+    if (i < nt) {
+      loads_begin();
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks) dp = mfma32(rows256(vt, L, 32 * kb, ks), df[ks], dp);
-      const bool edge = key0 + 32 > wave_all;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float e = exp2_fast(fmaf(s[i], c, -lse));
-        if (edge && key0 + drow(i, L.half) >= see) e = 0.f;
-        dp[i] = e * (dp[i] - delta);
-      }
-#pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        const bf16x8 sb = pack8(dp, a);
-#pragma unroll
-        for (int d = 0; d < 4; ++d) dq[d] = mfma32(cols256(tl, L, 32 * kb + 16 * a, d), sb, dq[d]);
-#pragma unroll
-        for (int d = 0; d < 2; ++d) dq[4 + d] = mfma32(cols128(tl + kNopeTile, L, 32 * kb + 16 * a, d), sb, dq[4 + d]);
-      }
+      for (int n = 0; n < Load::kLoads; ++n) ld.issue(n, kvt, krt, w, lds + i * kFwdTile);
+      loads_end();
     }
+  const int k_at = at256(L), r_at = kNopeTile + at128(L), v_at = kNopeTile + kRopeTile + at256(L);
+  const int kt_at = at256t(L), rt_at = kNopeTile + at128t(L);
+  constexpr int kAhead = 4;
+
+  // S^T and dP^T of 32 keys (rows: sub * 32 of the tile at LDS offset `at`) by the wave's queries (columns)
+  auto products = [&](f32x16& s, f32x16& dp, int at, int sub, auto&& between) {
+    const int ka = opaque(k_at + at + sub * 32 * 256), ra = opaque(r_at + at + sub * 32 * 128),
+              va = opaque(v_at + at + sub * 32 * 256);
+    bf16x8 f[kAhead];
+    auto fetch = [&](int i) {
+      return i < 8 ? get256(tiles, ka, 0, i) : i < 12 ? get128(tiles, ra, 0, i - 8) : get256(tiles, va, 0, i - 12);
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) f[i] = fetch(i);
+    s = zero16();
+    dp = zero16();
+#pragma unroll
+    for (int i = 0; i < 20; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (i < 12)
+        s = mfma32(f[i % kAhead], qf[i], s);
+      else
+        dp = mfma32(f[i % kAhead], df[i - 12], dp);
+      if (i + kAhead < 20) f[i % kAhead] = fetch(i + kAhead);
+      between(i);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto mask = [&](f32x16& s, int j) {
+    if (32 * j + 32 <= wave_all) return;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (32 * j + drow(i, L.half) >= see) s[i] = neg_inf();
+  };
+
+  f32x16 s, dp;
+  if (nt > 0) {
+    if (nt > 1)
+      attn_wait<Load::kLoads>();
+    else
+      attn_wait<0>();
+    attn_barrier();
+    if (wave_steps > 0) {
+      products(s, dp, 0, 0, [](int) {});
+      mask(s, 0);
+    }
+  }
+  int buf = 0;      // of step j's tile
+  for (int j = 0; j < steps; ++j) {
+    const int sub = j & 1, next = buf + 1 == NBUF ? 0 : buf + 1, prev = buf == 0 ? NBUF - 1 : buf - 1;
+    const int at = buf * kFwdTile;
+    bool load = false;
+    if (sub == 1) {      // the next step's tile is in LDS for everyone, and the one before this is free
+      attn_wait<0>();
+      attn_barrier();
+      load = loaded < nt;
+      if (load) loads_begin();
+    }
+    auto issue = [&](int n) { ld.issue(n, kvt, krt, w, lds + prev * kFwdTile); };
+    if (j < wave_steps) {
+      f32x16 sn, dpn;
+      bf16x8 sb[2];
+      auto weigh = [&](int i) {      // element i of the lane's 16
+        sb[i >> 3][i & 7] = (__bf16)(exp2_fast(fmaf(s[i], c, -lse)) * (dp[i] - delta));
+      };
+      const int nat = sub ? next * kFwdTile : at;
+      const bool more = j + 1 < wave_steps;
+      if (more && load)
+        products(sn, dpn, nat, sub ^ 1, [&](int i) {
+          if (i < 16) weigh(i);
+          if (i * Load::kLoads / 20 != (i + 1) * Load::kLoads / 20) issue(i * Load::kLoads / 20);
+        });
+      else {
+        if (load) {
+#pragma unroll
+          for (int n = 0; n < Load::kLoads; ++n) issue(n);
+        }
+        if (more)
+          products(sn, dpn, nat, sub ^ 1, [&](int i) {
+            if (i < 16) weigh(i);
+          });
+        else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) weigh(i);
+        }
+      }
+      if (more) mask(sn, j + 1);
+      const int ka = opaque(kt_at + at + sub * 32 * 256), ra = opaque(rt_at + at + sub * 32 * 128);
+      bf16x8 f[kAhead];
+      auto fetch = [&](int i) {      // step i: 16 keys i/6, column block i%6
+        const int a = 16 * (i / 6), k = i % 6;
+        return k < 4 ? get256t(tiles, ka, a, k) : get128t(tiles, ra, a, k - 4);
+      };
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) f[i] = fetch(i);
+#pragma unroll
+      for (int i = 0; i < 12; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
+        dq[i % 6] = mfma32(f[i % kAhead], sb[i / 6], dq[i % 6]);
+        if (i + kAhead < 12) f[i % kAhead] = fetch(i + kAhead);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      s = sn;
+      dp = dpn;
+    } else if (load) {      // nothing here for this wave: only its share of the loads
+#pragma unroll
+      for (int n = 0; n < Load::kLoads; ++n) issue(n);
+    }
+    if (load) loads_end();
+    if (sub == 1) buf = next;
   }
   if (qi < Lq) {
     uint16_t* op = p.dq + ((int64_t)(u.r0 + qi) * p.H + head) * kQk + 4 * L.half;
@@ -584,7 +792,7 @@ hipError_t launch_mla_prefill_bwd(const MlaPrefill& p, hipStream_t stream) {
   if (p.Tq > 0) {
     hipLaunchKernelGGL(mla_delta_kernel, dim3((unsigned)((rows + 15) / 16)), dim3(256), 0, stream, p);
     const int64_t units = blocks(p.Tq, p.B, 128);
-    hipLaunchKernelGGL(mla_dq_kernel<4>, dim3(unit_grid(units, p.H)), dim3(256), 0, stream, p, (int)units);
+    hipLaunchKernelGGL(mla_dq_kernel, dim3(unit_grid(units, p.H)), dim3(256), 0, stream, p, (int)units);
   }
   if (p.Tk > 0) {
     const int64_t units = blocks(p.Tk, p.B, 128);

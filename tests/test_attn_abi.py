@@ -72,7 +72,7 @@ def test_prefill_bwd_refusals(L):
         assert call(**{name: P + 8}) == -3, name
     assert call(scale=0.0) == -9 and call(H=0) == -2
     ws = L.fp8bs_mla_prefill_bwd_workspace_bytes
-    assert ws(10, 12, 2) == 256 + 12 * 2 * 64 * 4 and ws(-1, 2, 2) == -2 and ws(4, 4, 0) == -2
+    assert ws(10, 12, 2) == 2 * 256 + 12 * 2 * 64 * 4 and ws(-1, 2, 2) == -2 and ws(4, 4, 0) == -2
 
 
 def _decode(L, shared=False, **kw):
