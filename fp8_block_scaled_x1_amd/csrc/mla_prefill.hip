@@ -343,21 +343,33 @@ __global__ __launch_bounds__(256) void mla_delta_kernel(const MlaPrefill p) {
   }
 }
 
-// Gradients of keys and values: 4 waves of 32 keys each, whose dK and dV stay
-// in registers (160 a lane, next to 80 of the keys and values themselves: one
-// wave per SIMD) while 32 queries at a time pass, in tiles of 64 (Q, dO, lse,
-// D) of which one is used and two are on their way. Staggered by one step: the
-// scores and dP of the next 32 queries are formed while the weights and dS of
-// these are, then dK and dV take these.
+// Gradients of keys and values: 32 keys are a pair of waves' work, which share
+// a SIMD, while 32 queries at a time pass, in tiles of 64 (Q, dO, lse, D). The
+// first of the pair forms the scores and the weights, hands the weights (FP32)
+// to the second through LDS and adds up dV; the second, a step behind, forms dP
+// and dS and adds up dK: 20 products of 32x32x16 each, none formed twice, and
+// no more than 48 + 64 (32 + 96) registers of operands and sums, so both fit
+// in 256 and one's vector work runs beside the other's products. (One wave for
+// both needs 240 for operands and sums alone; alone on its SIMD, with the rest
+// in accumulation registers, it took 20-60% longer.)
+template <int N>
+struct Const {
+  static constexpr int value = N;
+};
+
 constexpr int kBq = 64;
 constexpr int kQNope = kBq * 256, kQRope = kBq * 128, kDo = kBq * 256;
 constexpr int kBwdTile = kQNope + kQRope + kDo + 2 * kBq * 4;
 
-__global__ __launch_bounds__(256, 1) void mla_dkv_kernel(const MlaPrefill p, int units) {
-  constexpr int NW = 4, BK = 32 * NW, NBUF = 3, kLoads = 4 + 2 + 4 + 1;
-  __shared__ __align__(1024) char tiles[NBUF * kBwdTile];
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void mla_dkv_kernel(const MlaPrefill p,
+                                                                                            int units) {
+  constexpr int BK = 128, NBUF = 3, kLoads = 2 + 2 + 1 + 1, kAhead = 6;
+  constexpr int kWeights = 32 * 32 * 4;      // a pair's, of one step
+  __shared__ __align__(1024) char lds_mem[NBUF * kBwdTile + 2 * 4 * kWeights];
+  char* const tiles = lds_mem;
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int pair = w & 3;
   int unit, head;
   if (!unit_of(units, p.H, unit, head)) return;
   const ExpertSlot u = locate_expert(p.cu_k, p.B, p.Tk, unit, BK, 1);
@@ -366,209 +378,215 @@ __global__ __launch_bounds__(256, 1) void mla_dkv_kernel(const MlaPrefill p, int
   const int q1 = __builtin_amdgcn_readfirstlane(min(max(p.cu_q[u.e + 1], q0), p.Tq));
   const int Lk = u.r1 - u.r0, Lq = q1 - q0, off = Lk - Lq;
   const int kb0 = (unit - u.base) * BK;
-  const int key0 = kb0 + 32 * w;
+  const int key0 = kb0 + 32 * pair;
   const int start = p.causal ? max(0, kb0 - off) : 0;        // first query that sees the block's first key
   const int steps = Lq > start ? (Lq - start + 31) / 32 : 0, nt = (steps + 1) / 2;
 
   const TileLane L(lane);
   const int key = key0 + L.row, kc = min(key, Lk - 1);
-  bf16x8 kf[12], vf[8];
-  {
-    const uint16_t* row = p.kv + (int64_t)(u.r0 + kc) * p.kv_stride + head * (kNope + kVDim);
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks) kf[ks] = *reinterpret_cast<const bf16x8*>(row + 16 * ks + 8 * L.half);
-    load_operand(vf, row + kNope, L.half);
-    const uint16_t* rr = p.k_rope + (int64_t)(u.r0 + kc) * p.rope_stride;
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) kf[8 + ks] = *reinterpret_cast<const bf16x8*>(rr + 16 * ks + 8 * L.half);
-  }
-  f32x16 dk[6], dv[4];
-#pragma unroll
-  for (int d = 0; d < 6; ++d) dk[d] = zero16();
-#pragma unroll
-  for (int d = 0; d < 4; ++d) dv[d] = zero16();
-
   const uint16_t* qb = p.q + (int64_t)q0 * p.q_stride + head * kQk;
   const uint16_t* db = p.dout + ((int64_t)q0 * p.H + head) * kVDim;
-  const float* stat = (w & 1 ? p.delta : p.lse2) + (int64_t)head * p.Tq + q0;      // (twice each, alike)
+  const float* stat = (w & 1 ? p.delta : p.lse2) + (int64_t)head * p.Tq + q0;      // (four times each, alike)
   const uint32_t lds = lds_offset(tiles);
   // A tile's loads: offsets from its first query in registers, clamped to the
   // last query where the tile has fewer than 64.
-  uint32_t off_q[4], off_d[4], off_r[2], off_s;
+  uint32_t off_q[2], off_d[2], off_r, off_s;
   auto place = [&](int last) {
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      const int r = 16 * w + 4 * n + (lane >> 4), x = ((lane & 15) ^ swz256(r)) << 3;
+    for (int n = 0; n < 2; ++n) {
+      const int r = 8 * w + 4 * n + (lane >> 4), x = ((lane & 15) ^ swz256(r)) << 3;
       off_q[n] = (uint32_t)(min(r, last) * (int)p.q_stride + x) * 2;
       off_d[n] = (uint32_t)(min(r, last) * p.H * kVDim + x) * 2;
     }
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const int r = 16 * w + 8 * n + (lane >> 3);
-      off_r[n] = (uint32_t)(min(r, last) * (int)p.q_stride + (((lane & 7) ^ swz128(r)) << 3)) * 2;
-    }
+    const int r = 8 * w + (lane >> 3);
+    off_r = (uint32_t)(min(r, last) * (int)p.q_stride + (((lane & 7) ^ swz128(r)) << 3)) * 2;
     off_s = (uint32_t)min(lane, last) * 4;
   };
-  auto tile_begin = [&](int t) { place(min(kBq, Lq - start - t * kBq) - 1); };
   auto issue = [&](int t, int n, uint32_t at) {
     const int64_t row0 = start + t * kBq;
-    if (n < 4)
-      dma16_s(qb + row0 * p.q_stride, off_q[n], at + (16 * w + 4 * n) * 256);
-    else if (n < 8)
-      dma16_s(db + row0 * (p.H * kVDim), off_d[n - 4], at + kQNope + kQRope + (16 * w + 4 * (n - 4)) * 256);
-    else if (n < 10)
-      dma16_s(qb + row0 * p.q_stride + kNope, off_r[n - 8], at + kQNope + (16 * w + 8 * (n - 8)) * 128);
+    const auto uniform = [](uint32_t x) { return (uint32_t)__builtin_amdgcn_readfirstlane(x); };
+    if (n < 2)
+      dma16_s(qb + row0 * p.q_stride, off_q[n], uniform(at + (8 * w + 4 * n) * 256));
+    else if (n < 4)
+      dma16_s(db + row0 * (p.H * kVDim), off_d[n - 2], uniform(at + kQNope + kQRope + (8 * w + 4 * (n - 2)) * 256));
+    else if (n == 4)
+      dma16_s(qb + row0 * p.q_stride + kNope, off_r, uniform(at + kQNope + 8 * w * 128));
     else
-      dma4_s(stat + row0, off_s, at + kQNope + kQRope + kDo + (w & 1) * kBq * 4);
+      dma4_s(stat + row0, off_s, uniform(at + kQNope + kQRope + kDo + (w & 1) * kBq * 4));
+  };
+  auto load_tile = [&](int t) {
+    const uint32_t to = lds + t % NBUF * kBwdTile;
+    if (t == 0 || t == nt - 1) place(min(kBq, Lq - start - t * kBq) - 1);
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) issue(t, n, to);
   };
   const float c = p.scale * kLog2e;
-  operands_loaded();
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (i < nt) {
-      if (i == 0 || i == nt - 1) tile_begin(i);
-#pragma unroll
-      for (int n = 0; n < kLoads; ++n) issue(i, n, lds + i * kBwdTile);
-    }
-  const int q_at = at256(L), qr_at = kQNope + at128(L), do_at = kQNope + kQRope + at256(L);
-  const int qt_at = at256t(L), qrt_at = kQNope + at128t(L), dot_at = kQNope + kQRope + at256t(L);
-  constexpr int kAhead = 4;
+  const uint16_t* krow = p.kv + (int64_t)(u.r0 + kc) * p.kv_stride + head * (kNope + kVDim);
+  // the pair's weights of steps j and j + 1: [register quad][lane]
+  char* const hand = lds_mem + NBUF * kBwdTile + pair * kWeights + 16 * lane;
 
-  // S and dP of 32 queries (rows: sub * 32 of the tile at LDS offset `at`) by the wave's keys (columns)
-  auto products = [&](f32x16& s, f32x16& dp, int at, int sub, auto&& between) {
-    const int qa = opaque(q_at + at + sub * 32 * 256), ra = opaque(qr_at + at + sub * 32 * 128),
-              da = opaque(do_at + at + sub * 32 * 256);
-    bf16x8 f[kAhead];
-    auto fetch = [&](int i) {
-      return i < 8 ? get256(tiles, qa, 0, i) : i < 12 ? get128(tiles, ra, 0, i - 8) : get256(tiles, da, 0, i - 12);
-    };
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) f[i] = fetch(i);
-    s = zero16();
-    dp = zero16();
-#pragma unroll
-    for (int i = 0; i < 20; ++i) {
-      __builtin_amdgcn_sched_barrier(0);
-      if (i < 12)
-        s = mfma32(f[i % kAhead], kf[i], s);
-      else
-        dp = mfma32(f[i % kAhead], vf[i - 12], dp);
-      if (i + kAhead < 20) f[i % kAhead] = fetch(i + kAhead);
-      between(i);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-  };
-
-  // Hides what a query must not see, and rows past the last query.
-  auto mask = [&](f32x16& s, int j) {
-    const int qr = start + 32 * j;
-    if (qr + 32 <= Lq && !(p.causal && qr + off < key0 + 31)) return;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int qi = qr + drow(i, L.half);
-      if (qi >= Lq || (p.causal && qi + off < key)) s[i] = neg_inf();
-    }
-  };
-
-  f32x16 s, dp;
-  if (nt > 0) {
-    if (nt > 1)
-      attn_wait<kLoads>();
-    else
-      attn_wait<0>();
+  // Step j of the loop belongs to the first wave's queries 32 j .. and the
+  // second's 32 (j - 1) ..; one barrier each. Even steps begin a tile t = j / 2:
+  // it was loaded before, tile t - 2 is free since both are past it.
+  auto meet = [&](int j) {
+    if (!(j & 1)) attn_wait<0>();
     attn_barrier();
-    products(s, dp, 0, 0, [](int) {});
-    mask(s, 0);
-  }
-  int buf = 0;      // of step j's tile
-  for (int j = 0; j < steps; ++j) {
-    const int sub = j & 1, t = j >> 1, next = buf + 1 == NBUF ? 0 : buf + 1, prev = buf == 0 ? NBUF - 1 : buf - 1;
-    const int at = buf * kBwdTile;
-    bool load = false;
-    if (sub == 1) {      // the next step's tile is in LDS for everyone, and the one before this is free
-      attn_wait<0>();
-      attn_barrier();
-      load = t + 2 < nt;
-      if (t + 2 == nt - 1) tile_begin(nt - 1);
-    }
-    f32x16 sn, dpn;
-    bf16x8 pb[2], sb[2];
-    const float* st = reinterpret_cast<const float*>(tiles + at + kQNope + kQRope + kDo) + 32 * sub + 4 * L.half;
-    f32x4 ls[4], de[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      ls[i] = *reinterpret_cast<const f32x4*>(st + 8 * i);
-      de[i] = *reinterpret_cast<const f32x4*>(st + kBq + 8 * i);
-    }
-    auto weigh = [&](int i) {      // element i of the lane's 16
-      const float e = exp2_fast(fmaf(s[i], c, -ls[i >> 2][i & 3]));
-      pb[i >> 3][i & 7] = (__bf16)e;
-      sb[i >> 3][i & 7] = (__bf16)(e * (dp[i] - de[i >> 2][i & 3]));
-    };
-    const int nat = sub ? next * kBwdTile : at;
-    if (j + 1 < steps) {
-      if (load)
-        products(sn, dpn, nat, sub ^ 1, [&](int i) {
-          if (i < 16) weigh(i);
-          if (i * kLoads / 20 != (i + 1) * kLoads / 20) issue(t + 2, i * kLoads / 20, lds + prev * kBwdTile);
-        });
-      else
-        products(sn, dpn, nat, sub ^ 1, [&](int i) {
-          if (i < 16) weigh(i);
-        });
-      mask(sn, j + 1);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) weigh(i);
-    }
-    // dV and dK: D[column drow(i)][key lane%32]
-    const int qt = opaque(qt_at + at + sub * 32 * 256), rt = opaque(qrt_at + at + sub * 32 * 128),
-              dt = opaque(dot_at + at + sub * 32 * 256);
-    bf16x8 f[kAhead];
-    auto fetch = [&](int i) {      // step i: 16 queries i/10; dV columns, dK columns, rotary ones
-      const int a = 16 * (i / 10), k = i % 10;
-      return k < 4 ? get256t(tiles, dt, a, k) : k < 8 ? get256t(tiles, qt, a, k - 4) : get128t(tiles, rt, a, k - 8);
-    };
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) f[i] = fetch(i);
-#pragma unroll
-    for (int i = 0; i < 20; ++i) {
-      __builtin_amdgcn_sched_barrier(0);
-      const int a = i / 10, k = i % 10;
-      if (k < 4)
-        dv[k] = mfma32(f[i % kAhead], pb[a], dv[k]);
-      else
-        dk[k - 4] = mfma32(f[i % kAhead], sb[a], dk[k - 4]);
-      if (i + kAhead < 20) f[i % kAhead] = fetch(i + kAhead);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    s = sn;
-    dp = dpn;
-    if (sub == 1) buf = next;
-  }
+    if (!(j & 1) && (j >> 1) + 1 < nt) load_tile((j >> 1) + 1);
+  };
 
-  if (key < Lk) {
-    uint16_t* out = p.dkv + ((int64_t)(u.r0 + key) * p.H + head) * (kNope + kVDim) + 4 * L.half;
-    float* rp = p.rope_part + ((int64_t)head * p.Tk + u.r0 + key) * kRopeDim + 4 * L.half;
+  if (w < 4) {      // scores, weights, dV
+    bf16x8 kf[12];
+    const uint16_t* rr = p.k_rope + (int64_t)(u.r0 + kc) * p.rope_stride;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int ks = 0; ks < 8; ++ks) kf[ks] = *reinterpret_cast<const bf16x8*>(krow + 16 * ks + 8 * L.half);
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        bf16x4 a, b;
+    for (int ks = 0; ks < 4; ++ks) kf[8 + ks] = *reinterpret_cast<const bf16x8*>(rr + 16 * ks + 8 * L.half);
+    f32x16 dv[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          a[j] = (__bf16)(dk[d][4 * i + j] * p.scale);
-          b[j] = (__bf16)dv[d][4 * i + j];
+    for (int d = 0; d < 4; ++d) dv[d] = zero16();
+    operands_loaded();
+    if (nt > 0) load_tile(0);
+    const int q_at = at256(L), r_at = kQNope + at128(L), dt_at = kQNope + kQRope + at256t(L);
+    const int q_first = p.causal ? key - off : -1, q_all = p.causal ? key0 + 31 - off : -1;
+    for (int j = 0; j <= steps; ++j) {
+      meet(j);
+      if (j == steps) break;      // the second wave's last step
+      const int at = (j >> 1) % NBUF * kBwdTile, qr = start + 32 * j;
+      const int qa = opaque(q_at + at + (j & 1) * 32 * 256), ra = opaque(r_at + at + (j & 1) * 32 * 128),
+                da = opaque(dt_at + at + (j & 1) * 32 * 256);
+      bf16x8 f[kAhead];
+      f32x16 s = zero16();
+      {
+        auto fetch = [&](int i) { return i < 8 ? get256(tiles, qa, 0, i) : get128(tiles, ra, 0, i - 8); };
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) f[i] = fetch(i);
+#pragma unroll
+        for (int i = 0; i < 12; ++i) {
+          __builtin_amdgcn_sched_barrier(0);
+          s = mfma32(f[i % kAhead], kf[i], s);
+          if (i + kAhead < 12) f[i % kAhead] = fetch(i + kAhead);
         }
-        *reinterpret_cast<bf16x4*>(out + 32 * d + 8 * i) = a;
-        *reinterpret_cast<bf16x4*>(out + kNope + 32 * d + 8 * i) = b;
+        __builtin_amdgcn_sched_barrier(0);
       }
+      const float* st = reinterpret_cast<const float*>(tiles + at + kQNope + kQRope + kDo) + 32 * (j & 1) + 4 * L.half;
+      f32x4 ls[4];
 #pragma unroll
-      for (int d = 0; d < 2; ++d) {
-        f32x4 v;
+      for (int i = 0; i < 4; ++i) ls[i] = *reinterpret_cast<const f32x4*>(st + 8 * i);
+      auto fetch = [&](int i) { return get256t(tiles, da, 16 * (i >> 2), i & 3); };
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = dk[4 + d][4 * i + j] * p.scale;
-        *reinterpret_cast<f32x4*>(rp + 32 * d + 8 * i) = v;
+      for (int i = 0; i < kAhead; ++i) f[i] = fetch(i);
+      if (qr + 32 > Lq || qr < q_all) {      // hide the key from queries that must not see it, and rows past the last
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int qi = qr + drow(i, L.half);
+          s[i] = (qi < q_first) | (qi >= Lq) ? neg_inf() : s[i];
+        }
+      }
+      char* const to = hand + (j & 1) * 4 * kWeights;
+#pragma unroll
+      for (int i4 = 0; i4 < 4; ++i4) {
+        f32x4 e;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          e[k] = exp2_fast(fmaf(s[4 * i4 + k], c, -ls[i4][k]));
+          s[4 * i4 + k] = e[k];
+        }
+        *reinterpret_cast<f32x4*>(to + 1024 * i4) = e;
+      }
+      const bf16x8 pb[2] = {pack8(s, 0), pack8(s, 1)};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {      // D[column drow(i)][key lane%32]
+        __builtin_amdgcn_sched_barrier(0);
+        dv[i & 3] = mfma32(f[i % kAhead], pb[i >> 2], dv[i & 3]);
+        if (i + kAhead < 8) f[i % kAhead] = fetch(i + kAhead);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (key < Lk) {
+      uint16_t* out = p.dkv + ((int64_t)(u.r0 + key) * p.H + head) * (kNope + kVDim) + kNope + 4 * L.half;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          bf16x4 b;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) b[k] = (__bf16)dv[d][4 * i + k];
+          *reinterpret_cast<bf16x4*>(out + 32 * d + 8 * i) = b;
+        }
+    }
+  } else {      // dP, dS, dK
+    bf16x8 vf[8];
+    load_operand(vf, krow + kNope, L.half);
+    f32x16 dk[6];
+#pragma unroll
+    for (int d = 0; d < 6; ++d) dk[d] = zero16();
+    operands_loaded();
+    if (nt > 0) load_tile(0);
+    const int d_at = kQNope + kQRope + at256(L), qt_at = at256t(L), rt_at = kQNope + at128t(L);
+    for (int j = 0; j <= steps; ++j) {
+      meet(j);
+      if (j == 0) continue;      // the first wave's first step
+      const int k = j - 1, at = (k >> 1) % NBUF * kBwdTile;
+      const int da = opaque(d_at + at + (k & 1) * 32 * 256), qa = opaque(qt_at + at + (k & 1) * 32 * 256),
+                ra = opaque(rt_at + at + (k & 1) * 32 * 128);
+      bf16x8 f[kAhead];
+      f32x16 dp = zero16();
+      {
+        auto fetch = [&](int i) { return get256(tiles, da, 0, i); };
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) f[i] = fetch(i);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          __builtin_amdgcn_sched_barrier(0);
+          dp = mfma32(f[i % kAhead], vf[i], dp);
+          if (i + kAhead < 8) f[i % kAhead] = fetch(i + kAhead);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      const float* st = reinterpret_cast<const float*>(tiles + at + kQNope + kQRope + kDo) + kBq + 32 * (k & 1) + 4 * L.half;
+      const char* from = hand + (k & 1) * 4 * kWeights;
+      f32x4 e[4], de[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        e[i] = *reinterpret_cast<const f32x4*>(from + 1024 * i);
+        de[i] = *reinterpret_cast<const f32x4*>(st + 8 * i);
+      }
+      auto fetch = [&](int i) {      // step i: 16 queries i/6, column block i%6
+        const int a = 16 * (i / 6), d = i % 6;
+        return d < 4 ? get256t(tiles, qa, a, d) : get128t(tiles, ra, a, d - 4);
+      };
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) f[i] = fetch(i);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) dp[i] = e[i >> 2][i & 3] * (dp[i] - de[i >> 2][i & 3]);
+      const bf16x8 sb[2] = {pack8(dp, 0), pack8(dp, 1)};
+#pragma unroll
+      for (int i = 0; i < 12; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
+        dk[i % 6] = mfma32(f[i % kAhead], sb[i / 6], dk[i % 6]);
+        if (i + kAhead < 12) f[i % kAhead] = fetch(i + kAhead);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (key < Lk) {
+      uint16_t* out = p.dkv + ((int64_t)(u.r0 + key) * p.H + head) * (kNope + kVDim) + 4 * L.half;
+      float* rp = p.rope_part + ((int64_t)head * p.Tk + u.r0 + key) * kRopeDim + 4 * L.half;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          bf16x4 b;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) b[x] = (__bf16)(dk[d][4 * i + x] * p.scale);
+          *reinterpret_cast<bf16x4*>(out + 32 * d + 8 * i) = b;
+        }
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          f32x4 v;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) v[x] = dk[4 + d][4 * i + x] * p.scale;
+          *reinterpret_cast<f32x4*>(rp + 32 * d + 8 * i) = v;
+        }
       }
     }
   }
@@ -671,7 +689,7 @@ __global__ __launch_bounds__(256, 1) void mla_dq_kernel(const MlaPrefill p, int 
       if (32 * j + drow(i, L.half) >= see) s[i] = neg_inf();
   };
 
-  f32x16 s, dp;
+  f32x16 s0, dp0, s1, dp1;
   if (nt > 0) {
     if (nt > 1)
       attn_wait<Load::kLoads>();
@@ -679,16 +697,18 @@ __global__ __launch_bounds__(256, 1) void mla_dq_kernel(const MlaPrefill p, int 
       attn_wait<0>();
     attn_barrier();
     if (wave_steps > 0) {
-      products(s, dp, 0, 0, [](int) {});
-      mask(s, 0);
+      products(s0, dp0, 0, 0, [](int) {});
+      mask(s0, 0);
     }
   }
-  int buf = 0;      // of step j's tile
-  for (int j = 0; j < steps; ++j) {
-    const int sub = j & 1, next = buf + 1 == NBUF ? 0 : buf + 1, prev = buf == 0 ? NBUF - 1 : buf - 1;
+  int buf = 0;      // of the steps' tile
+  // Step j, half `sub` of its tile, whose scores and dP are in s and dp; those of step j+1 go to sn and dpn.
+  auto step = [&](int j, auto half, f32x16& s, f32x16& dp, f32x16& sn, f32x16& dpn) {
+    constexpr int sub = decltype(half)::value;
+    const int next = buf + 1 == NBUF ? 0 : buf + 1, prev = buf == 0 ? NBUF - 1 : buf - 1;
     const int at = buf * kFwdTile;
     bool load = false;
-    if (sub == 1) {      // the next step's tile is in LDS for everyone, and the one before this is free
+    if constexpr (sub == 1) {      // the next step's tile is in LDS for everyone, and the one before this is free
       attn_wait<0>();
       attn_barrier();
       load = loaded < nt;
@@ -696,7 +716,6 @@ __global__ __launch_bounds__(256, 1) void mla_dq_kernel(const MlaPrefill p, int 
     }
     auto issue = [&](int n) { ld.issue(n, kvt, krt, w, lds + prev * kFwdTile); };
     if (j < wave_steps) {
-      f32x16 sn, dpn;
       bf16x8 sb[2];
       auto weigh = [&](int i) {      // element i of the lane's 16
         sb[i >> 3][i & 7] = (__bf16)(exp2_fast(fmaf(s[i], c, -lse)) * (dp[i] - delta));
@@ -738,14 +757,16 @@ __global__ __launch_bounds__(256, 1) void mla_dq_kernel(const MlaPrefill p, int 
         if (i + kAhead < 12) f[i % kAhead] = fetch(i + kAhead);
       }
       __builtin_amdgcn_sched_barrier(0);
-      s = sn;
-      dp = dpn;
     } else if (load) {      // nothing here for this wave: only its share of the loads
 #pragma unroll
       for (int n = 0; n < Load::kLoads; ++n) issue(n);
     }
     if (load) loads_end();
-    if (sub == 1) buf = next;
+    if constexpr (sub == 1) buf = next;
+  };
+  for (int j = 0; j < steps; j += 2) {
+    step(j, Const<0>{}, s0, dp0, s1, dp1);
+    if (j + 1 < steps) step(j + 1, Const<1>{}, s1, dp1, s0, dp0);
   }
   if (qi < Lq) {
     uint16_t* op = p.dq + ((int64_t)(u.r0 + qi) * p.H + head) * kQk + 4 * L.half;
@@ -796,7 +817,7 @@ hipError_t launch_mla_prefill_bwd(const MlaPrefill& p, hipStream_t stream) {
   }
   if (p.Tk > 0) {
     const int64_t units = blocks(p.Tk, p.B, 128);
-    hipLaunchKernelGGL(mla_dkv_kernel, dim3(unit_grid(units, p.H)), dim3(256), 0, stream, p, (int)units);
+    hipLaunchKernelGGL(mla_dkv_kernel, dim3(unit_grid(units, p.H)), dim3(512), 0, stream, p, (int)units);
     hipLaunchKernelGGL(mla_rope_sum_kernel, dim3((unsigned)(((int64_t)p.Tk * kRopeDim / 4 + 255) / 256)), dim3(256), 0,
                        stream, p);
   }
