@@ -7,11 +7,11 @@ library on the current torch stream of the inputs' device.
 """
 
 import ctypes
+import functools
 
 import torch
 
 from . import _lib
-from ._lib import _check, _dev, _in_dtype, _stream
 
 ATTN_VERSION = 1
 CACHE_BF16, CACHE_FP8 = 0, 1
@@ -50,61 +50,94 @@ def attn_lib():
     return _attn
 
 
-_BF16, _F32, _I32, _U8 = (torch.bfloat16,), (torch.float32,), (torch.int32,), (torch.uint8,)
+_bf16, _f32, _i32, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
-def _want(t, name, shape):
+def _ptr(t, name, dtype, shape, device):
+    """The address of a contiguous tensor of this dtype, shape and device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _same_device(**tensors):
-    devs = {t.device for t in tensors.values() if t is not None}
-    if len(devs) > 1:
-        raise ValueError(f"{', '.join(tensors)} are on different devices")
+def _on_gpu(t, name, dims):
+    """The device of the tensor that the call goes by, after its first checks."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dim() != len(dims) or any(d is not None and d != n for d, n in zip(dims, t.shape)):
+        raise ValueError(f"{name} must be [{']['.join('*' if d is None else str(d) for d in dims)}], got {tuple(t.shape)}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a GPU (got {t.device})")
+    return t.device
 
 
-def _tokens(t, name, inner):
+def _tokens(t, name, inner, device):
     """(pointer, numbers from token to token) of a BF16 tensor [T][inner...]
     whose tokens are contiguous inside but may lie apart."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if tuple(t.shape[1:]) != tuple(inner) or t.dim() != 1 + len(inner):
+    if t.shape[1:] != inner:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (tokens, {', '.join(map(str, inner))})")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must be on a GPU (got {t.device})")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected torch.bfloat16")
+    if t.dtype != _bf16:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {_bf16}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
     n = 1
-    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+    for size, stride in zip(reversed(inner), reversed(t.stride()[1:])):
         if size != 1 and stride != n:
             raise ValueError(f"{name}: the numbers of a token must be contiguous")
         n *= size
     return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else n
 
 
-def _workspace(nbytes, fn, device):
-    _check(fn, min(0, nbytes))
-    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+def _call(fn, device, *args):
+    """Calls the entry point on the device's current stream, with the device current."""
+    entry = getattr(attn_lib(), fn)
+    if device.index == torch.cuda.current_device():
+        status = entry(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = entry(*args, torch.cuda.current_stream(device).cuda_stream)
+    if status != 0:
+        raise _lib.Fp8bsError(fn, status)
+
+
+@functools.lru_cache(maxsize=4096)
+def _bytes(fn, device_index, *sizes):
+    """What a *_workspace_bytes function says of these sizes (on this device)."""
+    with torch.cuda.device(device_index):
+        n = getattr(attn_lib(), fn)(*sizes)
+    if n < 0:
+        raise _lib.Fp8bsError(fn, n)
+    return max(n, 16)
+
+
+def _workspace(fn, device, *sizes):
+    return torch.empty(_bytes(fn, device.index, *sizes), dtype=_u8, device=device)
 
 
 def _prefill_args(q, kv, k_rope, cu_q, cu_k):
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be [Tq][H][192]")
+    device = _on_gpu(q, "q", (None, None, 192))
     H = q.shape[1]
-    pq, sq = _tokens(q, "q", (H, 192))
-    pkv, skv = _tokens(kv, "kv", (H, 256))
-    pr, sr = _tokens(k_rope, "k_rope", (64,))
+    pq, sq = _tokens(q, "q", (H, 192), device)
+    pkv, skv = _tokens(kv, "kv", (H, 256), device)
+    pr, sr = _tokens(k_rope, "k_rope", (64,), device)
     if k_rope.shape[0] != kv.shape[0]:
         raise ValueError("kv and k_rope disagree on the number of tokens")
     if not isinstance(cu_q, torch.Tensor) or cu_q.dim() != 1 or cu_q.shape[0] < 1:
         raise ValueError("cu_q must have B+1 entries")
-    _want(cu_k, "cu_k", cu_q.shape)
-    _same_device(q=q, kv=kv, k_rope=k_rope, cu_q=cu_q, cu_k=cu_k)
-    return (pq, sq, pkv, skv, pr, sr), (_dev(cu_q, "cu_q", _I32), _dev(cu_k, "cu_k", _I32), cu_q.shape[0] - 1,
-                                        q.shape[0], kv.shape[0], H)
+    off = cu_q.shape
+    return device, (pq, sq, pkv, skv, pr, sr), (_ptr(cu_q, "cu_q", _i32, off, device),
+                                                _ptr(cu_k, "cu_k", _i32, off, device), off[0] - 1, q.shape[0],
+                                                kv.shape[0], H)
 
 
 def fp8bs_mla_prefill(q, kv, k_rope, cu_q, cu_k, scale, causal=True):
@@ -112,40 +145,32 @@ def fp8bs_mla_prefill(q, kv, k_rope, cu_q, cu_k, scale, causal=True):
     [Tk][H][256] (keys then values of each head), k_rope [Tk][64], all BF16 and
     possibly with gaps between tokens; cu_q, cu_k int32 [B+1] on the GPU.
     Returns (out bf16 [Tq][H][128], lse f32 [H][Tq])."""
-    ptrs, sizes = _prefill_args(q, kv, k_rope, cu_q, cu_k)
+    device, ptrs, sizes = _prefill_args(q, kv, k_rope, cu_q, cu_k)
     Tq, H = q.shape[:2]
-    out = torch.empty((Tq, H, 128), dtype=torch.bfloat16, device=q.device)
-    lse = torch.empty((H, Tq), dtype=torch.float32, device=q.device)
-    with torch.cuda.device(q.device):
-        _check("fp8bs_mla_prefill", attn_lib().fp8bs_mla_prefill(*ptrs, *sizes, float(scale), int(bool(causal)),
-                                                                 out.data_ptr(), lse.data_ptr(), _stream(q)))
+    out = torch.empty((Tq, H, 128), dtype=_bf16, device=device)
+    lse = torch.empty((H, Tq), dtype=_f32, device=device)
+    _call("fp8bs_mla_prefill", device, *ptrs, *sizes, float(scale), int(bool(causal)), out.data_ptr(), lse.data_ptr())
     return out, lse
 
 
 def fp8bs_mla_prefill_bwd(dout, q, kv, k_rope, out, lse, cu_q, cu_k, scale, causal=True):
     """Gradients of fp8bs_mla_prefill's out: (dq [Tq][H][192], dkv [Tk][H][256],
     dk_rope [Tk][64]), BF16; out and lse as the forward returned them."""
-    ptrs, sizes = _prefill_args(q, kv, k_rope, cu_q, cu_k)
+    device, ptrs, sizes = _prefill_args(q, kv, k_rope, cu_q, cu_k)
     Tq, H = q.shape[:2]
     Tk = kv.shape[0]
-    _want(dout, "dout", (Tq, H, 128))
-    _want(out, "out", (Tq, H, 128))
-    _want(lse, "lse", (H, Tq))
-    _same_device(q=q, dout=dout, out=out, lse=lse)
-    pd, po, pl = _dev(dout, "dout", _BF16), _dev(out, "out", _BF16), _dev(lse, "lse", _F32)
-    L = attn_lib()
-    ws = _workspace(L.fp8bs_mla_prefill_bwd_workspace_bytes(Tq, Tk, H), "fp8bs_mla_prefill_bwd_workspace_bytes", q.device)
-    dq = torch.empty((Tq, H, 192), dtype=torch.bfloat16, device=q.device)
-    dkv = torch.empty((Tk, H, 256), dtype=torch.bfloat16, device=q.device)
-    dk_rope = torch.empty((Tk, 64), dtype=torch.bfloat16, device=q.device)
-    with torch.cuda.device(q.device):
-        _check("fp8bs_mla_prefill_bwd",
-               L.fp8bs_mla_prefill_bwd(pd, *ptrs, po, pl, *sizes, float(scale), int(bool(causal)), dq.data_ptr(),
-                                       dkv.data_ptr(), dk_rope.data_ptr(), ws.data_ptr(), _stream(q)))
+    pd, po = _ptr(dout, "dout", _bf16, (Tq, H, 128), device), _ptr(out, "out", _bf16, (Tq, H, 128), device)
+    pl = _ptr(lse, "lse", _f32, (H, Tq), device)
+    ws = _workspace("fp8bs_mla_prefill_bwd_workspace_bytes", device, Tq, Tk, H)
+    dq = torch.empty((Tq, H, 192), dtype=_bf16, device=device)
+    dkv = torch.empty((Tk, H, 256), dtype=_bf16, device=device)
+    dk_rope = torch.empty((Tk, 64), dtype=_bf16, device=device)
+    _call("fp8bs_mla_prefill_bwd", device, pd, *ptrs, po, pl, *sizes, float(scale), int(bool(causal)), dq.data_ptr(),
+          dkv.data_ptr(), dk_rope.data_ptr(), ws.data_ptr())
     return dq, dkv, dk_rope
 
 
-def _cache_args(cache):
+def _cache_args(cache, device):
     """(kind, pointers, pages, page size) of a cache: BF16 [pages][page][576],
     or the FP8 triple (codes uint8 [..][512], scales f32 [..][4], rope bf16 [..][64])."""
     if isinstance(cache, (tuple, list)):
@@ -154,49 +179,38 @@ def _cache_args(cache):
         codes, scales, rope = cache
         if not isinstance(codes, torch.Tensor) or codes.dim() != 3:
             raise ValueError("cache codes must be [pages][page][512]")
-        pages, page = codes.shape[:2]
-        _want(codes, "cache codes", (pages, page, 512))
-        _want(scales, "cache scales", (pages, page, 4))
-        _want(rope, "cache rope", (pages, page, 64))
-        _same_device(codes=codes, scales=scales, rope=rope)
-        return (CACHE_FP8, _dev(codes, "cache codes", _U8), _dev(scales, "cache scales", _F32),
-                _dev(rope, "cache rope", _BF16), pages, page), codes
+        n, page = codes.shape[:2]
+        return (CACHE_FP8, _ptr(codes, "cache codes", _u8, (n, page, 512), device),
+                _ptr(scales, "cache scales", _f32, (n, page, 4), device),
+                _ptr(rope, "cache rope", _bf16, (n, page, 64), device), n, page)
     if not isinstance(cache, torch.Tensor) or cache.dim() != 3:
         raise ValueError("cache must be [pages][page][576] or (codes, scales, rope)")
-    pages, page = cache.shape[:2]
-    _want(cache, "cache", (pages, page, 576))
-    return (CACHE_BF16, _dev(cache, "cache", _BF16), None, None, pages, page), cache
+    n, page = cache.shape[:2]
+    return CACHE_BF16, _ptr(cache, "cache", _bf16, (n, page, 576), device), None, None, n, page
 
 
 def _decode(fn, q, cache, prefix, table, lens, scale):
-    if not isinstance(q, torch.Tensor) or q.dim() != 4 or q.shape[3] != 576:
-        raise ValueError("q must be [B][T][H][576]")
+    device = _on_gpu(q, "q", (None, None, None, 576))
     B, T, H, _ = q.shape
     if not isinstance(table, torch.Tensor) or table.dim() != 2 or table.shape[0] != B:
         raise ValueError("table must be [B][width]")
-    _want(lens, "lens", (B,))
-    cache_args, first = _cache_args(cache)
-    page = cache_args[-1]
     width = table.shape[1]
+    pq = _ptr(q, "q", _bf16, q.shape, device)
+    cache_args = _cache_args(cache, device)
     pre, n_pre = (), 0
     if prefix is not None:
         prefix_table, prefix_len = prefix
         if not isinstance(prefix_table, torch.Tensor) or prefix_table.dim() != 1:
             raise ValueError("prefix_table must be [pages of the prefix]")
-        _want(prefix_len, "prefix_len", (1,))
-        _same_device(q=q, prefix_table=prefix_table, prefix_len=prefix_len)
         n_pre = prefix_table.shape[0]
-        pre = (_dev(prefix_table, "prefix_table", _I32), n_pre, _dev(prefix_len, "prefix_len", _I32))
-    _same_device(q=q, cache=first, table=table, lens=lens)
-    pq, pt, pl = _dev(q, "q", _BF16), _dev(table, "table", _I32), _dev(lens, "lens", _I32)
-    L = attn_lib()
-    out = torch.empty((B, T, H, 512), dtype=torch.bfloat16, device=q.device)
-    lse = torch.empty((B, T, H), dtype=torch.float32, device=q.device)
-    with torch.cuda.device(q.device):
-        ws = _workspace(L.fp8bs_mla_decode_workspace_bytes(B, T, H, width, page, n_pre),
-                        "fp8bs_mla_decode_workspace_bytes", q.device)
-        _check(fn, getattr(L, fn)(pq, *cache_args, *pre, pt, width, pl, B, T, H, float(scale), out.data_ptr(),
-                                  lse.data_ptr(), ws.data_ptr(), _stream(q)))
+        pre = (_ptr(prefix_table, "prefix_table", _i32, (n_pre,), device), n_pre,
+               _ptr(prefix_len, "prefix_len", _i32, (1,), device))
+    pt, pl = _ptr(table, "table", _i32, (B, width), device), _ptr(lens, "lens", _i32, (B,), device)
+    out = torch.empty((B, T, H, 512), dtype=_bf16, device=device)
+    lse = torch.empty((B, T, H), dtype=_f32, device=device)
+    ws = _workspace("fp8bs_mla_decode_workspace_bytes", device, B, T, H, width, cache_args[5], n_pre)
+    _call(fn, device, pq, *cache_args, *pre, pt, width, pl, B, T, H, float(scale), out.data_ptr(), lse.data_ptr(),
+          ws.data_ptr())
     return out, lse
 
 
@@ -218,31 +232,23 @@ def fp8bs_verify_drafts(p, q, drafts, n_drafts, u, u_next):
     [B][K][V] (or None: drafts chosen without chance) probabilities, f32 or bf16;
     drafts int32 [B][K], n_drafts int32 [B], u f32 [B][K], u_next f32 [B].
     Returns (tokens int32 [B][K+1], accepted int32 [B])."""
-    if not isinstance(p, torch.Tensor) or p.dim() != 3:
-        raise ValueError("p must be [B][K+1][V]")
-    B, K, V = p.shape[0], p.shape[1] - 1, p.shape[2]
+    if isinstance(q, torch.Tensor) and isinstance(p, torch.Tensor) and q.dtype != p.dtype:
+        raise TypeError("p and q must have one dtype")
+    device = _on_gpu(p, "p", (None, None, None))
+    B, K1, V = p.shape
+    K = K1 - 1
     if K < 0:
         raise ValueError("p must be [B][K+1][V]")
-    if q is not None:
-        _want(q, "q", (B, K, V))
-        if q.dtype != p.dtype:
-            raise TypeError("p and q must have one dtype")
-    pp, pq = _dev(p, "p", (torch.float32, torch.bfloat16)), None
-    if q is not None:
-        pq = _dev(q, "q", (torch.float32, torch.bfloat16))
-    _want(drafts, "drafts", (B, K))
-    _want(n_drafts, "n_drafts", (B,))
-    _want(u, "u", (B, K))
-    _want(u_next, "u_next", (B,))
-    _same_device(p=p, q=q, drafts=drafts, n_drafts=n_drafts, u=u, u_next=u_next)
-    args = (_dev(drafts, "drafts", _I32), _dev(n_drafts, "n_drafts", _I32), _dev(u, "u", _F32),
-            _dev(u_next, "u_next", _F32))
-    L = attn_lib()
-    tokens = torch.empty((B, K + 1), dtype=torch.int32, device=p.device)
-    accepted = torch.empty((B,), dtype=torch.int32, device=p.device)
-    ws = _workspace(L.fp8bs_verify_drafts_workspace_bytes(B, V), "fp8bs_verify_drafts_workspace_bytes", p.device)
-    with torch.cuda.device(p.device):
-        _check("fp8bs_verify_drafts",
-               L.fp8bs_verify_drafts(pp, pq, _in_dtype(p), *args, B, K, V, tokens.data_ptr(), accepted.data_ptr(),
-                                     ws.data_ptr(), _stream(p)))
+    dtype = p.dtype
+    if dtype not in (_f32, _bf16):
+        raise TypeError(f"p has dtype {dtype}, expected float32 or bfloat16")
+    pp = _ptr(p, "p", dtype, p.shape, device)
+    pq = None if q is None else _ptr(q, "q", dtype, (B, K, V), device)
+    args = (_ptr(drafts, "drafts", _i32, (B, K), device), _ptr(n_drafts, "n_drafts", _i32, (B,), device),
+            _ptr(u, "u", _f32, (B, K), device), _ptr(u_next, "u_next", _f32, (B,), device))
+    tokens = torch.empty((B, K1), dtype=_i32, device=device)
+    accepted = torch.empty((B,), dtype=_i32, device=device)
+    ws = _workspace("fp8bs_verify_drafts_workspace_bytes", device, B, V)
+    _call("fp8bs_verify_drafts", device, pp, pq, _lib.BF16 if dtype == _bf16 else _lib.F32, *args, B, K, V,
+          tokens.data_ptr(), accepted.data_ptr(), ws.data_ptr())
     return tokens, accepted

@@ -16,7 +16,6 @@ constexpr int64_t kGridMax = kI32 - 1;
 constexpr int kTile = 64;
 
 bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
-bool off8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) != 0; }
 bool off4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 int status_of(hipError_t e) { return e == hipSuccess ? FP8BS_OK : FP8BS_ERR_LAUNCH; }
 hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
@@ -245,8 +244,8 @@ int fp8bs_mla_decode_shared(const uint16_t* q, int cache_kind, const void* cache
 
 int64_t fp8bs_verify_drafts_workspace_bytes(int B, int64_t V) {
   if (B < 0 || V < 1) return FP8BS_ERR_SHAPE;
-  if (V > 1 << 24 || B * fp8bs::verify_chunks(V) > kGridMax) return FP8BS_ERR_TOO_LARGE;
-  return 16 * B * fp8bs::verify_chunks(V);
+  if (V > 1 << 24 || B * (fp8bs::verify_chunks(V) + 1) > kGridMax) return FP8BS_ERR_TOO_LARGE;
+  return 16 * B * (fp8bs::verify_chunks(V) + 1);
 }
 
 int fp8bs_verify_drafts(const void* p, const void* q, int dtype, const int32_t* drafts, const int32_t* n_drafts,
@@ -260,14 +259,15 @@ int fp8bs_verify_drafts(const void* p, const void* q, int dtype, const int32_t* 
   if (!p || !n_drafts || !u_next || !tokens || !accepted || !workspace) return FP8BS_ERR_NULL_PTR;
   if (K > 0 && (!drafts || !u)) return FP8BS_ERR_NULL_PTR;
   if (off4(p) || off4(q) || off4(drafts) || off4(n_drafts) || off4(u) || off4(u_next) || off4(tokens) ||
-      off4(accepted) || off8(workspace))
+      off4(accepted) || off16(workspace))
     return FP8BS_ERR_ALIGN;
   fp8bs::VerifyDrafts v{};
   v.p = p; v.q = q;
   v.drafts = drafts; v.n_drafts = n_drafts;
   v.u = u; v.u_next = u_next;
   v.B = B; v.K = K; v.V = (int)V;
-  v.sums = static_cast<uint64_t*>(workspace);
+  v.rows = static_cast<int4*>(workspace);
+  v.sums = reinterpret_cast<uint64_t*>(v.rows + B);
   v.tokens = tokens; v.accepted = accepted;
   return status_of(fp8bs::launch_verify_drafts(v, dtype == FP8BS_BF16, as_stream(stream)));
 }

@@ -70,6 +70,7 @@ struct VerifyDrafts {
   const float* u_next;    // [B]
   int B, K, V;
   uint64_t* sums;         // [B][chunks][2]
+  int4* rows;             // [B]: accepted, whether one was turned down, its token
   int32_t* tokens;        // [B][K+1]
   int32_t* accepted;      // [B]
 };

@@ -85,50 +85,65 @@ __device__ __forceinline__ void advance(const MlaDecode& p, Cursor& c) {
   c.tiles = (c.len + kTile - 1) / kTile;
 }
 
-__device__ __forceinline__ int wave_sum(int v) {
+__device__ __forceinline__ int wave_scan(int v) {
+  const int lane = threadIdx.x & 63;
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
+  for (int d = 1; d < 64; d <<= 1) {
+    const int x = __shfl_up(v, d, 64);
+    if (lane >= d) v += x;
+  }
   return v;
 }
 
-// All tiles of the batch.
-__device__ __forceinline__ int total_tiles(const MlaDecode& p) {
-  int sum = 0;
-  for (int b = threadIdx.x & 63; b < p.B; b += 64) sum += (clamp_len(p, b) + kTile - 1) / kTile;
-  return __builtin_amdgcn_readfirstlane(wave_sum(sum));
-}
+// The groups' ranges of `total` tiles: consecutive, of equal length but for one
+// tile, the longer ones (and, if there are fewer tiles than groups, those that
+// have any) first.
+struct Ranges {
+  int each, longer;
+  __device__ __forceinline__ Ranges(int total, int groups)
+      : each(total / groups), longer(total - total / groups * groups) {}
+  __device__ __forceinline__ int start(int g) const { return g * each + min(g, longer); }
+  __device__ __forceinline__ int of(int t) const {      // the group of tile t
+    const int head = longer * (each + 1);
+    return t < head ? t / (each + 1) : longer + (t - head) / max(each, 1);
+  }
+};
 
-// The cursor of tile t (t < all tiles).
-__device__ __forceinline__ Cursor locate(const MlaDecode& p, int t, int left) {
+__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
+
+// The range of group g as a cursor on its first tile (left = 0: it has none).
+__device__ __forceinline__ Cursor first_tile(const MlaDecode& p, int g) {
   const int lane = threadIdx.x & 63;
+  // tiles of all requests; up to 64 requests are read once
+  int len = 0, incl = 0, total = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 64) {
+    len = b0 + lane < p.B ? clamp_len(p, b0 + lane) : 0;
+    incl = wave_scan(tiles_of(len));
+    total += __builtin_amdgcn_readlane(incl, 63);
+  }
+  const Ranges r(total, p.groups);
+  const int t = r.start(g), left = r.start(g + 1) - t;
+  if (left <= 0) return Cursor{0, 0, 0, 0, 0};
   int base = 0;
   for (int b0 = 0; b0 < p.B; b0 += 64) {
-    const int len = b0 + lane < p.B ? clamp_len(p, b0 + lane) : 0;
-    const int n = (len + kTile - 1) / kTile;
-    int incl = n;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int v = __shfl_up(incl, d, 64);
-      if (lane >= d) incl += v;
+    if (p.B > 64) {
+      len = b0 + lane < p.B ? clamp_len(p, b0 + lane) : 0;
+      incl = wave_scan(tiles_of(len));
     }
     const uint64_t hit = __ballot(t < base + incl);
     if (hit) {
-      const int l = __ffsll((unsigned long long)hit) - 1;
+      const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
       Cursor c;
       c.b = b0 + l;
-      c.len = __builtin_amdgcn_readfirstlane(__shfl(len, l, 64));
-      c.tiles = __builtin_amdgcn_readfirstlane(__shfl(n, l, 64));
-      c.tile = __builtin_amdgcn_readfirstlane(t - base - __shfl(incl - n, l, 64));
+      c.len = __builtin_amdgcn_readlane(len, l);
+      c.tiles = tiles_of(c.len);
+      c.tile = t - base - (__builtin_amdgcn_readlane(incl, l) - c.tiles);
       c.left = left;
       return c;
     }
-    base += __shfl(incl, 63, 64);
+    base += __builtin_amdgcn_readlane(incl, 63);
   }
-  return Cursor{p.B, 0, 0, 0, 0};
-}
-
-__device__ __forceinline__ int range_start(int g, int total, int groups) {
-  return (int)((int64_t)g * total / groups);
+  return Cursor{0, 0, 0, 0, 0};
 }
 
 // The flat cache token (page * page size + slot) of token `tok`, given its
@@ -253,15 +268,13 @@ __global__ __launch_bounds__(256 * RT) __attribute__((amdgpu_waves_per_eu(2))) v
   const int xcd = blockIdx.x % kAttnXcds;
   const int wg = xcd * per + min(xcd, rest) + blockIdx.x / kAttnXcds;
   const int g = wg / p.row_blocks;
-  const int total = total_tiles(p);
-  const int t0 = range_start(g, total, p.groups), t1 = range_start(g + 1, total, p.groups);
-  if (t0 >= t1) return;
+  Cursor cur = first_tile(p, g);
+  if (cur.left == 0) return;
 
   const uint32_t lds_tiles = lds_offset(tiles);
   const int* const entries = reinterpret_cast<const int*>(slots + NW * kSlot + wave * 256);
   const uint32_t lds_entries = lds_offset(entries);
   int entry = 0;         // of row `lane` of the tile that is loaded next (NBUF == 2)
-  Cursor cur = locate(p, t0, t1 - t0);
   Cursor nxt = cur;      // the tile that is loaded next
   Cursor ent = cur;      // the tile whose block-table entries are fetched next
   auto fetch_entries = [&] {
@@ -563,76 +576,137 @@ __global__ __launch_bounds__(256 * RT) __attribute__((amdgpu_waves_per_eu(2))) v
 }
 
 // Joins the partials of the rows whose request was cut between groups (and, in
-// the shared form, the prefix's with the request's own). One wave per row,
-// lane l columns 8l .. 8l+7.
-struct Joiner {
-  float m = neg_inf(), l = 0.f;
-  float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  __device__ __forceinline__ void add(const MlaDecode& p, int64_t part, int row, int lane) {
-    const int64_t at = part * p.rows + row;
-    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
-    const f32x4* src = reinterpret_cast<const f32x4*>(p.part + at * kLatent + 8 * lane);
-    const f32x4 a = src[0], b = src[1];
-    const float mn = fmaxf(m, ml.x), ref = mn == neg_inf() ? 0.f : mn;
-    const float x = exp2_fast(m - ref), y = exp2_fast(ml.x - ref);
-    l = fmaf(l, x, ml.y * y);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o[i] = fmaf(o[i], x, a[i] * y);
-      o[4 + i] = fmaf(o[4 + i], x, b[i] * y);
-    }
-    m = mn;
-  }
+// the shared form, the prefix's with the request's own). W waves per row, lane
+// l columns 8l .. 8l+7; all pieces' maxima are read at once, so every load of
+// a piece's output is under way before the first is needed.
+struct Pieces {      // of one row in one problem: part(i), i < n
+  const MlaDecode* p;
+  int n, row;
+  int64_t first;      // the first piece's slot; the others lie 2 slots apart from `rest`
+  int64_t rest;
+  bool done;          // the row's result is written already
+  __device__ __forceinline__ int64_t at(int i) const { return (i == 0 ? first : rest + 2 * (int64_t)i) * p->rows + row; }
 };
 
-// Adds the partials of one row; false if the row's result is written already.
-__device__ __forceinline__ bool add_pieces(const MlaDecode& p, int64_t o, int lane, Joiner& j) {
-  const int b = (int)(o / p.rows), row = (int)(o - (int64_t)b * p.rows);
-  // tiles before the request, its own and all
-  int before = 0, all = 0;
-  for (int x = lane; x < p.B; x += 64) {
-    const int n = (clamp_len(p, x) + kTile - 1) / kTile;
-    all += n;
-    before += x < b ? n : 0;
+__device__ __forceinline__ Pieces pieces_of(const MlaDecode& p, int64_t o) {
+  const int lane = threadIdx.x & 63;
+  const int b = (int)(o / p.rows);
+  Pieces r{&p, 0, (int)(o - (int64_t)b * p.rows), 0, 0, false};
+  int before = 0, all = 0, own = 0;      // tiles before the request, of all, its own
+  for (int b0 = 0; b0 < p.B; b0 += 64) {
+    const int n = b0 + lane < p.B ? tiles_of(clamp_len(p, b0 + lane)) : 0, incl = wave_scan(n);
+    if (b >= b0 && b < b0 + 64) {
+      own = __builtin_amdgcn_readlane(n, b - b0);
+      before = all + __builtin_amdgcn_readlane(incl, b - b0) - own;
+    }
+    all += __builtin_amdgcn_readlane(incl, 63);
   }
-  all = wave_sum(all);
-  before = wave_sum(before);
-  const int own = (clamp_len(p, b) + kTile - 1) / kTile;
-  if (own == 0) return true;
-  // the group of tile t is the last whose range starts at or before it
-  auto group_of = [&](int t) {
-    int g = (int)((int64_t)t * p.groups / all);
-    while (g + 1 < p.groups && range_start(g + 1, all, p.groups) <= t) ++g;
-    while (range_start(g, all, p.groups) > t) --g;
-    return g;
-  };
-  const int g0 = group_of(before), g1 = group_of(before + own - 1);
+  if (own == 0) return r;
+  const Ranges ranges(all, p.groups);
+  const int g0 = ranges.of(before), g1 = ranges.of(before + own - 1);
   if (g0 == g1) {
-    if (!p.join) return false;
-    j.add(p, 2 * (int64_t)p.groups + b, row, lane);
-    return true;
+    r.done = !p.join;
+    r.n = 1;
+    r.first = 2 * (int64_t)p.groups + b;
+  } else {
+    r.n = g1 - g0 + 1;
+    r.first = 2 * (int64_t)g0 + (ranges.start(g0) < before ? 1 : 0);
+    r.rest = 2 * (int64_t)g0;
   }
-  for (int g = g0; g <= g1; ++g) {
-    const int start = range_start(g, all, p.groups);
-    if (start == range_start(g + 1, all, p.groups)) continue;     // an empty range
-    j.add(p, 2 * (int64_t)g + (start >= before ? 0 : 1), row, lane);
-  }
-  return true;
+  return r;
 }
 
+template <int W>
 __global__ __launch_bounds__(kThreads) void mla_join_kernel(const MlaDecode p, const MlaDecode prefix) {
+  constexpr int kRowsPerBlock = kThreads / 64 / W, kBatch = 4;
+  __shared__ float2 ml[W > 1 ? W : 1];
+  __shared__ __align__(16) float sums[W > 1 ? W : 1][512];
   const int lane = threadIdx.x & 63;
-  const int64_t o = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wave % W;
+  const int64_t o = (int64_t)blockIdx.x * kRowsPerBlock + wave / W;
   if (o >= p.all_rows) return;
-  Joiner j;
-  if (!add_pieces(p, o, lane, j)) return;
-  if (p.join) add_pieces(prefix, o, lane, j);
-  const float inv = j.l > 0.f ? 1.f / j.l : 0.f;
+  const Pieces own = pieces_of(p, o);
+  if (own.done) return;
+  Pieces pre{};
+  if (p.join) pre = pieces_of(prefix, o);
+  const int n = own.n + pre.n;
+  // this wave's pieces: every W-th
+  float m = neg_inf(), l = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int i0 = w; i0 < n; i0 += 64 * W) {
+    const int i = i0 + lane * W;      // lane's piece
+    const bool mine = i < own.n;
+    float2 x = make_float2(neg_inf(), 0.f);
+    if (i < n) x = *reinterpret_cast<const float2*>((mine ? p.part_ml : prefix.part_ml) + 2 * (mine ? own.at(i) : pre.at(i - own.n)));
+    float mn = x.x;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) mn = fmaxf(mn, __shfl_xor(mn, d, 64));
+    mn = fmaxf(mn, m);
+    const float ref = mn == neg_inf() ? 0.f : mn;
+    const float old = exp2_fast(m - ref), weight = exp2_fast(x.x - ref);
+    float add = x.y * weight;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) add += __shfl_xor(add, d, 64);
+    l = fmaf(l, old, add);
+    m = mn;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] *= old;
+    const int count = min(64, (n - i0 + W - 1) / W);
+    for (int k0 = 0; k0 < count; k0 += kBatch) {
+      f32x4 v[kBatch][2];
+      float wt[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int kc = min(k0 + k, count - 1), j = i0 + kc * W;
+        const bool a = j < own.n;
+        const float* src = (a ? p.part : prefix.part) + (a ? own.at(j) : pre.at(j - own.n)) * kLatent + 8 * lane;
+        v[k][0] = *reinterpret_cast<const f32x4*>(src);
+        v[k][1] = *reinterpret_cast<const f32x4*>(src + 4);
+        const float got = __shfl(weight, kc, 64);
+        wt[k] = k0 + k < count ? got : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          acc[j] = fmaf(v[k][0][j], wt[k], acc[j]);
+          acc[4 + j] = fmaf(v[k][1][j], wt[k], acc[4 + j]);
+        }
+    }
+  }
+  if constexpr (W > 1) {
+    if (lane == 0) ml[w] = make_float2(m, l);
+    __syncthreads();
+    float mn = neg_inf();
+#pragma unroll
+    for (int k = 0; k < W; ++k) mn = fmaxf(mn, ml[k].x);
+    const float ref = mn == neg_inf() ? 0.f : mn, x = exp2_fast(m - ref);
+    l = 0.f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) l = fmaf(ml[k].y, exp2_fast(ml[k].x - ref), l);
+    m = mn;
+    f32x4 a, b;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      a[j] = acc[j] * x;
+      b[j] = acc[4 + j] * x;
+    }
+    *reinterpret_cast<f32x4*>(&sums[w][8 * lane]) = a;
+    *reinterpret_cast<f32x4*>(&sums[w][8 * lane + 4]) = b;
+    __syncthreads();
+    if (w > 0) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      acc[j] = 0.f;
+#pragma unroll
+      for (int k = 0; k < W; ++k) acc[j] += sums[k][8 * lane + j];
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
   bf16x8 v;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = (__bf16)(j.o[i] * inv);
+  for (int i = 0; i < 8; ++i) v[i] = (__bf16)(acc[i] * inv);
   *reinterpret_cast<bf16x8*>(p.out + o * kLatent + 8 * lane) = v;
-  if (lane == 0) p.lse[o] = j.l > 0.f ? (j.m + __builtin_log2f(j.l)) * kLn2 : neg_inf();
+  if (lane == 0) p.lse[o] = l > 0.f ? (m + __builtin_log2f(l)) * kLn2 : neg_inf();
 }
 
 int compute_units() {
@@ -678,8 +752,14 @@ int mla_decode_groups(int64_t row_blocks, int64_t max_tiles) {
 hipError_t launch_mla_decode(const MlaDecode& own, const MlaDecode* prefix, bool fp8, hipStream_t stream) {
   if (prefix) launch_tiles(*prefix, fp8, stream);
   if (own.max_len > 0) launch_tiles(own, fp8, stream);
-  hipLaunchKernelGGL(mla_join_kernel, dim3((unsigned)((own.all_rows + 3) / 4)), dim3(kThreads), 0, stream, own,
-                     prefix ? *prefix : own);
+  // few rows have many pieces each: a workgroup per row (256 rows of about 28
+  // pieces: 27 us with a wave per row); many rows have one or two, and a wave
+  // per row has less to set up
+  const MlaDecode& other = prefix ? *prefix : own;
+  if (own.all_rows <= 2048)
+    hipLaunchKernelGGL(mla_join_kernel<4>, dim3((unsigned)own.all_rows), dim3(kThreads), 0, stream, own, other);
+  else
+    hipLaunchKernelGGL(mla_join_kernel<1>, dim3((unsigned)((own.all_rows + 3) / 4)), dim3(kThreads), 0, stream, own, other);
   return hipGetLastError();
 }
 

@@ -21,7 +21,7 @@ namespace fp8bs {
 
 namespace {
 
-constexpr int kChunk = 4096, kVThreads = 256, kPer = kChunk / kVThreads;
+constexpr int kChunk = 8192, kVThreads = 256, kPer = kChunk / kVThreads;      // kPer consecutive entries a thread
 constexpr float kWeightOne = 274877906944.0f;      // 2^38
 
 template <bool BF16>
@@ -66,14 +66,53 @@ __device__ __forceinline__ Row accept(const VerifyDrafts& v, int b) {
   return r;
 }
 
-// The weights of vocabulary entry i: after a rejection, and plain.
-template <bool BF16>
-__device__ __forceinline__ void weights(const VerifyDrafts& v, int64_t prow, int64_t qrow, const Row& r, int i,
-                                        uint64_t& residual, uint64_t& plain) {
-  const float p = prob<BF16>(v.p, prow + i);
-  plain = weight(p);
-  residual = plain;
-  if (r.rejected) residual = v.q ? weight(p - prob<BF16>(v.q, qrow + i)) : (i == r.token ? 0ull : plain);
+// Entries first .. first+3 of a row, 0 past its end. VEC: rows begin and end on
+// whole groups of four.
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void load4(const void* row, int64_t at, int first, int V, float (&x)[4]) {
+  if constexpr (VEC) {
+    x[0] = x[1] = x[2] = x[3] = 0.f;
+    if (first >= V) return;
+    if constexpr (BF16) {
+      const uint2 d = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(row) + at + first);
+      x[0] = __uint_as_float(d.x << 16);
+      x[1] = __uint_as_float(d.x & 0xFFFF0000u);
+      x[2] = __uint_as_float(d.y << 16);
+      x[3] = __uint_as_float(d.y & 0xFFFF0000u);
+    } else {
+      const float4 d = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(row) + at + first);
+      x[0] = d.x;
+      x[1] = d.y;
+      x[2] = d.z;
+      x[3] = d.w;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = first + k < V ? prob<BF16>(row, at + first + k) : 0.f;
+  }
+}
+
+// The weights of the kPer entries that begin at `first`, `step` apart in groups
+// of four: after a rejection, and plain.
+template <bool BF16, bool VEC, typename F>
+__device__ __forceinline__ void weights(const VerifyDrafts& v, int b, const Row& r, int first, int step, F&& take) {
+  const int64_t prow = ((int64_t)b * (v.K + 1) + r.accepted) * v.V, qrow = ((int64_t)b * v.K + r.accepted) * v.V;
+  float p[kPer / 4][4], q[kPer / 4][4];
+#pragma unroll
+  for (int g = 0; g < kPer / 4; ++g) load4<BF16, VEC>(v.p, prow, first + g * step, v.V, p[g]);
+  if (r.rejected && v.q) {
+#pragma unroll
+    for (int g = 0; g < kPer / 4; ++g) load4<BF16, VEC>(v.q, qrow, first + g * step, v.V, q[g]);
+  } else {
+#pragma unroll
+    for (int g = 0; g < kPer / 4; ++g)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) q[g][k] = r.rejected && first + g * step + k == r.token ? __builtin_inff() : 0.f;
+  }
+#pragma unroll
+  for (int g = 0; g < kPer / 4; ++g)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) take(4 * g + k, weight(p[g][k] - q[g][k]), weight(p[g][k]));
 }
 
 __device__ __forceinline__ uint64_t wave_sum64(uint64_t x) {
@@ -91,23 +130,17 @@ __device__ __forceinline__ uint64_t wave_scan64(uint64_t x) {
   return x;
 }
 
-template <bool BF16>
+template <bool BF16, bool VEC>
 __global__ __launch_bounds__(kVThreads) void verify_sum_kernel(const VerifyDrafts v, int chunks) {
   __shared__ uint64_t part[kVThreads / 64][2];
   const int b = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
   const Row r = accept<BF16>(v, b);
-  const int64_t prow = ((int64_t)b * (v.K + 1) + r.accepted) * v.V, qrow = ((int64_t)b * v.K + r.accepted) * v.V;
+  if (chunk == 0 && threadIdx.x == 0) v.rows[b] = make_int4(r.accepted, r.rejected, r.token, 0);
   uint64_t a = 0, c = 0;
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int i = chunk * kChunk + k * kVThreads + (int)threadIdx.x;
-    if (i < v.V) {
-      uint64_t x, y;
-      weights<BF16>(v, prow, qrow, r, i, x, y);
-      a += x;
-      c += y;
-    }
-  }
+  weights<BF16, VEC>(v, b, r, chunk * kChunk + 4 * (int)threadIdx.x, 4 * kVThreads, [&](int, uint64_t x, uint64_t y) {
+    a += x;
+    c += y;
+  });
   a = wave_sum64(a);
   c = wave_sum64(c);
   if ((threadIdx.x & 63) == 0) {
@@ -120,12 +153,12 @@ __global__ __launch_bounds__(kVThreads) void verify_sum_kernel(const VerifyDraft
         part[0][threadIdx.x] + part[1][threadIdx.x] + part[2][threadIdx.x] + part[3][threadIdx.x];
 }
 
-template <bool BF16>
+template <bool BF16, bool VEC>
 __global__ __launch_bounds__(kVThreads) void verify_pick_kernel(const VerifyDrafts v, int chunks) {
-  __shared__ uint64_t seg[kChunk / 64];
+  __shared__ uint64_t waves[kVThreads / 64];
   const int b = blockIdx.x, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const Row r = accept<BF16>(v, b);
-  const int64_t prow = ((int64_t)b * (v.K + 1) + r.accepted) * v.V, qrow = ((int64_t)b * v.K + r.accepted) * v.V;
+  const int4 known = v.rows[b];
+  const Row r{known.x, known.y != 0, known.z};
   // which weights, and their sum
   const uint64_t* sums = v.sums + (int64_t)b * chunks * 2;
   uint64_t ta = 0, tc = 0;
@@ -137,7 +170,6 @@ __global__ __launch_bounds__(kVThreads) void verify_pick_kernel(const VerifyDraf
   tc = wave_sum64(tc);
   const bool plain = ta == 0;          // nothing left of p - q: p itself
   const uint64_t total = plain ? tc : ta;
-  int next = -1;
   if (total > 0) {
     // the token is the first whose running sum passes goal = floor(total * u)
     const float u = fminf(fmaxf(v.u_next[b], 0.f), 1.f - 0x1p-24f);
@@ -159,29 +191,26 @@ __global__ __launch_bounds__(kVThreads) void verify_pick_kernel(const VerifyDraf
       before = __shfl((unsigned long long)incl, 63, 64);
     }
     goal -= before;
-    // its 64 entries, then the entry
-    uint64_t mine[kPer];
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      const int i = chunk * kChunk + k * kVThreads + (int)threadIdx.x;
-      uint64_t x = 0, y = 0;
-      if (i < v.V) weights<BF16>(v, prow, qrow, r, i, x, y);
-      mine[k] = plain ? y : x;
-      const uint64_t s = wave_sum64(mine[k]);
-      if (lane == 0) seg[k * (kVThreads / 64) + w] = s;
-    }
+    // its thread's consecutive entries, then the entry
+    const int first = chunk * kChunk + kPer * (int)threadIdx.x;
+    uint64_t mine[kPer], own = 0;
+    weights<BF16, VEC>(v, b, r, first, 4, [&](int i, uint64_t x, uint64_t y) {
+      mine[i] = plain ? y : x;
+      own += mine[i];
+    });
+    uint64_t incl = wave_scan64(own);
+    if (lane == 63) waves[w] = incl;
     __syncthreads();
-    const uint64_t x = seg[lane], incl = wave_scan64(x);
-    const int s = __ffsll((unsigned long long)__ballot(incl > goal)) - 1;
-    goal -= __shfl((unsigned long long)(incl - x), s, 64);
-    if ((s & 3) == w) {
-      uint64_t y = 0;
+    for (int k = 0; k < w; ++k) incl += waves[k];
+    if (incl > goal && incl - own <= goal) {
+      uint64_t run = incl - own;
+      int at = 0;
 #pragma unroll
-      for (int k = 0; k < kPer; ++k)
-        if (k == s >> 2) y = mine[k];
-      const int e = __ffsll((unsigned long long)__ballot(wave_scan64(y) > goal)) - 1;
-      next = chunk * kChunk + s * 64 + e;
-      if (lane == 0) v.tokens[(int64_t)b * (v.K + 1) + r.accepted] = next;
+      for (int i = 0; i < kPer; ++i) {
+        run += mine[i];
+        at += run <= goal;
+      }
+      v.tokens[(int64_t)b * (v.K + 1) + r.accepted] = first + at;
     }
   } else if (threadIdx.x == 0) {
     v.tokens[(int64_t)b * (v.K + 1) + r.accepted] = -1;
@@ -191,11 +220,11 @@ __global__ __launch_bounds__(kVThreads) void verify_pick_kernel(const VerifyDraf
   if (threadIdx.x == 0) v.accepted[b] = r.accepted;
 }
 
-template <bool BF16>
+template <bool BF16, bool VEC>
 void launch(const VerifyDrafts& v, hipStream_t stream) {
   const int chunks = (int)verify_chunks(v.V);
-  hipLaunchKernelGGL(verify_sum_kernel<BF16>, dim3((unsigned)v.B * chunks), dim3(kVThreads), 0, stream, v, chunks);
-  hipLaunchKernelGGL(verify_pick_kernel<BF16>, dim3((unsigned)v.B), dim3(kVThreads), 0, stream, v, chunks);
+  hipLaunchKernelGGL((verify_sum_kernel<BF16, VEC>), dim3((unsigned)v.B * chunks), dim3(kVThreads), 0, stream, v, chunks);
+  hipLaunchKernelGGL((verify_pick_kernel<BF16, VEC>), dim3((unsigned)v.B), dim3(kVThreads), 0, stream, v, chunks);
 }
 
 }  // namespace
@@ -203,10 +232,13 @@ void launch(const VerifyDrafts& v, hipStream_t stream) {
 int64_t verify_chunks(int64_t V) { return (V + kChunk - 1) / kChunk; }
 
 hipError_t launch_verify_drafts(const VerifyDrafts& v, bool bf16, hipStream_t stream) {
+  // rows of whole groups of four entries, all of them aligned: wide loads
+  const uintptr_t at = reinterpret_cast<uintptr_t>(v.p) | reinterpret_cast<uintptr_t>(v.q);
+  const bool vec = v.V % 4 == 0 && at % (bf16 ? 8 : 16) == 0;
   if (bf16)
-    launch<true>(v, stream);
+    vec ? launch<true, true>(v, stream) : launch<true, false>(v, stream);
   else
-    launch<false>(v, stream);
+    vec ? launch<false, true>(v, stream) : launch<false, false>(v, stream);
   return hipGetLastError();
 }
 

@@ -204,3 +204,22 @@ def test_same_bits_on_a_stream_and_in_a_graph(dev, kind):
             assert torch.equal(a, b)
     for a, b in zip(res, ref):
         assert torch.equal(a, b)
+
+
+def test_binding_refusals(dev):
+    c = Paged(dev, "bf16", 16, [5, 9], 1)
+    q = _q(dev, 2, 1, 4, 1)
+    bad = [
+        (ValueError, (q, c.cache, c.table[:1], c.lens)), (ValueError, (q, c.cache, c.table, c.lens[:1])),
+        (TypeError, (q.float(), c.cache, c.table, c.lens)), (TypeError, (q, c.cache, c.table.long(), c.lens)),
+        (ValueError, (q, c.cache[..., :512], c.table, c.lens)), (ValueError, (q, c.cache.transpose(0, 1), c.table, c.lens)),
+        (ValueError, (q, (c.cache, c.cache), c.table, c.lens)), (ValueError, (q, c.cache, c.table.cpu(), c.lens)),
+        (ValueError, (torch.cat([q, q], 1)[:, ::2], c.cache, c.table, c.lens)), (ValueError, (q, c.cache, c.table[:, ::2], c.lens)),
+    ]
+    for error, args in bad:
+        with pytest.raises(error):
+            fb.fp8bs_mla_decode(*args, SCALE)
+    with pytest.raises(fb.Fp8bsError):
+        fb.fp8bs_mla_decode(q, c.cache, c.table, c.lens, -1.0)
+    with pytest.raises(ValueError):
+        fb.fp8bs_mla_decode_shared(q, c.cache, c.table, c.prefix_len, c.table, c.lens, SCALE)
