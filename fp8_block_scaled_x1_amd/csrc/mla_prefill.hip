@@ -25,15 +25,22 @@ namespace fp8bs {
 
 namespace {
 
-// Workgroup -> (unit, head). The heads are dealt over the XCDs, and the units
-// of a head follow each other there: they share its keys and values in L2.
+// Workgroup -> (unit, head). The heads are dealt over the XCDs and taken there
+// four at a time, unit by unit: the units of a head that run together share its
+// keys and values in L2 (all of an XCD's heads at once would not fit: 8% slower
+// with 16 heads of 8192 tokens), and the last units to run, the short ones of
+// four heads, leave little of the device idle (a head after the other: 3-12%
+// slower).
 __device__ __forceinline__ bool unit_of(int units, int H, int& unit, int& head) {
-  const int xcd = blockIdx.x % kAttnXcds, slot = blockIdx.x / kAttnXcds;
-  const int per = (H + kAttnXcds - 1) / kAttnXcds;
+  constexpr int kTogether = 4;
   if (H % kAttnXcds == 0) {
-    head = (slot / units) * kAttnXcds + xcd;
-    unit = slot % units;
-    return slot < per * units;
+    const int xcd = blockIdx.x % kAttnXcds, slot = blockIdx.x / kAttnXcds, heads = H / kAttnXcds;
+    if (slot >= heads * units) return false;
+    const int group = slot / (kTogether * units), in = slot - group * kTogether * units;
+    const int n = min(kTogether, heads - group * kTogether);
+    head = (group * kTogether + in % n) * kAttnXcds + xcd;
+    unit = in / n;
+    return true;
   }
   head = blockIdx.x % H;
   unit = blockIdx.x / H;
