@@ -98,14 +98,19 @@ def _tokens(t, name, inner, device):
     return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else n
 
 
+# the current stream's handle without the Stream object around it (2 us less per call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _call(fn, device, *args):
     """Calls the entry point on the device's current stream, with the device current."""
-    entry = getattr(attn_lib(), fn)
-    if device.index == torch.cuda.current_device():
-        status = entry(*args, torch.cuda.current_stream(device).cuda_stream)
+    entry, index = getattr(attn_lib(), fn), device.index
+    if index == torch.cuda.current_device():
+        status = entry(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            status = entry(*args, torch.cuda.current_stream(device).cuda_stream)
+            status = entry(*args, _raw_stream(index))
     if status != 0:
         raise _lib.Fp8bsError(fn, status)
 
