@@ -603,6 +603,12 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void m
 // staggered by 32 keys as the keys' gradient is; dS needs no sums between
 // workgroups (S and dP are formed a second time instead, 320 of its 512
 // multiplications per query and key, so no result depends on any order).
+// D comes from O rounded to BF16. Over many keys that rounding is far below
+// those of the weights and of dS; where few keys make O as large as V it is
+// their equal (requests of up to 260 tokens: error of dQ and dK 0.0028 of their
+// norm instead of 0.0024). A wave whose queries see the first tile alone forms
+// D = sum_j P_j dP_j in FP32 instead, for the keys' gradient too, which is
+// launched after this.
 __global__ __launch_bounds__(256, 1) void mla_dq_kernel(const MlaPrefill p, int units) {
   constexpr int NW = 4, BM = 32 * NW, NBUF = 3;
   using Load = KeyLoader<NW>;
@@ -647,7 +653,7 @@ __global__ __launch_bounds__(256, 1) void mla_dq_kernel(const MlaPrefill p, int 
   load_operand(qf, p.q + (int64_t)(u.r0 + qc) * p.q_stride + head * kQk, L.half);
   load_operand(df, p.dout + ((int64_t)(u.r0 + qc) * p.H + head) * kVDim, L.half);
   const float lse = p.lse2[(int64_t)head * p.Tq + u.r0 + qc];
-  const float delta = p.delta[(int64_t)head * p.Tq + u.r0 + qc];
+  float delta = p.delta[(int64_t)head * p.Tq + u.r0 + qc];
   const float c = p.scale * kLog2e;
   f32x16 dq[6];
 #pragma unroll
@@ -706,6 +712,19 @@ __global__ __launch_bounds__(256, 1) void mla_dq_kernel(const MlaPrefill p, int 
     if (wave_steps > 0) {
       products(s0, dp0, 0, 0, [](int) {});
       mask(s0, 0);
+      if (wave_steps <= kBn / 32) {
+        float d = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) d = fmaf(exp2_fast(fmaf(s0[i], c, -lse)), dp0[i], d);
+        if (wave_steps > 1) {
+          products(s1, dp1, 0, 1, [](int) {});
+          mask(s1, 1);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) d = fmaf(exp2_fast(fmaf(s1[i], c, -lse)), dp1[i], d);
+        }
+        delta = half_sum(d);
+        if (L.half == 0 && qi < Lq) p.delta[(int64_t)head * p.Tq + u.r0 + qi] = delta;
+      }
     }
   }
   int buf = 0;      // of the steps' tile

@@ -130,6 +130,22 @@ def test_requests_do_not_see_each_other(dev):
     assert torch.equal(o2[i], o1) and torch.equal(l2[:, i], l1)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+def test_gradients_of_few_keys_keep_their_precision(dev, causal):
+    # A rounding to BF16 is 2^-7 / sqrt(12) of its power of two, 0.00166 of the values' norm. dQ and dK hold two of
+    # them, of dS and of the result: 0.00235, one and a half single ones with room for the sample. The rounding of the
+    # output must not come in through D = dO . O, where few keys make it as large as theirs.
+    lens = [(n, n) for n in (2, 5, 17, 33, 48, 64)]
+    q, kv, kr, dout, cq, ck = _inputs(dev, lens, 8, 11)
+    tq, tk = torch.from_numpy(cq).to(dev), torch.from_numpy(ck).to(dev)
+    out, lse = fb.fp8bs_mla_prefill(q, kv, kr, tq, tk, SCALE, causal=causal)
+    grads = fb.fp8bs_mla_prefill_bwd(dout, q, kv, kr, out, lse, tq, tk, SCALE, causal=causal)
+    ref = oa.mla_prefill(_f64(q), _f64(kv), _f64(kr), cq, ck, SCALE, causal, _f64(dout))
+    for name, x in zip(("dq", "dkv", "dk_rope"), grads):
+        want = ref[name][0]
+        assert np.linalg.norm(_f64(x) - want) <= 0.0025 * np.linalg.norm(want), name
+
+
 def test_long_rows_against_float32(dev):
     # long enough to rescale often, with ends off every tile: the sampled rows of one head
     lens = [(1500, 2777)]
