@@ -329,27 +329,6 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
   }
 }
 
-// D[h][t] = dO . O, and lse in units of log2 (0 for a query that sees no key,
-// whose scores are all masked): 16 lanes per (token, head) row of 128.
-__global__ __launch_bounds__(256) void mla_delta_kernel(const MlaPrefill p) {
-  const int64_t r = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 4;
-  const int part = threadIdx.x & 15;
-  if (r >= (int64_t)p.Tq * p.H) return;
-  const bf16x8 a = *reinterpret_cast<const bf16x8*>(p.dout + r * kVDim + 8 * part);
-  const bf16x8 b = *reinterpret_cast<const bf16x8*>(p.out + r * kVDim + 8 * part);
-  float v = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v = fmaf((float)a[i], (float)b[i], v);
-#pragma unroll
-  for (int d = 1; d < 16; d <<= 1) v += __shfl_xor(v, d, 64);
-  if (part == 0) {
-    const int64_t at = (r % p.H) * p.Tq + r / p.H;
-    const float lse = p.lse[at];
-    p.delta[at] = v;
-    p.lse2[at] = lse == neg_inf() ? 0.f : lse * kLog2e;
-  }
-}
-
 // Gradients of keys and values: 32 keys are a pair of waves' work, which share
 // a SIMD, while 32 queries at a time pass, in tiles of 64 (Q, dO, lse, D). The
 // first of the pair forms the scores and the weights, hands the weights (FP32)
@@ -603,12 +582,15 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void m
 // staggered by 32 keys as the keys' gradient is; dS needs no sums between
 // workgroups (S and dP are formed a second time instead, 320 of its 512
 // multiplications per query and key, so no result depends on any order).
+// This kernel also forms what the keys' gradient, launched after it, needs of a
+// query: lse in units of log2 (0 if it sees no key: its scores are all masked)
+// and D = dO . O, here where dO is in registers already (a kernel
+// of its own read 134 MB in 24 us for 4096 tokens on 64 heads).
 // D comes from O rounded to BF16. Over many keys that rounding is far below
 // those of the weights and of dS; where few keys make O as large as V it is
 // their equal (requests of up to 260 tokens: error of dQ and dK 0.0028 of their
 // norm instead of 0.0024). A wave whose queries see the first tile alone forms
-// D = sum_j P_j dP_j in FP32 instead, for the keys' gradient too, which is
-// launched after this.
+// D = sum_j P_j dP_j in FP32 instead.
 __global__ __launch_bounds__(256, 1) void mla_dq_kernel(const MlaPrefill p, int units) {
   constexpr int NW = 4, BM = 32 * NW, NBUF = 3;
   using Load = KeyLoader<NW>;
@@ -652,8 +634,9 @@ __global__ __launch_bounds__(256, 1) void mla_dq_kernel(const MlaPrefill p, int 
   bf16x8 qf[12], df[8];
   load_operand(qf, p.q + (int64_t)(u.r0 + qc) * p.q_stride + head * kQk, L.half);
   load_operand(df, p.dout + ((int64_t)(u.r0 + qc) * p.H + head) * kVDim, L.half);
-  const float lse = p.lse2[(int64_t)head * p.Tq + u.r0 + qc];
-  float delta = p.delta[(int64_t)head * p.Tq + u.r0 + qc];
+  bf16x8 of[8];
+  load_operand(of, p.out + ((int64_t)(u.r0 + qc) * p.H + head) * kVDim, L.half);
+  float lse = p.lse[(int64_t)head * p.Tq + u.r0 + qc];
   const float c = p.scale * kLog2e;
   f32x16 dq[6];
 #pragma unroll
@@ -667,6 +650,13 @@ __global__ __launch_bounds__(256, 1) void mla_dq_kernel(const MlaPrefill p, int 
       for (int n = 0; n < Load::kLoads; ++n) ld.issue(n, kvt, krt, w, lds + i * kFwdTile);
       loads_end();
     }
+  lse = lse == neg_inf() ? 0.f : lse * kLog2e;
+  float delta = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) delta = fmaf((float)df[i][k], (float)of[i][k], delta);
+  delta = half_sum(delta);
   const int k_at = at256(L), r_at = kNopeTile + at128(L), v_at = kNopeTile + kRopeTile + at256(L);
   const int kt_at = at256t(L), rt_at = kNopeTile + at128t(L);
   constexpr int kAhead = 4;
@@ -723,9 +713,12 @@ __global__ __launch_bounds__(256, 1) void mla_dq_kernel(const MlaPrefill p, int 
           for (int i = 0; i < 16; ++i) d = fmaf(exp2_fast(fmaf(s1[i], c, -lse)), dp1[i], d);
         }
         delta = half_sum(d);
-        if (L.half == 0 && qi < Lq) p.delta[(int64_t)head * p.Tq + u.r0 + qi] = delta;
       }
     }
+  }
+  if (L.half == 0 && qi < Lq) {
+    p.delta[(int64_t)head * p.Tq + u.r0 + qi] = delta;
+    p.lse2[(int64_t)head * p.Tq + u.r0 + qi] = lse;
   }
   int buf = 0;      // of the steps' tile
   // Step j, half `sub` of its tile, whose scores and dP are in s and dp; those of step j+1 go to sn and dpn.
@@ -808,12 +801,23 @@ __global__ __launch_bounds__(256, 1) void mla_dq_kernel(const MlaPrefill p, int 
   }
 }
 
-// dk_rope = sum of the heads' rotary gradients, in head order.
+// dk_rope = sum of the heads' rotary gradients, always in the same order: a
+// workgroup's waves take every fourth head each of 256 numbers, so that enough
+// loads are under way (one thread for all heads of its numbers: 30 us instead
+// of 13 us for 4096 keys on 64 heads, 67 MB).
 __global__ __launch_bounds__(256) void mla_rope_sum_kernel(const MlaPrefill p) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, n = (int64_t)p.Tk * kRopeDim;
-  if (i >= n) return;
+  __shared__ f32x4 sums[3][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t n = (int64_t)p.Tk * kRopeDim, i = ((int64_t)blockIdx.x * 64 + lane) * 4;      // (n: a multiple of 64)
   f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-  for (int h = 0; h < p.H; ++h) sum += *reinterpret_cast<const f32x4*>(p.rope_part + h * n + i);
+  if (i < n) {
+#pragma unroll 4
+    for (int h = w; h < p.H; h += 4) sum += *reinterpret_cast<const f32x4*>(p.rope_part + h * n + i);
+  }
+  if (w > 0) sums[w - 1][lane] = sum;
+  __syncthreads();
+  if (w > 0 || i >= n) return;
+  sum = (sum + sums[0][lane]) + (sums[1][lane] + sums[2][lane]);
   bf16x4 b;
 #pragma unroll
   for (int j = 0; j < 4; ++j) b[j] = (__bf16)sum[j];
@@ -835,16 +839,14 @@ hipError_t launch_mla_prefill(const MlaPrefill& p, hipStream_t stream) {
 }
 
 hipError_t launch_mla_prefill_bwd(const MlaPrefill& p, hipStream_t stream) {
-  const int64_t rows = (int64_t)p.Tq * p.H;
   if (p.Tq > 0) {
-    hipLaunchKernelGGL(mla_delta_kernel, dim3((unsigned)((rows + 15) / 16)), dim3(256), 0, stream, p);
     const int64_t units = blocks(p.Tq, p.B, 128);
     hipLaunchKernelGGL(mla_dq_kernel, dim3(unit_grid(units, p.H)), dim3(256), 0, stream, p, (int)units);
   }
   if (p.Tk > 0) {
     const int64_t units = blocks(p.Tk, p.B, 128);
     hipLaunchKernelGGL(mla_dkv_kernel, dim3(unit_grid(units, p.H)), dim3(512), 0, stream, p, (int)units);
-    hipLaunchKernelGGL(mla_rope_sum_kernel, dim3((unsigned)(((int64_t)p.Tk * kRopeDim / 4 + 255) / 256)), dim3(256), 0,
+    hipLaunchKernelGGL(mla_rope_sum_kernel, dim3((unsigned)(((int64_t)p.Tk * kRopeDim + 255) / 256)), dim3(256), 0,
                        stream, p);
   }
   return hipGetLastError();
