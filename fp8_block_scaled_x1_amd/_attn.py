@@ -19,7 +19,8 @@ CACHE_BF16, CACHE_FP8 = 0, 1
 _i, _i64, _f, _vp = ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
 
 _SIGNATURES = {
-    "fp8bs_mla_prefill": [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i, _i64, _i64, _i, _f, _i, _vp, _vp, _vp],
+    "fp8bs_mla_prefill": [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i, _i64, _i64, _i, _f, _i, _vp, _vp, _vp, _vp],
+    "fp8bs_mla_prefill_workspace_bytes": [_i, _i64, _i64, _i],
     "fp8bs_mla_prefill_bwd": [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i, _i64, _i64, _i, _f, _i,
                               _vp, _vp, _vp, _vp, _vp],
     "fp8bs_mla_prefill_bwd_workspace_bytes": [_i64, _i64, _i],
@@ -122,11 +123,12 @@ def _bytes(fn, device_index, *sizes):
         n = getattr(attn_lib(), fn)(*sizes)
     if n < 0:
         raise _lib.Fp8bsError(fn, n)
-    return max(n, 16)
+    return n
 
 
 def _workspace(fn, device, *sizes):
-    return torch.empty(_bytes(fn, device.index, *sizes), dtype=_u8, device=device)
+    """A tensor of that many bytes, at least 16."""
+    return torch.empty(max(_bytes(fn, device.index, *sizes), 16), dtype=_u8, device=device)
 
 
 def _prefill_args(q, kv, k_rope, cu_q, cu_k):
@@ -154,7 +156,10 @@ def fp8bs_mla_prefill(q, kv, k_rope, cu_q, cu_k, scale, causal=True):
     Tq, H = q.shape[:2]
     out = torch.empty((Tq, H, 128), dtype=_bf16, device=device)
     lse = torch.empty((H, Tq), dtype=_f32, device=device)
-    _call("fp8bs_mla_prefill", device, *ptrs, *sizes, float(scale), int(bool(causal)), out.data_ptr(), lse.data_ptr())
+    need = _bytes("fp8bs_mla_prefill_workspace_bytes", device.index, *sizes[2:])
+    ws = torch.empty(need, dtype=_u8, device=device) if need else None
+    _call("fp8bs_mla_prefill", device, *ptrs, *sizes, float(scale), int(bool(causal)), out.data_ptr(), lse.data_ptr(),
+          ws.data_ptr() if need else None)
     return out, lse
 
 

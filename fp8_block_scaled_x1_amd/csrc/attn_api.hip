@@ -161,14 +161,20 @@ int fp8bs_attn_version(void) { return FP8BS_ATTN_VERSION; }
 int fp8bs_mla_prefill(const uint16_t* q, int64_t q_stride, const uint16_t* kv, int64_t kv_stride,
                       const uint16_t* k_rope, int64_t rope_stride, const int32_t* cu_q, const int32_t* cu_k, int B,
                       int64_t Tq, int64_t Tk, int H, float scale, int causal, uint16_t* out, float* lse,
-                      void* stream) {
+                      void* workspace, void* stream) {
   const int st = prefill_sizes(B, Tq, Tk, H, q_stride, kv_stride, rope_stride, scale);
   if (st != FP8BS_OK) return st;
   if (Tq == 0) return FP8BS_OK;
   if (!q || !cu_q || !cu_k || !out || !lse || (Tk > 0 && (!kv || !k_rope))) return FP8BS_ERR_NULL_PTR;
   if (off16(q) || off16(kv) || off16(k_rope) || off16(out)) return FP8BS_ERR_ALIGN;
   if (off4(cu_q) || off4(cu_k) || off4(lse)) return FP8BS_ERR_ALIGN;
+  const int parts = fp8bs::mla_prefill_parts(B, Tq, Tk, H);
+  if (parts > 1 && !workspace) return FP8BS_ERR_NULL_PTR;
+  if (parts > 1 && off16(workspace)) return FP8BS_ERR_ALIGN;
   fp8bs::MlaPrefill p{};
+  p.parts = parts;
+  p.part = static_cast<float*>(workspace);
+  p.part_ml = parts > 1 ? p.part + parts * Tq * H * 128 : nullptr;
   p.q = q; p.kv = kv; p.k_rope = k_rope;
   p.q_stride = q_stride; p.kv_stride = kv_stride; p.rope_stride = rope_stride;
   p.cu_q = cu_q; p.cu_k = cu_k;
@@ -178,6 +184,13 @@ int fp8bs_mla_prefill(const uint16_t* q, int64_t q_stride, const uint16_t* kv, i
   p.out = out;
   p.lse = lse;
   return status_of(fp8bs::launch_mla_prefill(p, as_stream(stream)));
+}
+
+int64_t fp8bs_mla_prefill_workspace_bytes(int B, int64_t Tq, int64_t Tk, int H) {
+  if (B < 0 || Tq < 0 || Tk < 0 || H < 1) return FP8BS_ERR_SHAPE;
+  if (Tq >= kI32 || Tk >= kI32 || H > 32768) return FP8BS_ERR_TOO_LARGE;
+  const int parts = fp8bs::mla_prefill_parts(B, Tq, Tk, H);
+  return parts > 1 ? parts * Tq * H * (128 + 2) * 4 : 0;
 }
 
 int64_t fp8bs_mla_prefill_bwd_workspace_bytes(int64_t Tq, int64_t Tk, int H) {

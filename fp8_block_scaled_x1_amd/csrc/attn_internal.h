@@ -20,6 +20,10 @@ struct MlaPrefill {
   int causal;
   uint16_t* out;       // [Tq][H][128]
   float* lse;          // [H][Tq]
+  // forward with the keys of a block of queries in parts
+  int parts;           // at most
+  float* part;         // [parts][Tq][H][128]
+  float* part_ml;      // [parts][Tq][H][2]: maximum, sum
   // backward only
   const uint16_t* dout;   // [Tq][H][128]
   float* delta;           // [H][Tq]
@@ -30,6 +34,8 @@ struct MlaPrefill {
   uint16_t* dk_rope;      // [Tk][64]
 };
 
+// Parts that launch_mla_prefill cuts the keys into at these sizes; 1: no workspace.
+int mla_prefill_parts(int B, int64_t Tq, int64_t Tk, int H);
 hipError_t launch_mla_prefill(const MlaPrefill& p, hipStream_t stream);
 hipError_t launch_mla_prefill_bwd(const MlaPrefill& p, hipStream_t stream);
 

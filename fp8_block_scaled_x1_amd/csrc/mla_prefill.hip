@@ -17,6 +17,9 @@
 // All products are 32x32x16 MFMAs, oriented so that the lane that owns a row
 // of the score tile owns it in the next product too.
 
+#include <algorithm>
+#include <cmath>
+
 #include "attn_internal.h"
 #include "device_common.h"
 #include "mla_tiles.h"
@@ -112,13 +115,21 @@ struct KeyLoader {
   }
 };
 
+// Parts that a block of queries with nt tiles of keys is cut into, `most` at
+// the most: no part has fewer than kPartTiles tiles.
+constexpr int kPartTiles = 8;
+__device__ __forceinline__ int parts_of(int nt, int most) { return max(1, min(most, nt / kPartTiles)); }
+constexpr int kJoinSlices = 16;      // workgroups of the join per block of 128 queries: 8 rows each
+
 // Forward: NW waves of 32 queries; key tiles of 64 in three LDS buffers. The
 // loop is staggered by one tile: the scores of tile t+1 are formed (matrix
 // unit) while the weights of tile t are (vector unit: 32 exponentials a lane,
 // about as long as the tile's products), and the values of tile t are added
 // while the maxima of tile t+1 are found; so one wave alone keeps both units
 // busy, and what it waits for is bridged by the SIMD's second wave.
-template <int NW>
+// With SPLIT the tiles of a block are shared by several workgroups, which leave
+// FP32 partials (output, maximum, sum) for the join below.
+template <int NW, bool SPLIT>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) void mla_fwd_kernel(const MlaPrefill p,
                                                                                                  int units) {
   constexpr int BM = 32 * NW, NBUF = 3;
@@ -127,24 +138,37 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int unit, head;
-  if (!unit_of(units, p.H, unit, head)) return;
+  if (!unit_of(SPLIT ? units * p.parts : units, p.H, unit, head)) return;
+  const int part = SPLIT ? unit / units : 0;
+  if (SPLIT) unit -= part * units;
   // the last blocks of a causal request see the most keys: they go first
   const ExpertSlot u = locate_expert(p.cu_q, p.B, p.Tq, units - 1 - unit, BM, 1);
   if (u.e < 0) return;
-  const int k0 = __builtin_amdgcn_readfirstlane(min(max(p.cu_k[u.e], 0), p.Tk));
+  int k0 = __builtin_amdgcn_readfirstlane(min(max(p.cu_k[u.e], 0), p.Tk));
   const int k1 = __builtin_amdgcn_readfirstlane(min(max(p.cu_k[u.e + 1], k0), p.Tk));
-  const int Lq = u.r1 - u.r0, Lk = k1 - k0, off = Lk - Lq;
+  const int Lq = u.r1 - u.r0;
+  int Lk = k1 - k0, off = Lk - Lq;
   const int first = (units - 1 - unit - u.base) * BM;
   const int end = min(first + BM, Lq);                                     // queries of the block
-  const int kend = p.causal ? min(Lk, max(end + off, 0)) : Lk;             // keys any of them sees
-  const int nt = (kend + kBn - 1) / kBn;
+  int kend = p.causal ? min(Lk, max(end + off, 0)) : Lk;                   // keys any of them sees
+  int nt = (kend + kBn - 1) / kBn;
+  const int parts = SPLIT ? parts_of(nt, p.parts) : 1;
+  if (SPLIT) {      // from here on the keys are this part's
+    if (part >= parts) return;
+    const int t0 = nt * part / parts, skip = t0 * kBn;
+    nt = nt * (part + 1) / parts - t0;
+    k0 += skip;
+    Lk -= skip;
+    off -= skip;
+    kend = min(kend - skip, nt * kBn);
+  }
 
   const TileLane L(lane);
   const int qi = first + 32 * w + L.row;                                   // this lane's query
   const int qc = min(qi, Lq - 1);
   const int see = p.causal ? min(Lk, qi + off + 1) : Lk;                   // keys it sees
   const int wave_all = p.causal ? min(Lk, first + 32 * w + off + 1) : Lk;  // keys all the wave's queries see
-  const int wave_any = p.causal ? min(kend, max(first + 32 * w + 32 + off, 0)) : Lk;
+  const int wave_any = p.causal ? min(kend, max(first + 32 * w + 32 + off, 0)) : kend;
   const int wave_nt = first + 32 * w < Lq ? (wave_any + kBn - 1) / kBn : 0;      // its tiles: the first ones
 
   const uint16_t* kv = p.kv + (int64_t)k0 * p.kv_stride + head * (kNope + kVDim);
@@ -312,7 +336,22 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
   }
 
   l = half_sum(l);
-  if (qi < Lq) {
+  if (SPLIT && parts > 1) {
+    if (qi < Lq) {
+      const int64_t at = ((int64_t)part * p.Tq + u.r0 + qi) * p.H + head;
+      float* op = p.part + at * kVDim + 4 * L.half;
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f32x4 v;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = o[d][4 * i + j];
+          *reinterpret_cast<f32x4*>(op + 32 * d + 8 * i) = v;
+        }
+      if (L.half == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(m, l);
+    }
+  } else if (qi < Lq) {
     const float inv = l > 0.f ? 1.f / l : 0.f;
     uint16_t* op = p.out + ((int64_t)(u.r0 + qi) * p.H + head) * kVDim + 4 * L.half;
 #pragma unroll
@@ -326,6 +365,57 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
       }
     if (L.half == 0)
       p.lse[(int64_t)head * p.Tq + u.r0 + qi] = l > 0.f ? (m + __builtin_log2f(l)) * kLn2 : neg_inf();
+  }
+}
+
+// Joins the parts of the blocks that have more than one: 32 lanes a row.
+__global__ __launch_bounds__(256) void mla_fwd_join_kernel(const MlaPrefill p, int units) {
+  constexpr int BM = 128, kAtOnce = 8;      // parts whose loads are under way together
+  const int lane = threadIdx.x & 31, slot = threadIdx.x >> 5;
+  const int unit = blockIdx.x / kJoinSlices / p.H, head = blockIdx.x / kJoinSlices % p.H, slice = blockIdx.x % kJoinSlices;
+  const ExpertSlot u = locate_expert(p.cu_q, p.B, p.Tq, unit, BM, 1);
+  if (u.e < 0) return;
+  const int k0 = min(max(p.cu_k[u.e], 0), p.Tk), Lk = min(max(p.cu_k[u.e + 1], k0), p.Tk) - k0;
+  const int Lq = u.r1 - u.r0, first = (unit - u.base) * BM, end = min(first + BM, Lq);
+  const int kend = p.causal ? min(Lk, max(end + Lk - Lq, 0)) : Lk;
+  const int parts = parts_of((kend + kBn - 1) / kBn, p.parts);
+  if (parts == 1) return;
+  const int64_t step = (int64_t)p.Tq * p.H;      // rows from part to part
+  if (const int r = first + 8 * slice + slot; r < end) {
+    const int64_t at = (int64_t)(u.r0 + r) * p.H + head;
+    float m = neg_inf(), l = 0.f;
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    for (int i0 = 0; i0 < parts; i0 += kAtOnce) {
+      f32x4 v[kAtOnce];
+      float2 ml[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int64_t row = at + min(i0 + k, parts - 1) * step;
+        v[k] = *reinterpret_cast<const f32x4*>(p.part + row * kVDim + 4 * lane);
+        ml[k] = *reinterpret_cast<const float2*>(p.part_ml + 2 * row);
+        if (i0 + k >= parts) ml[k] = make_float2(neg_inf(), 0.f);
+      }
+      float mn = m;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) mn = fmaxf(mn, ml[k].x);
+      const float ref = mn == neg_inf() ? 0.f : mn, old = exp2_fast(m - ref);
+      l *= old;
+      o *= old;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const float x = exp2_fast(ml[k].x - ref);
+        l = fmaf(ml[k].y, x, l);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = i0 + k < parts ? fmaf(v[k][j], x, o[j]) : o[j];
+      }
+      m = mn;
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    bf16x4 b;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b[j] = (__bf16)(o[j] * inv);
+    *reinterpret_cast<bf16x4*>(p.out + at * kVDim + 4 * lane) = b;
+    if (lane == 0) p.lse[(int64_t)head * p.Tq + u.r0 + r] = l > 0.f ? (m + __builtin_log2f(l)) * kLn2 : neg_inf();
   }
 }
 
@@ -829,12 +919,50 @@ int64_t blocks(int64_t tokens, int B, int rows) { return (tokens + rows - 1) / r
 
 }  // namespace
 
+static bool wide_blocks(int64_t Tq, int B, int H) { return blocks(Tq, B, 256) * H >= 1024; }
+
+// Few blocks of queries behind many keys leave compute units without work or
+// with a second block after the others are done. Cut into s parts, W blocks are
+// ceil(W s / CUs) parts after each other on a compute unit (or, causal, the
+// longest alone), a part takes 1.3 us per tile and 4 us to begin and end, and
+// writing, reading and joining its rows adds 27 ns of the device's time, 8 us
+// with the join's launch. The rule takes the s that this makes cheapest, for
+// requests of average length (the host does not know theirs).
+// Measured, whole against the rule's parts: 512 queries behind 8000 tokens on
+// 16 heads 167 and 64 us; 100 behind 100000 on 8 heads 2010 and 158 us; 550 and
+// 512 behind 7400 on 32 heads 315 and 272 us. Left whole by the rule, whole
+// against two parts: 512 behind 8000 on 128 heads 433 and 456 us, two of 512
+// with 1200 keys on 16 heads 35.2 and 37.3 us.
+int mla_prefill_parts(int B, int64_t Tq, int64_t Tk, int H) {
+  if (B < 1 || wide_blocks(Tq, B, H)) return 1;
+  constexpr double kUnits = 256, kTileUs = 1.3, kEndsUs = 4, kJoinUs = 8, kRowsUs = 0.027;
+  constexpr int kMost = 16;
+  const double q = (double)Tq / B, longest = (double)Tk / B / kBn, mean = std::max(longest - q / (2 * kBn), longest / 2);
+  const double W = std::ceil(q / 128) * B * H;
+  int parts = 1;
+  double best = 0;
+  for (int s = 1; s <= kMost && (s == 1 || s * kPartTiles <= longest); ++s) {
+    const double us = std::max(std::ceil(W * s / kUnits) * (mean / s * kTileUs + kEndsUs), longest / s * kTileUs + kEndsUs) +
+                      (s > 1 ? kJoinUs + W * s * kRowsUs : 0);
+    if (s == 1 || us < best) {
+      best = us;
+      parts = s;
+    }
+  }
+  return parts;
+}
+
 hipError_t launch_mla_prefill(const MlaPrefill& p, hipStream_t stream) {
   const int64_t wide = blocks(p.Tq, p.B, 256), units = blocks(p.Tq, p.B, 128);
-  if (wide * p.H >= 1024)
-    hipLaunchKernelGGL(mla_fwd_kernel<8>, dim3(unit_grid(wide, p.H)), dim3(512), 0, stream, p, (int)wide);
-  else
-    hipLaunchKernelGGL(mla_fwd_kernel<4>, dim3(unit_grid(units, p.H)), dim3(256), 0, stream, p, (int)units);
+  if (wide_blocks(p.Tq, p.B, p.H)) {
+    hipLaunchKernelGGL((mla_fwd_kernel<8, false>), dim3(unit_grid(wide, p.H)), dim3(512), 0, stream, p, (int)wide);
+  } else if (p.parts == 1) {
+    hipLaunchKernelGGL((mla_fwd_kernel<4, false>), dim3(unit_grid(units, p.H)), dim3(256), 0, stream, p, (int)units);
+  } else {
+    hipLaunchKernelGGL((mla_fwd_kernel<4, true>), dim3(unit_grid(units * p.parts, p.H)), dim3(256), 0, stream, p,
+                       (int)units);
+    hipLaunchKernelGGL(mla_fwd_join_kernel, dim3(unit_grid(units * kJoinSlices, p.H)), dim3(256), 0, stream, p, (int)units);
+  }
   return hipGetLastError();
 }
 

@@ -56,12 +56,15 @@ enum fp8bs_cache { FP8BS_CACHE_BF16 = 0, FP8BS_CACHE_FP8 = 1 };
  *   out     [Tq][H][128]  BF16      lse [H][Tq] float32
  * Strides: multiples of 8, at least a token's numbers, below 2^24. Scores, statistics and
  * sums are FP32; probabilities are rounded to BF16 for the matrix unit.
- * scale finite and > 0 (else FP8BS_ERR_VALUE); H >= 1.
+ * scale finite and > 0 (else FP8BS_ERR_VALUE); H >= 1. workspace: at least
+ * fp8bs_mla_prefill_workspace_bytes(B, Tq, Tk, H) bytes, for the parts of few
+ * queries' many keys (0 bytes where there are none: then it may be NULL).
  */
 FP8BS_API int fp8bs_mla_prefill(const uint16_t* q, int64_t q_stride, const uint16_t* kv, int64_t kv_stride,
                       const uint16_t* k_rope, int64_t rope_stride, const int32_t* cu_q,
                       const int32_t* cu_k, int B, int64_t Tq, int64_t Tk, int H, float scale,
-                      int causal, uint16_t* out, float* lse, void* stream);
+                      int causal, uint16_t* out, float* lse, void* workspace, void* stream);
+FP8BS_API int64_t fp8bs_mla_prefill_workspace_bytes(int B, int64_t Tq, int64_t Tk, int H);
 
 /*
  * Its gradients: with out and lse as fp8bs_mla_prefill wrote them for the same

@@ -27,7 +27,7 @@ def L():
 
 def test_header_and_exports(L):
     assert set(_declared()) == {
-        "fp8bs_mla_prefill", "fp8bs_mla_prefill_bwd", "fp8bs_mla_prefill_bwd_workspace_bytes", "fp8bs_mla_decode",
+        "fp8bs_mla_prefill", "fp8bs_mla_prefill_workspace_bytes", "fp8bs_mla_prefill_bwd", "fp8bs_mla_prefill_bwd_workspace_bytes", "fp8bs_mla_decode",
         "fp8bs_mla_decode_shared", "fp8bs_mla_decode_workspace_bytes", "fp8bs_verify_drafts",
         "fp8bs_verify_drafts_workspace_bytes", "fp8bs_attn_version"}
     raw = ctypes.CDLL(fb.LIB_PATH)
@@ -39,7 +39,7 @@ def test_header_and_exports(L):
 
 def _prefill(L, **kw):
     a = dict(q=P, qs=384, kv=P, kvs=512, r=P, rs=64, cq=P, ck=P, B=2, Tq=10, Tk=12, H=2, scale=0.1, causal=1, out=P,
-             lse=P, stream=NULL)
+             lse=P, ws=NULL, stream=NULL)
     a.update(kw)
     return L.fp8bs_mla_prefill(*a.values())
 
@@ -57,6 +57,18 @@ def test_prefill_refusals(L):
         assert _prefill(L, scale=s) == -9
     assert _prefill(L, Tq=1 << 31) == -7
     assert _prefill(L, H=70000, qs=70000 * 192, kvs=70000 * 256) == -7
+
+
+def test_prefill_workspace(L):
+    ws = L.fp8bs_mla_prefill_workspace_bytes
+    assert ws(-1, 1, 1, 1) == -2 and ws(1, 1, 1, 0) == -2 and ws(1, 1 << 31, 1, 1) == -7
+    assert ws(2, 300, 300, 16) == 0 and ws(0, 0, 0, 4) == 0          # few keys: nothing to share
+    assert ws(2, 40000, 40000, 128) == 0                             # more than enough blocks
+    # few queries, many keys: whole parts of [Tq][H] rows of 128 numbers, a maximum and a sum
+    n = ws(1, 20, 50000, 4)
+    assert n > 0 and n % (20 * 4 * 130 * 4) == 0 and n // (20 * 4 * 130 * 4) >= 2
+    many = dict(B=1, Tq=20, Tk=50000, H=4, qs=768, kvs=1024)
+    assert _prefill(L, **many, ws=NULL) == -1 and _prefill(L, **many, ws=P + 8) == -3
 
 
 def test_prefill_bwd_refusals(L):

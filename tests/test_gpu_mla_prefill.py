@@ -75,6 +75,19 @@ def test_against_oracle(dev, lens, causal):
     _check(dev, lens, 3, causal, seed=len(lens))
 
 
+@pytest.mark.parametrize("lens", [
+    [(3, 5000)],
+    [(1, 1300), (130, 2049), (33, 700)],            # parts ending on and off the causal edge, one block without parts
+    [(257, 1500), (1, 1), (0, 4000), (64, 1023)],
+    [(1500, 1200)],                                 # causal: the first 300 queries see nothing
+], ids=str)
+@pytest.mark.parametrize("causal", [True, False])
+def test_keys_in_parts(dev, lens, causal):
+    sizes = len(lens), sum(a for a, _ in lens), sum(b for _, b in lens)
+    assert fb.attn_lib().fp8bs_mla_prefill_workspace_bytes(*sizes, 2) > 0
+    _check(dev, lens, 2, causal, seed=3)
+
+
 @pytest.mark.parametrize("H", [1, 2, 5, 8, 16, 24])
 def test_head_counts(dev, H):
     _check(dev, [(77, 77), (1, 130)], H, True, seed=H)
@@ -161,8 +174,9 @@ def test_long_rows_against_float32(dev):
             _inside(lse[h, row:row + 1], (l, bl), f"lse {row} head {h}")
 
 
-def test_same_bits_every_time_and_in_a_graph(dev):
-    q, kv, kr, dout, cq, ck = _inputs(dev, [(130, 130), (70, 200)], 8, 9)
+@pytest.mark.parametrize("lens", [[(130, 130), (70, 200)], [(70, 3000)]], ids=str)      # (whole, in parts)
+def test_same_bits_every_time_and_in_a_graph(dev, lens):
+    q, kv, kr, dout, cq, ck = _inputs(dev, lens, 8, 9)
     tq, tk = torch.from_numpy(cq).to(dev), torch.from_numpy(ck).to(dev)
 
     def step():
