@@ -1,11 +1,9 @@
 // Device helpers shared by the attention kernels: operand types, the direct
 // global-to-LDS loads, transposing LDS reads and small wave reductions.
 //
-// MFMA register layouts used throughout (lane l of 64):
-//   16x16x32: A row l%16 / B column l%16, k = 8*(l/16) .. +7;
-//             D column l%16, rows 4*(l/16) + i, i < 4.
-//   32x32x16: A row l%32 / B column l%32, k = 8*(l/32) .. +7;
-//             D column l%32, rows 8*(i/4) + 4*(l/32) + i%4, i < 16.
+// MFMA register layout used throughout (32x32x16, lane l of 64): A row l%32 /
+// B column l%32, k = 8*(l/32) .. +7; D column l%32, rows 8*(i/4) + 4*(l/32) +
+// i%4, i < 16.
 // The inner index of a product may be numbered freely as long as A and B
 // agree. Every kernel here uses that: with scores formed as keys x queries, a
 // lane's D rows (4 consecutive keys at a time) are taken directly as its
@@ -118,9 +116,6 @@ __device__ __forceinline__ float half_sum(float v) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-__device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
 __device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }

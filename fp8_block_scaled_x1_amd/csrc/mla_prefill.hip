@@ -55,29 +55,11 @@ constexpr int kBn = 64;      // keys per tile
 constexpr int kNopeTile = kBn * 256, kRopeTile = kBn * 128, kVTile = kBn * 256;
 constexpr int kFwdTile = kNopeTile + kRopeTile + kVTile;
 
-template <int NW>
-__device__ __forceinline__ void load_keys(const MlaPrefill& p, const uint16_t* kv, const uint16_t* kr, int row0,
-                                          int last, int w, int lane, uint32_t lds) {
-  load_tile256<kBn, NW>(kv, p.kv_stride, row0, last, w, lane, lds);
-  load_tile128<kBn, NW>(kr, p.rope_stride, row0, last, w, lane, lds + kNopeTile);
-  load_tile256<kBn, NW>(kv + kNope, p.kv_stride, row0, last, w, lane, lds + kNopeTile + kRopeTile);
-}
-
 // The lane's 32x32x16 operand of 192 query columns (or, offset, 128 of dO).
 template <int N>
 __device__ __forceinline__ void load_operand(bf16x8 (&f)[N], const uint16_t* row, int half) {
 #pragma unroll
   for (int ks = 0; ks < N; ++ks) f[ks] = *reinterpret_cast<const bf16x8*>(row + 16 * ks + 8 * half);
-}
-
-// S^T of 32 keys of the tile (rows) by the wave's 32 queries (columns).
-__device__ __forceinline__ f32x16 scores(const char* t, const TileLane& L, int key0, const bf16x8 (&qf)[12]) {
-  f32x16 s = zero16();
-#pragma unroll
-  for (int ks = 0; ks < 8; ++ks) s = mfma32(rows256(t, L, key0, ks), qf[ks], s);
-#pragma unroll
-  for (int ks = 0; ks < 4; ++ks) s = mfma32(rows128(t + kNopeTile, L, key0, ks), qf[8 + ks], s);
-  return s;
 }
 
 // The weights' reference follows the running maximum only once that is more
@@ -126,7 +108,20 @@ constexpr int kJoinSlices = 16;      // workgroups of the join per block of 128 
 // unit) while the weights of tile t are (vector unit: 32 exponentials a lane,
 // about as long as the tile's products), and the values of tile t are added
 // while the maxima of tile t+1 are found; so one wave alone keeps both units
-// busy, and what it waits for is bridged by the SIMD's second wave.
+// busy, and what it waits for is bridged by the SIMD's second wave. (Formed and
+// weighed tile by tile, 550 queries behind 7500 tokens took 238 us, so 190.)
+//
+// 256 queries (NW = 8) halve the tiles' traffic into LDS and give each SIMD
+// its second wave; 128 (NW = 4) give twice the workgroups. The rule in
+// launch_mla_prefill takes 256 where that leaves every compute unit four
+// workgroups (two requests of 8192 tokens on 128 heads: 3.74 ms, with 128
+// queries 4.08 ms), and 128 otherwise (two of 512 behind 8000 on 32 heads:
+// 190 us, with 256 queries 268 us).
+//
+// Bound by the matrix unit's rate at the clock that the power limit leaves:
+// two requests of 6000 to 8192 tokens on 128 heads run at 1.04 PFLOP/s, 0.49 of
+// the unit's cycles at 1.87 GHz; loads, barriers and exponentials are worth 4
+// to 11% each.
 // With SPLIT the tiles of a block are shared by several workgroups, which leave
 // FP32 partials (output, maximum, sum) for the join below.
 template <int NW, bool SPLIT>
@@ -427,7 +422,10 @@ __global__ __launch_bounds__(256) void mla_fwd_join_kernel(const MlaPrefill p, i
 // no more than 48 + 64 (32 + 96) registers of operands and sums, so both fit
 // in 256 and one's vector work runs beside the other's products. (One wave for
 // both needs 240 for operands and sums alone; alone on its SIMD, with the rest
-// in accumulation registers, it took 20-60% longer.)
+// in accumulation registers, it took 20-60% longer.) 4096 tokens on 64 heads:
+// 0.83 ms, 0.83 PFLOP/s; 20 products of 32 cycles a wave and step leave the
+// matrix unit 0.37 busy at 2.2 GHz, the rest is what a step's chain waits for:
+// products, exponentials, LDS and the barrier between the two waves.
 template <int N>
 struct Const {
   static constexpr int value = N;
@@ -671,7 +669,8 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void m
 // Gradient of the queries: 4 waves of 32 queries over tiles of 64 keys,
 // staggered by 32 keys as the keys' gradient is; dS needs no sums between
 // workgroups (S and dP are formed a second time instead, 320 of its 512
-// multiplications per query and key, so no result depends on any order).
+// multiplications per query and key, so no result depends on any order). 4096
+// tokens on 64 heads: 0.64 ms, 0.86 PFLOP/s, bound as the keys' gradient is.
 // This kernel also forms what the keys' gradient, launched after it, needs of a
 // query: lse in units of log2 (0 if it sees no key: its scores are all masked)
 // and D = dO . O, here where dO is in registers already (a kernel

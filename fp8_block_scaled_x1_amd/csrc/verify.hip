@@ -13,6 +13,10 @@
 //
 // Only one row of p (and of q) per request is read, once for the sums of its
 // chunks and, for the one chunk that holds the token, once more (from L2).
+// Chunks of 8192 entries give a request 16 workgroups at a vocabulary of 129280.
+// One request: 11 us in a graph, the latency of two launches; 96 requests with
+// 4 drafts, FP32: 26 us, 87 MB in 19 us (4.6 TB/s), then 8 us for the one chunk
+// of each request, again the latency of a launch and of a chunk's loads.
 
 #include "attn_common.h"
 #include "attn_internal.h"
@@ -232,7 +236,8 @@ void launch(const VerifyDrafts& v, hipStream_t stream) {
 int64_t verify_chunks(int64_t V) { return (V + kChunk - 1) / kChunk; }
 
 hipError_t launch_verify_drafts(const VerifyDrafts& v, bool bf16, hipStream_t stream) {
-  // rows of whole groups of four entries, all of them aligned: wide loads
+  // Rows of whole groups of four entries, all of them aligned: wide loads (96
+  // requests, FP32: 28 us; one entry at a time, vocabulary 129281, 42 us).
   const uintptr_t at = reinterpret_cast<uintptr_t>(v.p) | reinterpret_cast<uintptr_t>(v.q);
   const bool vec = v.V % 4 == 0 && at % (bf16 ? 8 : 16) == 0;
   if (bf16)

@@ -96,7 +96,8 @@ FP8BS_API int64_t fp8bs_mla_prefill_bwd_workspace_bytes(int64_t Tq, int64_t Tk, 
  *          cache_rope unused (NULL)
  *          FP8BS_CACHE_FP8: E4M3 codes [pages][page][512] of the latent
  *          numbers, their scales cache_scales float32 [pages][page][4], one per
- *          128 (codes and scales of a token as fp8_quant_act_1x128 gives them),
+ *          128 (codes and scales as fp8_quant_act_1x128 gives them, the scales
+ *          transposed: here a token's four lie together),
  *          and cache_rope BF16 [pages][page][64]
  *   table  [B][table_width] int32: token j of request b is in slot j % page of
  *          page table[b][j / page]; entries are clamped into [0, pages), those
