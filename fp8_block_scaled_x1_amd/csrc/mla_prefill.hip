@@ -119,8 +119,8 @@ constexpr int kJoinSlices = 16;      // workgroups of the join per block of 128 
 // 190 us, with 256 queries 268 us).
 //
 // Bound by the matrix unit's rate at the clock that the power limit leaves:
-// two requests of 6000 to 8192 tokens on 128 heads run at 1.04 PFLOP/s, 0.49 of
-// the unit's cycles at 1.87 GHz; loads, barriers and exponentials are worth 4
+// two requests of 6000 to 8192 tokens on 128 heads run at 1.04 PFLOP/s, 0.53 of
+// the unit's cycles at 1.9 GHz; loads, barriers and exponentials are worth 4
 // to 11% each.
 // With SPLIT the tiles of a block are shared by several workgroups, which leave
 // FP32 partials (output, maximum, sum) for the join below.
@@ -423,8 +423,8 @@ __global__ __launch_bounds__(256) void mla_fwd_join_kernel(const MlaPrefill p, i
 // in 256 and one's vector work runs beside the other's products. (One wave for
 // both needs 240 for operands and sums alone; alone on its SIMD, with the rest
 // in accumulation registers, it took 20-60% longer.) 4096 tokens on 64 heads:
-// 0.83 ms, 0.83 PFLOP/s; 20 products of 32 cycles a wave and step leave the
-// matrix unit 0.37 busy at 2.2 GHz, the rest is what a step's chain waits for:
+// 0.81 ms, 0.85 PFLOP/s; 20 products of 32 cycles a wave and step leave the
+// matrix unit 0.39 busy at 2.2 GHz, the rest is what a step's chain waits for:
 // products, exponentials, LDS and the barrier between the two waves.
 template <int N>
 struct Const {
@@ -670,7 +670,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void m
 // staggered by 32 keys as the keys' gradient is; dS needs no sums between
 // workgroups (S and dP are formed a second time instead, 320 of its 512
 // multiplications per query and key, so no result depends on any order). 4096
-// tokens on 64 heads: 0.64 ms, 0.86 PFLOP/s, bound as the keys' gradient is.
+// tokens on 64 heads: 0.63 ms, 0.87 PFLOP/s, bound as the keys' gradient is.
 // This kernel also forms what the keys' gradient, launched after it, needs of a
 // query: lse in units of log2 (0 if it sees no key: its scores are all masked)
 // and D = dO . O, here where dO is in registers already (a kernel
