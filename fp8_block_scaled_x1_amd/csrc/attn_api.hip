@@ -6,6 +6,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "attn_internal.h"
 #include "fp8bs_attn.h"
 
@@ -46,7 +48,7 @@ struct DecodeSizes {
   int B;                        // requests
   int64_t rows, all_rows;       // of a request, of all
   int64_t max_len;
-  int block_rows, groups;
+  int groups;
   int64_t row_blocks;
   int64_t pieces;               // partials of a request's rows
   int64_t bytes_out() const { return align256(4 * pieces * rows * 512); }
@@ -61,8 +63,7 @@ int decode_sizes(int B, int64_t rows, int64_t all_rows, int64_t width, int page,
   s.max_len = width * page;
   const int64_t tiles = (int64_t)B * ((s.max_len + kTile - 1) / kTile);
   if (tiles >= kI32) return FP8BS_ERR_TOO_LARGE;
-  s.block_rows = fp8bs::mla_decode_block_rows(rows);
-  s.row_blocks = (rows + s.block_rows - 1) / s.block_rows;
+  s.row_blocks = (rows + fp8bs::kMlaDecodeBlockRows - 1) / fp8bs::kMlaDecodeBlockRows;
   s.groups = fp8bs::mla_decode_groups(s.row_blocks, tiles);
   if (s.groups * s.row_blocks > kGridMax) return FP8BS_ERR_TOO_LARGE;
   s.pieces = 2 * (int64_t)s.groups + (joined ? B : 0);
@@ -77,7 +78,7 @@ int decode_plan(int B, int T, int H, int64_t width, int page, int64_t prefix_pag
   int st = decode_sizes(B, rows, all, width, page, prefix_pages > 0, own);
   if (st != FP8BS_OK || prefix_pages == 0) return st;
   // the prefix: every block of everyone's rows is a request over the same tokens
-  const int block = fp8bs::mla_decode_block_rows(all);
+  const int block = (int)std::max<int64_t>(1, std::min<int64_t>(all, fp8bs::kMlaDecodeBlockRows));
   return decode_sizes((int)((all + block - 1) / block), block, all, prefix_pages, page, true, prefix);
 }
 
@@ -105,7 +106,6 @@ void fill(fp8bs::MlaDecode& p, const uint16_t* q, const void* cache, const float
   p.page_shift = 31 + L;
   p.page_magic = (uint32_t)(((uint64_t)1 << (31 + L)) / (uint64_t)page + 1);
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.block_rows = s.block_rows;
   p.row_blocks = (int)s.row_blocks;
   p.groups = s.groups;
   p.join = join;

@@ -17,7 +17,7 @@
 // rows in one group; the row blocks of a group sit on one XCD, next to each
 // other in time, so the L2 serves the tiles to all but the first.
 //
-// RT teams (1 or 2) of four waves, 32 rows each, share the tiles in LDS. A
+// Two teams of four waves, 32 rows each, share the tiles in LDS. A
 // wave forms the partial scores of 32 tokens over half of the key's columns
 // (so it holds 32 x 288 query numbers only), trades one half of them for its
 // partner's (the same tokens, the other columns), and has the scores of 16
@@ -25,7 +25,7 @@
 // order in which the value product's operand wants them, and adds the 64
 // tokens' values into its 32 x 128 part of the output. No product is formed
 // twice, and 72 + 64 + 16 registers of queries, output and scores leave room
-// for operands to be fetched ahead, with two waves per SIMD for RT = 2. The
+// for operands to be fetched ahead, with two waves per SIMD. The
 // row maxima need no exchange of their own: the weights are taken against a
 // reference that the team shares and that is only raised (a second exchange,
 // for all) when some wave finds a score 2^8 above it.
@@ -244,12 +244,23 @@ struct ValueFeed {
   }
 };
 
-template <int RT, bool FP8, int NBUF>
-__global__ __launch_bounds__(256 * RT) __attribute__((amdgpu_waves_per_eu(2))) void mla_decode_kernel(
-    const MlaDecode p) {
-  static_assert(RT == 1 || RT == 2, "row teams");
+constexpr int kTeams = kMlaDecodeBlockRows / 32;
+
+// One problem, or two that do not wait for each other (a prefix and the
+// requests' own tokens): workgroups from `split` on belong to the second.
+struct Problems {
+  MlaDecode p[2];
+  int split;
+};
+
+template <bool FP8, int NBUF, bool TWO>
+__global__ __launch_bounds__(256 * kTeams) __attribute__((amdgpu_waves_per_eu(2))) void mla_decode_kernel(
+    const Problems problems) {
+  const bool second = TWO && (int)blockIdx.x >= problems.split;
+  const MlaDecode& p = problems.p[second];
+  const int block = blockIdx.x - (second ? problems.split : 0);
   using T = Tile<FP8>;
-  constexpr int NW = 4 * RT, kRows = kTile / NW;        // waves; rows of a tile that each loads
+  constexpr int NW = 4 * kTeams, kRows = kTile / NW;        // waves; rows of a tile that each loads
   using Load = Loader<FP8, kRows>;
   using Values = ValueFeed<FP8>;
   constexpr int kLoads = Load::kLoads;
@@ -273,9 +284,9 @@ __global__ __launch_bounds__(256 * RT) __attribute__((amdgpu_waves_per_eu(2))) v
 
   // workgroup -> (group, row block): workgroups are dealt over the XCDs one by
   // one; renumbered so that an XCD's are consecutive, row blocks of a group first
-  const int per = gridDim.x / kAttnXcds, rest = gridDim.x % kAttnXcds;
-  const int xcd = blockIdx.x % kAttnXcds;
-  const int wg = xcd * per + min(xcd, rest) + blockIdx.x / kAttnXcds;
+  const int blocks = p.groups * p.row_blocks, per = blocks / kAttnXcds, rest = blocks % kAttnXcds;
+  const int xcd = block % kAttnXcds;
+  const int wg = xcd * per + min(xcd, rest) + block / kAttnXcds;
   const int g = wg / p.row_blocks;
   Cursor cur = first_tile(p, g);
   if (cur.left == 0) return;
@@ -333,8 +344,9 @@ __global__ __launch_bounds__(256 * RT) __attribute__((amdgpu_waves_per_eu(2))) v
   }
   const int scale0 = T::kLatentBytes + T::kRopeBytes + 16 * L.half;      // [group][token]
 
-  const int row = ((wg - g * p.row_blocks) * RT + rt) * 32 + L.row;      // this lane's row
+  const int row = ((wg - g * p.row_blocks) * kTeams + rt) * 32 + L.row;  // this lane's row
   const int late = p.tokens - 1 - min(row, p.rows - 1) / p.heads;        // newest tokens hidden from it
+  const bool idle = __builtin_amdgcn_readfirstlane(row) >= p.rows;       // a team without rows
 
   bf16x8 qf[18];
   f32x16 acc[4];
@@ -361,6 +373,16 @@ __global__ __launch_bounds__(256 * RT) __attribute__((amdgpu_waves_per_eu(2))) v
     operands_loaded();
 
     for (bool last = false; !last;) {
+      auto step = [&] {
+        last = cur.tile + 1 == cur.tiles || cur.left == 1;
+        if (last) return;
+        advance(p, cur);
+        buf = buf + 1 == NBUF ? 0 : buf + 1;
+      };
+      // any wave's wish to raise the reference: the answer is the same for all
+      auto raised = [&] {
+        return __any(*reinterpret_cast<const float*>(slots + (lane % NW) * kSlot + kProbBytes + 128) != 0.f) != 0;
+      };
       if (nxt.left > 0 && NBUF > 2)
         attn_wait<kLoads>();
       else
@@ -426,6 +448,19 @@ __global__ __launch_bounds__(256 * RT) __attribute__((amdgpu_waves_per_eu(2))) v
             }
         }
       };
+      if (idle) {      // its share of the loads, and the barriers of the others
+        if (nxt.left > 0) {
+          const Load ld = start_next(buf == 0 ? NBUF - 1 : buf - 1);
+#pragma unroll
+          for (int n = 0; n < kLoads; ++n) ld.issue(n);
+        }
+        if (lane == 0) my_stat[32] = 0.f;
+        attn_barrier();
+        attn_barrier();
+        if (raised()) attn_barrier();
+        step();
+        continue;
+      }
       if (nxt.left > 0) {
         const Load ld = start_next(buf == 0 ? NBUF - 1 : buf - 1);
         partial([&](int i) {
@@ -493,8 +528,7 @@ __global__ __launch_bounds__(256 * RT) __attribute__((amdgpu_waves_per_eu(2))) v
       const bool grown = __any(top > m + kSlack);
       if (lane == 0) my_stat[32] = grown ? 1.f : 0.f;
       attn_barrier();
-      // every wave's wish: the answer is the same for all
-      if (__any(*reinterpret_cast<const float*>(slots + (lane % NW) * kSlot + kProbBytes + 128) != 0.f)) {
+      if (raised()) {
         float mn = m;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -534,11 +568,7 @@ __global__ __launch_bounds__(256 * RT) __attribute__((amdgpu_waves_per_eu(2))) v
         if (i + Values::kAhead < 16) vf.fetch(i + Values::kAhead);
       }
       __builtin_amdgcn_sched_barrier(0);
-      last = cur.tile + 1 == cur.tiles || cur.left == 1;
-      if (!last) {
-        advance(p, cur);
-        buf = buf + 1 == NBUF ? 0 : buf + 1;
-      }
+      step();
     }
 
     // sums over the lanes' and the waves' tokens
@@ -732,28 +762,17 @@ int compute_units() {
 
 // A BF16 tile has 74 KB, so two fit; of the FP8 tiles (41 KB) three do, which
 // leaves a tile's loads the time of two.
-template <int RT>
-void launch_rows(const MlaDecode& p, bool fp8, hipStream_t stream) {
-  const dim3 grid((unsigned)((int64_t)p.groups * p.row_blocks));
+template <bool TWO>
+void launch_tiles(const Problems& two, bool fp8, hipStream_t stream) {
+  const MlaDecode& b = two.p[1];
+  const dim3 grid((unsigned)(two.split + (TWO ? (int64_t)b.groups * b.row_blocks : 0)));
   if (fp8)
-    hipLaunchKernelGGL((mla_decode_kernel<RT, true, 3>), grid, dim3(256 * RT), 0, stream, p);
+    hipLaunchKernelGGL((mla_decode_kernel<true, 3, TWO>), grid, dim3(256 * kTeams), 0, stream, two);
   else
-    hipLaunchKernelGGL((mla_decode_kernel<RT, false, 2>), grid, dim3(256 * RT), 0, stream, p);
-}
-
-void launch_tiles(const MlaDecode& p, bool fp8, hipStream_t stream) {
-  if (p.block_rows == 32)
-    launch_rows<1>(p, fp8, stream);
-  else
-    launch_rows<2>(p, fp8, stream);
+    hipLaunchKernelGGL((mla_decode_kernel<false, 2, TWO>), grid, dim3(256 * kTeams), 0, stream, two);
 }
 
 }  // namespace
-
-// Rows per workgroup: 64 halve the tiles' traffic (128 rows of 128 requests: 156
-// us, with 32 each 200 us), and where there are no more than 32 rows the others
-// would be empty (32 rows of 8 requests, FP8: 82 us, with 64 each 99 us).
-int mla_decode_block_rows(int64_t rows) { return rows <= 32 ? 32 : 64; }
 
 // Groups that share the tiles (max_tiles: the most there can be, from the
 // sizes the host knows), so that groups times row blocks fill the device once
@@ -767,17 +786,23 @@ int mla_decode_groups(int64_t row_blocks, int64_t max_tiles) {
 }
 
 hipError_t launch_mla_decode(const MlaDecode& own, const MlaDecode* prefix, bool fp8, hipStream_t stream) {
-  if (prefix) launch_tiles(*prefix, fp8, stream);
-  if (own.max_len > 0) launch_tiles(own, fp8, stream);
+  // A prefix and the requests' own tokens in one launch: alone, neither of two
+  // small problems fills the device (prefix of 1000, 6 requests of 16 heads:
+  // 23 us, in two launches 30 us).
+  const MlaDecode& head = prefix ? *prefix : own;
+  const Problems two{{head, own}, head.groups * (int)head.row_blocks};
+  if (prefix && own.max_len > 0)
+    launch_tiles<true>(two, fp8, stream);
+  else if (prefix || own.max_len > 0)
+    launch_tiles<false>(two, fp8, stream);
   // Few rows have many pieces each: a workgroup per row (whole call with it and
   // with a wave per row: 256 rows of about 28 pieces 82 and 85 us, 96 rows of
   // 6 requests 30 and 35 us); many rows have one or two, and a wave per row has
   // less to set up (16384 rows: 156 us, with a workgroup each 178 us).
-  const MlaDecode& other = prefix ? *prefix : own;
   if (own.all_rows <= 2048)
-    hipLaunchKernelGGL(mla_join_kernel<4>, dim3((unsigned)own.all_rows), dim3(kThreads), 0, stream, own, other);
+    hipLaunchKernelGGL(mla_join_kernel<4>, dim3((unsigned)own.all_rows), dim3(kThreads), 0, stream, own, head);
   else
-    hipLaunchKernelGGL(mla_join_kernel<1>, dim3((unsigned)((own.all_rows + 3) / 4)), dim3(kThreads), 0, stream, own, other);
+    hipLaunchKernelGGL(mla_join_kernel<1>, dim3((unsigned)((own.all_rows + 3) / 4)), dim3(kThreads), 0, stream, own, head);
   return hipGetLastError();
 }
 
