@@ -34,14 +34,15 @@
 // score of its 128 columns (FP32) and the probability that meets its 128
 // output columns, so the latent vector itself is never rounded.
 //
-// Bound, BF16 cache, 64 rows: a tile costs a compute unit 2.9 us, of which the
-// products need 1.0 us (matrix unit 0.36 busy at 2.15 GHz) and its 74 KB into
-// LDS 1.4 us; two tiles fill the LDS, so a tile's phases (scores, exchange,
-// weights, values) follow each other for all waves, with only the next tile's
-// loads beside them. 192 requests of 32 heads behind 16000 common tokens:
-// 0.27 ms, 0.8 PFLOP/s; 128 requests of 300 to 4500 tokens on 128 heads: 0.16 ms
-// with the join, 387 MB. FP8 cache, 32 rows: 256 MB in 74 us, 3.5 TB/s, bound by
-// the codes' conversion and the same phases.
+// Bound, BF16 cache, 64 rows: a tile costs a compute unit 2.9 us from L2, of
+// which the products need 1.0 us (matrix unit 0.36 busy at 2.15 GHz) and its 74
+// KB into LDS 1.4 us; two tiles fill the LDS, so a tile's phases (scores,
+// exchange, weights, values) follow each other for all waves, with only the
+// next tile's loads beside them. 192 requests of 32 heads behind 16000 common
+// tokens: 0.27 ms, 0.8 PFLOP/s. From HBM a tile costs 4.0 us: 128 requests of
+// 300 to 4500 tokens on 128 heads, 387 MB: 0.16 ms with the join. FP8 cache, 32
+// rows: 256 MB in 70 us, 3.7 TB/s, bound by the codes' conversion and the same
+// phases.
 //
 // Roundings below 32 bits: probabilities (times the scale, FP8) to BF16 for
 // the matrix unit (relative 2^-8 at most each, on the terms of a mean), and the output.
@@ -796,8 +797,8 @@ hipError_t launch_mla_decode(const MlaDecode& own, const MlaDecode* prefix, bool
   else if (prefix || own.max_len > 0)
     launch_tiles<false>(two, fp8, stream);
   // Few rows have many pieces each: a workgroup per row (whole call with it and
-  // with a wave per row: 256 rows of about 28 pieces 82 and 85 us, 96 rows of
-  // 6 requests 30 and 35 us); many rows have one or two, and a wave per row has
+  // with a wave per row: 256 rows of about 28 pieces 82 and 85 us, 96 rows
+  // of 6 requests 30 and 35 us, then with two launches before it); many rows have one or two, and a wave per row has
   // less to set up (16384 rows: 156 us, with a workgroup each 178 us).
   if (own.all_rows <= 2048)
     hipLaunchKernelGGL(mla_join_kernel<4>, dim3((unsigned)own.all_rows), dim3(kThreads), 0, stream, own, head);

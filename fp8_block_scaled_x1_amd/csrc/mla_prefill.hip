@@ -109,19 +109,19 @@ constexpr int kJoinSlices = 16;      // workgroups of the join per block of 128 
 // about as long as the tile's products), and the values of tile t are added
 // while the maxima of tile t+1 are found; so one wave alone keeps both units
 // busy, and what it waits for is bridged by the SIMD's second wave. (Formed and
-// weighed tile by tile, 550 queries behind 7500 tokens took 238 us, so 190.)
+// weighed tile by tile, two chunks of 510 queries with 8000 keys on 32 heads
+// took 238 us, so 190.)
 //
 // 256 queries (NW = 8) halve the tiles' traffic into LDS and give each SIMD
 // its second wave; 128 (NW = 4) give twice the workgroups. The rule in
 // launch_mla_prefill takes 256 where that leaves every compute unit four
-// workgroups (two requests of 8192 tokens on 128 heads: 3.74 ms, with 128
-// queries 4.08 ms), and 128 otherwise (two of 512 behind 8000 on 32 heads:
-// 190 us, with 256 queries 268 us).
+// workgroups (two requests of 6000 to 8192 tokens on 128 heads: 3.68 ms, with
+// 128 queries 4.44 ms), and 128 otherwise (the two chunks: 188 us, with 256
+// queries 239 us).
 //
-// Bound by the matrix unit's rate at the clock that the power limit leaves:
-// two requests of 6000 to 8192 tokens on 128 heads run at 1.04 PFLOP/s, 0.53 of
-// the unit's cycles at 1.9 GHz; loads, barriers and exponentials are worth 4
-// to 11% each.
+// Bound by the matrix unit's rate at the clock that the power limit leaves: the
+// two long requests run at 1.0 PFLOP/s, 0.53 of the unit's cycles at 1.9 GHz.
+// Loads, LDS reads and exponentials are worth 8 to 11% each.
 // With SPLIT the tiles of a block are shared by several workgroups, which leave
 // FP32 partials (output, maximum, sum) for the join below.
 template <int NW, bool SPLIT>
