@@ -116,19 +116,23 @@ def _call(fn, device, *args):
         raise _lib.Fp8bsError(fn, status)
 
 
-@functools.lru_cache(maxsize=4096)
-def _bytes(fn, device_index, *sizes):
-    """What a *_workspace_bytes function says of these sizes (on this device)."""
-    with torch.cuda.device(device_index):
-        n = getattr(attn_lib(), fn)(*sizes)
+def _bytes(fn, *sizes):
+    """What a *_workspace_bytes function says of these sizes."""
+    n = getattr(attn_lib(), fn)(*sizes)
     if n < 0:
         raise _lib.Fp8bsError(fn, n)
     return n
 
 
-def _workspace(fn, device, *sizes):
-    """A tensor of that many bytes, at least 16."""
-    return torch.empty(max(_bytes(fn, device.index, *sizes), 16), dtype=_u8, device=device)
+@functools.lru_cache(maxsize=4096)
+def _bytes_on(device_index, fn, *sizes):
+    """The same where the answer depends on the device: asked once per device and sizes."""
+    with torch.cuda.device(device_index):
+        return _bytes(fn, *sizes)
+
+
+def _workspace(need, device):
+    return torch.empty(max(need, 16), dtype=_u8, device=device)
 
 
 def _prefill_args(q, kv, k_rope, cu_q, cu_k):
@@ -156,7 +160,7 @@ def fp8bs_mla_prefill(q, kv, k_rope, cu_q, cu_k, scale, causal=True):
     Tq, H = q.shape[:2]
     out = torch.empty((Tq, H, 128), dtype=_bf16, device=device)
     lse = torch.empty((H, Tq), dtype=_f32, device=device)
-    need = _bytes("fp8bs_mla_prefill_workspace_bytes", device.index, *sizes[2:])
+    need = _bytes("fp8bs_mla_prefill_workspace_bytes", *sizes[2:])
     ws = torch.empty(need, dtype=_u8, device=device) if need else None
     _call("fp8bs_mla_prefill", device, *ptrs, *sizes, float(scale), int(bool(causal)), out.data_ptr(), lse.data_ptr(),
           ws.data_ptr() if need else None)
@@ -171,7 +175,7 @@ def fp8bs_mla_prefill_bwd(dout, q, kv, k_rope, out, lse, cu_q, cu_k, scale, caus
     Tk = kv.shape[0]
     pd, po = _ptr(dout, "dout", _bf16, (Tq, H, 128), device), _ptr(out, "out", _bf16, (Tq, H, 128), device)
     pl = _ptr(lse, "lse", _f32, (H, Tq), device)
-    ws = _workspace("fp8bs_mla_prefill_bwd_workspace_bytes", device, Tq, Tk, H)
+    ws = _workspace(_bytes("fp8bs_mla_prefill_bwd_workspace_bytes", Tq, Tk, H), device)
     dq = torch.empty((Tq, H, 192), dtype=_bf16, device=device)
     dkv = torch.empty((Tk, H, 256), dtype=_bf16, device=device)
     dk_rope = torch.empty((Tk, 64), dtype=_bf16, device=device)
@@ -218,7 +222,7 @@ def _decode(fn, q, cache, prefix, table, lens, scale):
     pt, pl = _ptr(table, "table", _i32, (B, width), device), _ptr(lens, "lens", _i32, (B,), device)
     out = torch.empty((B, T, H, 512), dtype=_bf16, device=device)
     lse = torch.empty((B, T, H), dtype=_f32, device=device)
-    ws = _workspace("fp8bs_mla_decode_workspace_bytes", device, B, T, H, width, cache_args[5], n_pre)
+    ws = _workspace(_bytes_on(device.index, "fp8bs_mla_decode_workspace_bytes", B, T, H, width, cache_args[5], n_pre), device)
     _call(fn, device, pq, *cache_args, *pre, pt, width, pl, B, T, H, float(scale), out.data_ptr(), lse.data_ptr(),
           ws.data_ptr())
     return out, lse
@@ -258,7 +262,7 @@ def fp8bs_verify_drafts(p, q, drafts, n_drafts, u, u_next):
             _ptr(u, "u", _f32, (B, K), device), _ptr(u_next, "u_next", _f32, (B,), device))
     tokens = torch.empty((B, K1), dtype=_i32, device=device)
     accepted = torch.empty((B,), dtype=_i32, device=device)
-    ws = _workspace("fp8bs_verify_drafts_workspace_bytes", device, B, V)
+    ws = _workspace(_bytes("fp8bs_verify_drafts_workspace_bytes", B, V), device)
     _call("fp8bs_verify_drafts", device, pp, pq, _lib.BF16 if dtype == _bf16 else _lib.F32, *args, B, K, V,
           tokens.data_ptr(), accepted.data_ptr(), ws.data_ptr())
     return tokens, accepted

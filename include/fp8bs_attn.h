@@ -56,6 +56,8 @@ enum fp8bs_cache { FP8BS_CACHE_BF16 = 0, FP8BS_CACHE_FP8 = 1 };
  *   out     [Tq][H][128]  BF16      lse [H][Tq] float32
  * Strides: multiples of 8, at least a token's numbers, below 2^24. Scores, statistics and
  * sums are FP32; probabilities are rounded to BF16 for the matrix unit.
+ * A request's own keys and values are finite: one that a query does not see has
+ * weight 0, and 0 * inf is NaN. Other requests' numbers do not matter.
  * scale finite and > 0 (else FP8BS_ERR_VALUE); H >= 1. workspace: at least
  * fp8bs_mla_prefill_workspace_bytes(B, Tq, Tk, H) bytes, for the parts of few
  * queries' many keys (0 bytes where there are none: then it may be NULL).

@@ -141,6 +141,10 @@ def test_requests_do_not_see_each_other(dev):
     kv[ck[2]:], kr[ck[2]:] = float("inf"), float("nan")
     o2, l2 = fb.fp8bs_mla_prefill(q, kv, kr, tq, tk, SCALE)
     assert torch.equal(o2[i], o1) and torch.equal(l2[:, i], l1)
+    g1 = fb.fp8bs_mla_prefill_bwd(dout[i].contiguous(), q[i].contiguous(), kv[j].contiguous(), kr[j].contiguous(), o1, l1,
+                                  *one, SCALE)
+    g2 = fb.fp8bs_mla_prefill_bwd(dout, q, kv, kr, o2, l2, tq, tk, SCALE)
+    assert torch.equal(g2[0][i], g1[0]) and torch.equal(g2[1][j], g1[1]) and torch.equal(g2[2][j], g1[2])
 
 
 @pytest.mark.parametrize("causal", [True, False])
