@@ -23,6 +23,9 @@ int status_of(hipError_t e) { return e == hipSuccess ? FP8BS_OK : FP8BS_ERR_LAUN
 hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 bool bad_scale(float s) { return !(s > 0.f) || !isfinite(s); }
 
+// A launch has fewer than 2^32 threads.
+bool launch_too_large(int64_t workgroups, int threads) { return workgroups > (((int64_t)1 << 32) - 1) / threads; }
+
 int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 
 int prefill_sizes(int B, int64_t Tq, int64_t Tk, int H, int64_t q_stride, int64_t kv_stride, int64_t rope_stride,
@@ -257,8 +260,10 @@ int fp8bs_mla_decode_shared(const uint16_t* q, int cache_kind, const void* cache
 
 int64_t fp8bs_verify_drafts_workspace_bytes(int B, int64_t V) {
   if (B < 0 || V < 1) return FP8BS_ERR_SHAPE;
-  if (V > 1 << 24 || B * (fp8bs::verify_chunks(V) + 1) > kGridMax) return FP8BS_ERR_TOO_LARGE;
-  return 16 * B * (fp8bs::verify_chunks(V) + 1);
+  if (V > 1 << 24) return FP8BS_ERR_TOO_LARGE;
+  const int64_t chunks = fp8bs::verify_chunks(V);
+  if (launch_too_large(B * chunks, fp8bs::kVerifyThreads)) return FP8BS_ERR_TOO_LARGE;
+  return (int64_t)16 * B * (chunks + 1);
 }
 
 int fp8bs_verify_drafts(const void* p, const void* q, int dtype, const int32_t* drafts, const int32_t* n_drafts,

@@ -85,6 +85,7 @@ struct VerifyDrafts {
   int32_t* accepted;      // [B]
 };
 
+constexpr int kVerifyThreads = 256;      // of a workgroup: one per request and chunk
 int64_t verify_chunks(int64_t V);
 hipError_t launch_verify_drafts(const VerifyDrafts& v, bool bf16, hipStream_t stream);
 

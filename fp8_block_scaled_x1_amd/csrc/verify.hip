@@ -25,7 +25,7 @@ namespace fp8bs {
 
 namespace {
 
-constexpr int kChunk = 8192, kVThreads = 256, kPer = kChunk / kVThreads;      // kPer consecutive entries a thread
+constexpr int kChunk = 8192, kVThreads = kVerifyThreads, kPer = kChunk / kVThreads;      // kPer consecutive entries a thread
 constexpr float kWeightOne = 274877906944.0f;      // 2^38
 
 template <bool BF16>

@@ -152,7 +152,7 @@ FP8BS_API int64_t fp8bs_mla_decode_workspace_bytes(int B, int T, int H, int64_t 
  *   u [B][K], u_next [B] float32 in [0, 1)
  *   tokens [B][K+1] int32: the accepted drafts, the next token, then -1
  *   accepted [B] int32
- * 0 <= K <= 63, 1 <= V <= 2^24. p and q 4-byte aligned. workspace:
+ * 0 <= K <= 63, 1 <= V <= 2^24, B * ceil(V / 8192) < 2^24. p and q 4-byte aligned. workspace:
  * fp8bs_verify_drafts_workspace_bytes(B, V) bytes.
  */
 FP8BS_API int fp8bs_verify_drafts(const void* p, const void* q, int dtype, const int32_t* drafts,

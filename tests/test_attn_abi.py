@@ -139,6 +139,16 @@ def test_verify_refusals(L):
     assert L.fp8bs_verify_drafts_workspace_bytes(2, 8193) == 16 * 2 * 3
 
 
+def test_verify_more_requests_than_a_launch_holds(L):
+    # one workgroup of 256 threads per request and chunk, and a launch has fewer than 2^32 threads
+    ws = L.fp8bs_verify_drafts_workspace_bytes
+    assert ws((1 << 24) - 1, 1) == 16 * 2 * ((1 << 24) - 1)
+    assert ws((1 << 23) - 1, 8193) == 16 * 3 * ((1 << 23) - 1)
+    for B, V in ((1 << 24, 1), (1 << 23, 8193), (1 << 27, 1), (1 << 28, 1), ((1 << 31) - 1, 1), (1 << 13, 1 << 24)):
+        assert ws(B, V) == -7, (B, V)
+        assert L.fp8bs_verify_drafts(P, NULL, 0, NULL, P, NULL, P, B, 0, V, P, P, P, NULL) == -7, (B, V)
+
+
 def test_binding_refusals():
     import torch
     bf, i32 = torch.bfloat16, torch.int32
