@@ -14,7 +14,6 @@
 namespace {
 
 constexpr int64_t kI32 = (int64_t)1 << 31;
-constexpr int64_t kGridMax = kI32 - 1;
 constexpr int kTile = 64;
 
 bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
@@ -37,8 +36,8 @@ int prefill_sizes(int B, int64_t Tq, int64_t Tk, int H, int64_t q_stride, int64_
   if (q_stride % 8 || kv_stride % 8 || rope_stride % 8) return FP8BS_ERR_ALIGN;
   // a tile's rows are addressed by 32-bit byte offsets from its first
   if (q_stride >= 1 << 24 || kv_stride >= 1 << 24 || rope_stride >= 1 << 24) return FP8BS_ERR_TOO_LARGE;
-  const int64_t most = Tq > Tk ? Tq : Tk;
-  if ((most / 32 + 1 + B) * H > kGridMax || most * H > kGridMax * 8) return FP8BS_ERR_TOO_LARGE;
+  // (the forward's narrower blocks have half the threads and are at most twice as many)
+  if (launch_too_large(fp8bs::mla_blocks(Tq, B, 256) * H, 512)) return FP8BS_ERR_TOO_LARGE;
   if (bad_scale(scale)) return FP8BS_ERR_VALUE;
   return FP8BS_OK;
 }
@@ -68,7 +67,6 @@ int decode_sizes(int B, int64_t rows, int64_t all_rows, int64_t width, int page,
   if (tiles >= kI32) return FP8BS_ERR_TOO_LARGE;
   s.row_blocks = (rows + fp8bs::kMlaDecodeBlockRows - 1) / fp8bs::kMlaDecodeBlockRows;
   s.groups = fp8bs::mla_decode_groups(s.row_blocks, tiles);
-  if (s.groups * s.row_blocks > kGridMax) return FP8BS_ERR_TOO_LARGE;
   s.pieces = 2 * (int64_t)s.groups + (joined ? B : 0);
   return FP8BS_OK;
 }
@@ -77,7 +75,7 @@ int decode_plan(int B, int T, int H, int64_t width, int page, int64_t prefix_pag
                 DecodeSizes& prefix) {
   if (B < 0 || T < 1 || H < 1 || width < 0 || page < 1 || prefix_pages < 0) return FP8BS_ERR_SHAPE;
   const int64_t rows = (int64_t)T * H, all = B * rows;
-  if (rows >= 1 << 24 || all >= kI32 / 8) return FP8BS_ERR_TOO_LARGE;
+  if (rows >= 1 << 24 || launch_too_large((all + 3) / 4, 256)) return FP8BS_ERR_TOO_LARGE;      // the join: a wave a row
   int st = decode_sizes(B, rows, all, width, page, prefix_pages > 0, own);
   if (st != FP8BS_OK || prefix_pages == 0) return st;
   // the prefix: every block of everyone's rows is a request over the same tokens
@@ -209,6 +207,9 @@ int fp8bs_mla_prefill_bwd(const uint16_t* dout, const uint16_t* q, int64_t q_str
                           void* workspace, void* stream) {
   const int st = prefill_sizes(B, Tq, Tk, H, q_stride, kv_stride, rope_stride, scale);
   if (st != FP8BS_OK) return st;
+  if (launch_too_large(fp8bs::mla_blocks(Tq, B, 128) * H, 256) ||
+      launch_too_large(fp8bs::mla_blocks(Tk, B, 128) * H, 512) || launch_too_large(Tk, 64))
+    return FP8BS_ERR_TOO_LARGE;
   if (Tq == 0 && Tk == 0) return FP8BS_OK;
   if (!cu_q || !cu_k || !workspace) return FP8BS_ERR_NULL_PTR;
   if (Tq > 0 && (!dout || !q || !out || !lse || !dq)) return FP8BS_ERR_NULL_PTR;

@@ -34,6 +34,8 @@ struct MlaPrefill {
   uint16_t* dk_rope;      // [Tk][64]
 };
 
+// Blocks of `rows` tokens of a packed batch, at most: every request ends inside one.
+inline int64_t mla_blocks(int64_t tokens, int B, int rows) { return (tokens + rows - 1) / rows + B; }
 // Parts that launch_mla_prefill cuts the keys into at these sizes; 1: no workspace.
 int mla_prefill_parts(int B, int64_t Tq, int64_t Tk, int H);
 hipError_t launch_mla_prefill(const MlaPrefill& p, hipStream_t stream);

@@ -913,12 +913,9 @@ __global__ __launch_bounds__(256) void mla_rope_sum_kernel(const MlaPrefill p) {
   *reinterpret_cast<bf16x4*>(p.dk_rope + i) = b;
 }
 
-// Blocks of a packed batch, at most: every request ends inside one.
-int64_t blocks(int64_t tokens, int B, int rows) { return (tokens + rows - 1) / rows + B; }
-
 }  // namespace
 
-static bool wide_blocks(int64_t Tq, int B, int H) { return blocks(Tq, B, 256) * H >= 1024; }
+static bool wide_blocks(int64_t Tq, int B, int H) { return mla_blocks(Tq, B, 256) * H >= 1024; }
 
 // Few blocks of queries behind many keys leave compute units without work or
 // with a second block after the others are done. Cut into s parts, W blocks are
@@ -952,7 +949,7 @@ int mla_prefill_parts(int B, int64_t Tq, int64_t Tk, int H) {
 }
 
 hipError_t launch_mla_prefill(const MlaPrefill& p, hipStream_t stream) {
-  const int64_t wide = blocks(p.Tq, p.B, 256), units = blocks(p.Tq, p.B, 128);
+  const int64_t wide = mla_blocks(p.Tq, p.B, 256), units = mla_blocks(p.Tq, p.B, 128);
   if (wide_blocks(p.Tq, p.B, p.H)) {
     hipLaunchKernelGGL((mla_fwd_kernel<8, false>), dim3(unit_grid(wide, p.H)), dim3(512), 0, stream, p, (int)wide);
   } else if (p.parts == 1) {
@@ -967,11 +964,11 @@ hipError_t launch_mla_prefill(const MlaPrefill& p, hipStream_t stream) {
 
 hipError_t launch_mla_prefill_bwd(const MlaPrefill& p, hipStream_t stream) {
   if (p.Tq > 0) {
-    const int64_t units = blocks(p.Tq, p.B, 128);
+    const int64_t units = mla_blocks(p.Tq, p.B, 128);
     hipLaunchKernelGGL(mla_dq_kernel, dim3(unit_grid(units, p.H)), dim3(256), 0, stream, p, (int)units);
   }
   if (p.Tk > 0) {
-    const int64_t units = blocks(p.Tk, p.B, 128);
+    const int64_t units = mla_blocks(p.Tk, p.B, 128);
     hipLaunchKernelGGL(mla_dkv_kernel, dim3(unit_grid(units, p.H)), dim3(512), 0, stream, p, (int)units);
     hipLaunchKernelGGL(mla_rope_sum_kernel, dim3((unsigned)(((int64_t)p.Tk * kRopeDim + 255) / 256)), dim3(256), 0,
                        stream, p);

@@ -11,6 +11,7 @@
  * nothing; workspaces are the caller's, sized by the *_workspace_bytes
  * functions, their contents on entry do not matter. Every entry point can be
  * captured into a HIP graph and gives the same bits for the same inputs.
+ * Sizes whose launch would pass 2^32 - 1 threads are refused (FP8BS_ERR_TOO_LARGE).
  * Pointers are 16-byte aligned unless said otherwise; int32 and float32 side
  * arrays (offsets, lengths, tables, random numbers, lse) 4-byte. Numbers that
  * take part in a result must be finite; what lies past a request's length, in

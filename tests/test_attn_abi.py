@@ -139,6 +139,22 @@ def test_verify_refusals(L):
     assert L.fp8bs_verify_drafts_workspace_bytes(2, 8193) == 16 * 2 * 3
 
 
+def test_attention_beyond_what_a_launch_holds(L):
+    # refused by its sizes, before a first kernel is enqueued: a launch has fewer than 2^32 threads
+    many = dict(B=65536, Tq=65536, Tk=65536, H=128, qs=128 * 192, kvs=128 * 256)
+    assert _prefill(L, **many) == -7
+    bwd = dict(dout=P, q=P, qs=128 * 192, kv=P, kvs=128 * 256, r=P, rs=64, out=P, lse=P, cq=P, ck=P, B=65536, Tq=65536,
+               Tk=65536, H=128, scale=0.1, causal=1, dq=P, dkv=P, dr=P, ws=P, stream=NULL)
+    assert L.fp8bs_mla_prefill_bwd(*bwd.values()) == -7
+    bwd.update(B=1, Tq=1, Tk=1 << 26, H=1, qs=192, kvs=256)          # the rotary sum: 64 threads a key
+    assert L.fp8bs_mla_prefill_bwd(*bwd.values()) == -7
+    # the join of the pieces: a wave a row
+    for shared in (False, True):
+        assert _decode(L, shared, B=1 << 16, T=8, H=128) == -7
+    ws = L.fp8bs_mla_decode_workspace_bytes
+    assert ws(1 << 16, 8, 128, 4, 16, 0) == -7 and ws((1 << 26) - 1, 1, 1, 1, 1, 0) == -7 and ws((1 << 16) - 1, 8, 128, 4, 16, 0) > 0
+
+
 def test_verify_more_requests_than_a_launch_holds(L):
     # one workgroup of 256 threads per request and chunk, and a launch has fewer than 2^32 threads
     ws = L.fp8bs_verify_drafts_workspace_bytes
