@@ -223,3 +223,78 @@ def test_binding_refusals(dev):
         fb.fp8bs_mla_decode(q, c.cache, c.table, c.lens, -1.0)
     with pytest.raises(ValueError):
         fb.fp8bs_mla_decode_shared(q, c.cache, c.table, c.prefix_len, c.table, c.lens, SCALE)
+
+
+def _groups(B, T, H, width, page):
+    """Workgroup ranges that the tiles of 64 tokens are shared by, from the workspace: two partials
+    (512 + 2 numbers, FP32) of a request's rows each."""
+    return fb.attn_lib().fp8bs_mla_decode_workspace_bytes(B, T, H, width, page, 0) // (2 * T * H * 514 * 4)
+
+
+def _tiles(lens):
+    return sum(-(-n // 64) for n in lens)
+
+
+SHORT = [100 + 37 * i % 600 for i in range(300)]
+MANY_TILES = [
+    (4, 128, [3000, 65, 700, 0, 129]),       # a request cut over ranges, ranges that hold several requests' ends
+    (3, 40, [2000, 1, 64, 900, 1500, 1100, 2500, 3000]),
+    (1, 16, [9000, 6400, 3, 0, 12000]),      # few rows, more tiles than workgroups
+    (1, 20, SHORT),                          # whole requests one after the other inside a range
+]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("T,H,lens", MANY_TILES, ids=["512 rows", "120 rows", "long", "300 requests"])
+def test_several_tiles_per_workgroup(dev, kind, T, H, lens):
+    c, *_ = _check(dev, kind, 64, lens, T, H, seed=T + H)
+    assert _tiles(lens) > 1.2 * _groups(len(lens), T, H, c.table.shape[1], 64)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("page", [1, 48])
+def test_several_tiles_per_workgroup_of_other_pages(dev, kind, page):
+    lens = [1000, 64, 0, 333, 1]
+    c, *_ = _check(dev, kind, page, lens, 8, 128, seed=page)
+    assert _tiles(lens) > 1.2 * _groups(len(lens), 8, 128, c.table.shape[1], page)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_reference_raised_over_sums(dev, kind):
+    # scores that grow along the request: each tile of a range raises the reference over what has been added up
+    lens, T, H = [2000, 1300], 8, 128
+    c = Paged(dev, kind, 64, lens, 4)
+    q = _q(dev, 2, T, H, 4, 6.0)
+    own = [torch.from_numpy(c.table[b, :-(-n // 64)].cpu().numpy()).long() for b, n in enumerate(lens)]
+    rope = c.cache[..., 512:] if kind == "bf16" else c.cache[2]
+    keys = [k.copy() for k in c.keys]
+    q[..., 512] = 30.0
+    for b, n in enumerate(lens):
+        # (whole numbers below 16: BF16 values)
+        ramp = (torch.arange(n) * 16 // n).float().to(torch.bfloat16)
+        pos = torch.arange(n)
+        rope[own[b][pos // 64].to(dev), (pos % 64).to(dev), 0] = ramp.to(dev)
+        keys[b][:, 512] = ramp.double().numpy()
+    out, lse = fb.fp8bs_mla_decode(q, c.cache, c.table, c.lens, SCALE)
+    torch.cuda.synchronize()
+    assert _tiles(lens) > 1.2 * _groups(2, T, H, c.table.shape[1], 64)
+    o, l, bo, bl = oa.mla_decode(_f64(q), keys, SCALE)
+    _inside(out, o, bo, "out")
+    _inside(lse, l, bl, "lse")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("B,T,H,prefix", [(20, 1, 128, 1000), (11, 3, 70, 900), (60, 2, 16, 3000), (150, 1, 16, 700)])
+def test_shared_prefix_of_several_tiles_per_workgroup(dev, kind, B, T, H, prefix):
+    # more tiles than workgroups in the prefix (one request per 64 rows there), and both joins of rows with a prefix
+    assert -(-B * T * H // 64) * -(-prefix // 64) > 1.2 * 256
+    rng = np.random.default_rng(B)
+    lens = [int(x) for x in rng.integers(T, 260, B)]
+    c = Paged(dev, kind, 64, lens, 6, prefix=prefix)
+    q = _q(dev, B, T, H, 6)
+    out, lse = fb.fp8bs_mla_decode_shared(q, c.cache, c.prefix_table, c.prefix_len, c.table, c.lens, SCALE)
+    torch.cuda.synchronize()
+    keys = [(prefix, np.concatenate([c.prefix_keys, k])) for k in c.keys]
+    o, l, bo, bl = oa.mla_decode(_f64(q), keys, SCALE)
+    _inside(out, o, bo, f"shared {prefix} {lens}")
+    _inside(lse, l, bl, f"shared lse {prefix} {lens}")

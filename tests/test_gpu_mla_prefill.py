@@ -12,6 +12,7 @@ import fp8_block_scaled_x1_amd as fb
 
 pytestmark = pytest.mark.gpu
 SCALE = 192 ** -0.5
+NAN = float("nan")
 
 
 def _f64(t):
@@ -194,6 +195,79 @@ def test_same_bits_every_time_and_in_a_graph(dev, lens):
         for a, b in zip(step(), ref):
             assert torch.equal(a, b)
     torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        res = step()
+    for _ in range(3):
+        for x in res:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(res, ref):
+            assert torch.equal(a, b)
+
+
+def _sampled(dev, lens, H, heads, causal, seed):
+    """out, lse, dq, dkv of some heads of a problem large enough for blocks of 256 queries, and
+    dk_rope where these are all the heads."""
+    q, kv, kr, dout, cq, ck = _inputs(dev, lens, H, seed)
+    tq, tk = torch.from_numpy(cq).to(dev), torch.from_numpy(ck).to(dev)
+    out, lse = fb.fp8bs_mla_prefill(q, kv, kr, tq, tk, SCALE, causal=causal)
+    dq, dkv, dk_rope = fb.fp8bs_mla_prefill_bwd(dout, q, kv, kr, out, lse, tq, tk, SCALE, causal=causal)
+    torch.cuda.synchronize()
+    at = torch.tensor(heads)
+    pick = lambda t: _f64(t[:, at.to(t.device)])
+    ref = oa.mla_prefill(pick(q), pick(kv), _f64(kr), cq, ck, SCALE, causal, pick(dout))
+    what = f"{lens} H {H} causal {causal}"
+    for name, x in (("out", out), ("dq", dq), ("dkv", dkv)):
+        _inside(x[:, at.to(dev)], ref[name], f"{name} {what}")
+    _inside(lse[at.to(dev)], ref["lse"], f"lse {what}")
+    if len(heads) == H:
+        _inside(dk_rope, ref["dk_rope"], f"dk_rope {what}")
+    return (q, kv, kr, dout, tq, tk), (out, lse, dq, dkv, dk_rope)
+
+
+# causal ends inside blocks and tiles, chunks, waves without queries, no keys, rows that see nothing
+MIXED = [(257, 257), (1, 70), (300, 513), (5, 0), (70, 20), (255, 256)]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("H", [128, 200])
+def test_blocks_of_256_queries(dev, H, causal):
+    # (groups of four heads per XCD: 128 has four whole ones, 200 six and one of a single head)
+    _sampled(dev, MIXED, H, [0, 7, 31, 63, 100, H - 9, H - 1], causal, seed=H)
+
+
+@pytest.mark.parametrize("H", [40, 48])
+def test_blocks_of_256_queries_every_head(dev, H):
+    # five and six heads per XCD: the last group has one and two; the rotary gradient sums them all
+    lens = [(33, 33), (1, 90), (64, 64), (20, 85), (3, 2)] * 6
+    _sampled(dev, lens, H, list(range(H)), True, seed=H)
+
+
+@pytest.mark.parametrize("H", [56, 64, 65, 72, 128, 256, 344])
+def test_both_sides_of_the_block_size_rule(dev, H):
+    _sampled(dev, [(300, 300), (212, 700)], H, [0, 3, H // 2, H - 1], True, seed=H)
+
+
+def test_blocks_of_256_queries_with_gaps_and_in_a_graph(dev):
+    H = 128
+    (q, kv, kr, dout, tq, tk), ref = _sampled(dev, MIXED, H, [5], True, seed=1)
+    ref = [x.clone() for x in ref]
+    wide = torch.full((len(q), H * 192 + 8), NAN, dtype=torch.bfloat16, device=dev)
+    wide[:, 8:] = q.reshape(len(q), -1)
+    wkv = torch.full((len(kv), H * 256 + 64), NAN, dtype=torch.bfloat16, device=dev)
+    wkv[:, :-64] = kv.reshape(len(kv), -1)
+    lat = torch.full((len(kr), 576), NAN, dtype=torch.bfloat16, device=dev)
+    lat[:, 512:] = kr
+    views = wide[:, 8:].unflatten(1, (H, 192)), wkv[:, :-64].unflatten(1, (H, 256)), lat[:, 512:]
+
+    def step():
+        out, lse = fb.fp8bs_mla_prefill(*views, tq, tk, SCALE)
+        return (out, lse, *fb.fp8bs_mla_prefill_bwd(dout, *views, out, lse, tq, tk, SCALE))
+
+    for a, b in zip(step(), ref):
+        assert torch.equal(a, b)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         res = step()

@@ -86,3 +86,59 @@ def test_same_in_a_graph(dev):
         torch.cuda.synchronize()
         for a, b in zip(res, ref):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [8191, 8192, 8193, 8196, 16384, 129280])
+def test_sizes_around_whole_chunks(dev, V, dtype):
+    # a row's sums are taken 8192 entries at a time; four entries a load where V is a multiple of four
+    p, q, drafts, n, u, un = _case(6, 2, V, V, dtype, sharp=0.5)
+    n[:] = torch.tensor([2, 2, 2, 1, 0, 2])
+    for b in (0, 3):         # likely drafts (accepted at a small u), the others are turned down
+        drafts[b] = p[b, :2].float().argmax(-1)
+        u[b] = 0.0
+    un[:] = torch.tensor([0.0, 0.999999, 0.5, 0.93, 0.07, 0.3])
+    _compare(dev, p, q, drafts, n, u, un)
+    _compare(dev, p, None, drafts, n, u, un)
+
+
+@pytest.mark.parametrize("dtype,skip", [(torch.float32, 1), (torch.bfloat16, 2)])
+def test_rows_that_are_not_aligned_for_wide_loads(dev, dtype, skip):
+    # four bytes behind an aligned address, rows of whole groups of four entries
+    p, q, *rest = _case(4, 2, 9000, 9, dtype)
+
+    def shifted(x):
+        buf = torch.zeros(x.numel() + skip, dtype=dtype, device=dev)
+        view = buf[skip:].view(x.shape)
+        view.copy_(x)
+        assert view.data_ptr() % 16 == 4
+        return view
+
+    want = fb.fp8bs_verify_drafts(*(x.to(dev) for x in (p, q, *rest)))
+    _compare(dev, p, q, *rest)
+    for a, b in ((shifted(p), q.to(dev)), (p.to(dev), shifted(q)), (shifted(p), shifted(q))):
+        got = fb.fp8bs_verify_drafts(a, b, *(x.to(dev) for x in rest))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_more_than_64_chunks(dev, dtype):
+    # 128 chunks of equal weights: token floor(u * V); at the chunks' limits, and the random number before each
+    V = 1 << 20
+    at = torch.tensor([0, 1, 63, 64, 65, 100, 127])
+    un = torch.cat([at / 128, (at[1:] / 128) - 2.0 ** -24, torch.tensor([1 - 2.0 ** -24, 0.51, 0.4999])]).float()
+    B = len(un)
+    p = torch.full((B, 1, V), 2.0 ** -20, dtype=dtype)
+    z = torch.zeros((B, 0))
+    args = p, None, z.int(), torch.zeros(B).int(), z, un
+    got = fb.fp8bs_verify_drafts(*(None if x is None else x.to(dev) for x in args))
+    assert got[0][:, 0].tolist() == torch.floor(un.double() * V).int().tolist() and got[1].tolist() == [0] * B
+
+
+def test_more_than_64_chunks_of_random_weights(dev):
+    V = 600001
+    p, q, drafts, n, u, un = _case(3, 1, V, 12, sharp=0.5)
+    un[:] = torch.tensor([1e-6, 0.9, 0.9999])
+    _compare(dev, p[:, :1].contiguous(), q[:, :0].contiguous(), drafts[:, :0].contiguous(), n * 0, u[:, :0].contiguous(), un)
+    u[:] = float("inf")
+    _compare(dev, p, q, drafts, n * 0 + 1, u, un)
