@@ -32,9 +32,7 @@ HIPCC_FLAGS = [
 
 # MFMA results straight into ordinary registers: these kernels fit in 256 of
 # them, and the accumulation registers would cost a copy per use
-# (and no NaN takes part in a maximum, which spares quieting its operands)
-FILE_FLAGS = {"mla_decode.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1", "-fno-honor-nans"],
-              "mla_prefill.hip": ["-fno-honor-nans"]}
+FILE_FLAGS = {"mla_decode.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 
 def hipcc():

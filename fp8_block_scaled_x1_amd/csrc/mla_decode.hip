@@ -495,8 +495,8 @@ __global__ __launch_bounds__(256 * kTeams) __attribute__((amdgpu_waves_per_eu(2)
           for (int j = 0; j < 4; ++j)
             if (tok0 + 8 * i + j >= seen) s[i][j] = neg_inf();
       }
-      float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
-                        fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
+      float top = max_nan(max_nan(max_nan(s[0][0], s[0][1]), max_nan(s[0][2], s[0][3])),
+                          max_nan(max_nan(s[1][0], s[1][1]), max_nan(s[1][2], s[1][3])));
       top = half_max(top) * p.scale_log2;
       float sum;
       auto weigh = [&] {
@@ -533,7 +533,7 @@ __global__ __launch_bounds__(256 * kTeams) __attribute__((amdgpu_waves_per_eu(2)
         float mn = m;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mn = fmaxf(mn, reinterpret_cast<const float*>(team + k * kSlot + kProbBytes)[L.row]);
+          mn = max_nan(mn, reinterpret_cast<const float*>(team + k * kSlot + kProbBytes)[L.row]);
         const float alpha = mn == neg_inf() ? 1.f : exp2_fast(m - mn);
         m = mn;
         l *= alpha;
@@ -582,7 +582,7 @@ __global__ __launch_bounds__(256 * kTeams) __attribute__((amdgpu_waves_per_eu(2)
     if (row < p.rows && (int64_t)cur.b * p.rows + row < p.all_rows) {
       if (whole && !p.join) {
         const int64_t o = (int64_t)cur.b * p.rows + row;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = inverse_of(l);
         uint16_t* op = p.out + o * kLatent + 128 * quarter + 4 * L.half;
 #pragma unroll
         for (int d = 0; d < 4; ++d)
@@ -593,7 +593,7 @@ __global__ __launch_bounds__(256 * kTeams) __attribute__((amdgpu_waves_per_eu(2)
             for (int j = 0; j < 4; ++j) b[j] = (__bf16)(acc[d][4 * i + j] * inv);
             *reinterpret_cast<bf16x4*>(op + 32 * d + 8 * i) = b;
           }
-        if (quarter == 0 && L.half == 0) p.lse[o] = l > 0.f ? (m + __builtin_log2f(l)) * kLn2 : neg_inf();
+        if (quarter == 0 && L.half == 0) p.lse[o] = lse_of(m, l);
       } else {
         const int64_t o = (whole ? 2 * (int64_t)p.groups + cur.b : 2 * (int64_t)g + (first ? 0 : 1)) * p.rows + row;
         float* op = p.part + o * kLatent + 128 * quarter + 4 * L.half;
@@ -679,8 +679,8 @@ __global__ __launch_bounds__(kThreads) void mla_join_kernel(const MlaDecode p, c
     if (i < n) x = *reinterpret_cast<const float2*>((mine ? p.part_ml : prefix.part_ml) + 2 * (mine ? own.at(i) : pre.at(i - own.n)));
     float mn = x.x;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) mn = fmaxf(mn, __shfl_xor(mn, d, 64));
-    mn = fmaxf(mn, m);
+    for (int d = 1; d < 64; d <<= 1) mn = max_nan(mn, __shfl_xor(mn, d, 64));
+    mn = max_nan(mn, m);
     const float ref = mn == neg_inf() ? 0.f : mn;
     const float old = exp2_fast(m - ref), weight = exp2_fast(x.x - ref);
     float add = x.y * weight;
@@ -718,7 +718,7 @@ __global__ __launch_bounds__(kThreads) void mla_join_kernel(const MlaDecode p, c
     __syncthreads();
     float mn = neg_inf();
 #pragma unroll
-    for (int k = 0; k < W; ++k) mn = fmaxf(mn, ml[k].x);
+    for (int k = 0; k < W; ++k) mn = max_nan(mn, ml[k].x);
     const float ref = mn == neg_inf() ? 0.f : mn, x = exp2_fast(m - ref);
     l = 0.f;
 #pragma unroll
@@ -741,12 +741,12 @@ __global__ __launch_bounds__(kThreads) void mla_join_kernel(const MlaDecode p, c
       for (int k = 0; k < W; ++k) acc[j] += sums[k][8 * lane + j];
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = inverse_of(l);
   bf16x8 v;
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = (__bf16)(acc[i] * inv);
   *reinterpret_cast<bf16x8*>(p.out + o * kLatent + 8 * lane) = v;
-  if (lane == 0) p.lse[o] = l > 0.f ? (m + __builtin_log2f(l)) * kLn2 : neg_inf();
+  if (lane == 0) p.lse[o] = lse_of(m, l);
 }
 
 int compute_units() {

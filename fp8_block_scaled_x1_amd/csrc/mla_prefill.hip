@@ -234,7 +234,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
   auto raise = [&](float top) {
     top = half_max(top) * c;
     if (__any(top > m + kSlack)) {
-      const float mn = fmaxf(m, top);
+      const float mn = max_nan(m, top);
       const float alpha = mn == neg_inf() ? 1.f : exp2_fast(m - mn);
       m = mn;
       l *= alpha;
@@ -242,7 +242,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
       for (int d = 0; d < 4; ++d) o[d] *= alpha;
     }
   };
-  auto max4 = [](const f32x16& v, int i) { return fmaxf(fmaxf(v[4 * i], v[4 * i + 1]), fmaxf(v[4 * i + 2], v[4 * i + 3])); };
+  auto max4 = [](const f32x16& v, int i) { return max_nan(max_nan(v[4 * i], v[4 * i + 1]), max_nan(v[4 * i + 2], v[4 * i + 3])); };
 
   int buf = 0;
   // Tile t, whose scores are in s; those of tile t+1 go to sn.
@@ -300,10 +300,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
         __builtin_amdgcn_sched_barrier(0);
         o[i & 3] = mfma32(vf[i % kAhead], pb[i >> 2], o[i & 3]);
         if (i + kAhead < 16) vf[i % kAhead] = fetch(i + kAhead);
-        if (i & 1) top[(i >> 1) & 1] = fmaxf(top[(i >> 1) & 1], max4(sn[i >> 3], (i >> 1) & 3));
+        if (i & 1) top[(i >> 1) & 1] = max_nan(top[(i >> 1) & 1], max4(sn[i >> 3], (i >> 1) & 3));
       }
       __builtin_amdgcn_sched_barrier(0);
-      if (more) raise(fmaxf(top[0], top[1]));
+      if (more) raise(max_nan(top[0], top[1]));
     } else if (load) {      // nothing here for this wave: only its share of the loads
 #pragma unroll
       for (int n = 0; n < Load::kLoads; ++n) issue(n);
@@ -321,7 +321,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
       mask(sa, 0);
       float top = neg_inf();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) top = fmaxf(top, max4(sa[i >> 2], i & 3));
+      for (int i = 0; i < 8; ++i) top = max_nan(top, max4(sa[i >> 2], i & 3));
       raise(top);
     }
   }
@@ -347,7 +347,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
       if (L.half == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(m, l);
     }
   } else if (qi < Lq) {
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = inverse_of(l);
     uint16_t* op = p.out + ((int64_t)(u.r0 + qi) * p.H + head) * kVDim + 4 * L.half;
 #pragma unroll
     for (int d = 0; d < 4; ++d)
@@ -359,7 +359,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
         *reinterpret_cast<bf16x4*>(op + 32 * d + 8 * i) = b;
       }
     if (L.half == 0)
-      p.lse[(int64_t)head * p.Tq + u.r0 + qi] = l > 0.f ? (m + __builtin_log2f(l)) * kLn2 : neg_inf();
+      p.lse[(int64_t)head * p.Tq + u.r0 + qi] = lse_of(m, l);
   }
 }
 
@@ -392,7 +392,7 @@ __global__ __launch_bounds__(256) void mla_fwd_join_kernel(const MlaPrefill p, i
       }
       float mn = m;
 #pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) mn = fmaxf(mn, ml[k].x);
+      for (int k = 0; k < kAtOnce; ++k) mn = max_nan(mn, ml[k].x);
       const float ref = mn == neg_inf() ? 0.f : mn, old = exp2_fast(m - ref);
       l *= old;
       o *= old;
@@ -405,12 +405,12 @@ __global__ __launch_bounds__(256) void mla_fwd_join_kernel(const MlaPrefill p, i
       }
       m = mn;
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = inverse_of(l);
     bf16x4 b;
 #pragma unroll
     for (int j = 0; j < 4; ++j) b[j] = (__bf16)(o[j] * inv);
     *reinterpret_cast<bf16x4*>(p.out + at * kVDim + 4 * lane) = b;
-    if (lane == 0) p.lse[(int64_t)head * p.Tq + u.r0 + r] = l > 0.f ? (m + __builtin_log2f(l)) * kLn2 : neg_inf();
+    if (lane == 0) p.lse[(int64_t)head * p.Tq + u.r0 + r] = lse_of(m, l);
   }
 }
 

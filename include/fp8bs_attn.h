@@ -14,8 +14,10 @@
  * Sizes whose launch would pass 2^32 - 1 threads are refused (FP8BS_ERR_TOO_LARGE).
  * Pointers are 16-byte aligned unless said otherwise; int32 and float32 side
  * arrays (offsets, lengths, tables, random numbers, lse) 4-byte. Numbers that
- * take part in a result must be finite; what lies past a request's length, in
- * a page's unused slots or behind unused table entries is never used.
+ * take part in an attention's result should be finite: a NaN among those that a
+ * score is formed from makes out and lse of the queries that see it NaN (they
+ * do not pass for queries that see no key). What lies past a request's length,
+ * in a page's unused slots or behind unused table entries is never used.
  *
  * Dimensions: a head has 128 + 64 query and key numbers (the 64 rotary ones of
  * the key shared by all heads) and 128 value numbers; the cached latent vector
