@@ -113,11 +113,8 @@ constexpr int kJoinSlices = 16;      // workgroups of the join per block of 128 
 // took 238 us, so 190.)
 //
 // 256 queries (NW = 8) halve the tiles' traffic into LDS and give each SIMD
-// its second wave; 128 (NW = 4) give twice the workgroups. The rule in
-// launch_mla_prefill takes 256 where that leaves every compute unit four
-// workgroups (two requests of 6000 to 8192 tokens on 128 heads: 3.68 ms, with
-// 128 queries 4.44 ms), and 128 otherwise (the two chunks: 188 us, with 256
-// queries 239 us).
+// its second wave; 128 (NW = 4) give twice the workgroups, which can also be
+// cut along the keys. Which is taken: see wide_blocks.
 //
 // Bound by the matrix unit's rate at the clock that the power limit leaves: the
 // two long requests run at 1.0 PFLOP/s, 0.53 of the unit's cycles at 1.9 GHz.
@@ -915,7 +912,13 @@ __global__ __launch_bounds__(256) void mla_rope_sum_kernel(const MlaPrefill p) {
 
 }  // namespace
 
-static bool wide_blocks(int64_t Tq, int B, int H) { return mla_blocks(Tq, B, 256) * H >= 1024; }
+// Compute units of the MI355X; not asked of the device, so that a workspace's
+// size does not depend on it.
+static constexpr int kUnits = 256;
+
+// Blocks of `rows` queries on all heads, for requests of average length (the
+// host does not know theirs).
+static double average_blocks(int64_t Tq, int B, int H, int rows) { return std::ceil((double)Tq / B / rows) * B * H; }
 
 // Few blocks of queries behind many keys leave compute units without work or
 // with a second block after the others are done. Cut into s parts, W blocks are
@@ -923,18 +926,20 @@ static bool wide_blocks(int64_t Tq, int B, int H) { return mla_blocks(Tq, B, 256
 // longest alone), a part takes 1.3 us per tile and 4 us to begin and end, and
 // writing, reading and joining its rows adds 27 ns of the device's time, 8 us
 // with the join's launch. The rule takes the s that this makes cheapest, for
-// requests of average length (the host does not know theirs).
+// requests of average length.
 // Measured, whole against the rule's parts: 512 queries behind 8000 tokens on
 // 16 heads 167 and 64 us; 100 behind 100000 on 8 heads 2010 and 158 us; 550 and
 // 512 behind 7400 on 32 heads 315 and 272 us. Left whole by the rule, whole
 // against two parts: 512 behind 8000 on 128 heads 433 and 456 us, two of 512
 // with 1200 keys on 16 heads 35.2 and 37.3 us.
-int mla_prefill_parts(int B, int64_t Tq, int64_t Tk, int H) {
-  if (B < 1 || wide_blocks(Tq, B, H)) return 1;
-  constexpr double kUnits = 256, kTileUs = 1.3, kEndsUs = 4, kJoinUs = 8, kRowsUs = 0.027;
+static int narrow_parts(int64_t Tq, int64_t Tk, int B, int H) {
+  // (from eight blocks per compute unit on, parts have little left to even out;
+  // this bounds the workspace and the launches)
+  if (mla_blocks(Tq, B, 128) * H >= 8 * kUnits) return 1;
+  constexpr double kTileUs = 1.3, kEndsUs = 4, kJoinUs = 8, kRowsUs = 0.027;
   constexpr int kMost = 16;
   const double q = (double)Tq / B, longest = (double)Tk / B / kBn, mean = std::max(longest - q / (2 * kBn), longest / 2);
-  const double W = std::ceil(q / 128) * B * H;
+  const double W = average_blocks(Tq, B, H, 128);
   int parts = 1;
   double best = 0;
   for (int s = 1; s <= kMost && (s == 1 || s * kPartTiles <= longest); ++s) {
@@ -948,9 +953,29 @@ int mla_prefill_parts(int B, int64_t Tq, int64_t Tk, int H) {
   return parts;
 }
 
+// Blocks of 256 queries where there are more than one and a half of them per
+// compute unit. Measured, 256 against 128 queries a block: 4096 tokens on 32
+// heads (512 blocks) 172 and 220 us, 3100 behind 30000 on 32 heads (416) 1.99
+// and 2.35 ms, two requests of 6000 to 8192 tokens on 128 heads 3.65 and 4.44
+// ms. With fewer, 128: 2300 behind 30000 on 32 heads (288) 1.93 and, in parts,
+// 1.73 ms, two chunks of 510 behind 7400 on 32 heads (128) 239 and 188 us; in
+// between it depends on the lengths (300 blocks: within 10% either way).
+// Requests of up to 128 queries have as many blocks of either size, which take
+// about as long (100 behind 2000, 16 requests on 32 heads: 132 and 142 us; one
+// behind 2000: 108 and 109 us), so only what blocks of 128 in parts are good for
+// counts (one behind 30000, 5 requests on 128 heads: 2.10 and 1.86 ms).
+static bool wide_blocks(int64_t Tq, int64_t Tk, int B, int H) {
+  const double wide = average_blocks(Tq, B, H, 256);
+  return wide > 1.5 * kUnits && (wide < average_blocks(Tq, B, H, 128) || narrow_parts(Tq, Tk, B, H) == 1);
+}
+
+int mla_prefill_parts(int B, int64_t Tq, int64_t Tk, int H) {
+  return B < 1 || wide_blocks(Tq, Tk, B, H) ? 1 : narrow_parts(Tq, Tk, B, H);
+}
+
 hipError_t launch_mla_prefill(const MlaPrefill& p, hipStream_t stream) {
   const int64_t wide = mla_blocks(p.Tq, p.B, 256), units = mla_blocks(p.Tq, p.B, 128);
-  if (wide_blocks(p.Tq, p.B, p.H)) {
+  if (wide_blocks(p.Tq, p.Tk, p.B, p.H)) {
     hipLaunchKernelGGL((mla_fwd_kernel<8, false>), dim3(unit_grid(wide, p.H)), dim3(512), 0, stream, p, (int)wide);
   } else if (p.parts == 1) {
     hipLaunchKernelGGL((mla_fwd_kernel<4, false>), dim3(unit_grid(units, p.H)), dim3(256), 0, stream, p, (int)units);

@@ -71,6 +71,19 @@ def test_prefill_workspace(L):
     assert _prefill(L, **many, ws=NULL) == -1 and _prefill(L, **many, ws=P + 8) == -3
 
 
+def test_prefill_workspace_of_filled_devices(L):
+    # Blocks of 256 queries, which are not cut in parts, from one and a half per compute unit on: counted for requests
+    # of average length, not with one more for each of them.
+    ws = L.fp8bs_mla_prefill_workspace_bytes
+    assert ws(1, 4200, 34200, 32) == 0                               # 17 blocks on 32 heads
+    assert ws(1, 2300, 32300, 32) > 0                                # 9 blocks
+    # one block of 128 holds a request's queries: parts where the device's last turn would be a short one
+    assert ws(5, 5, 5 * 30001, 128) > 0 and ws(7, 7, 7 * 20001, 128) > 0
+    assert ws(8, 8, 8 * 20001, 128) == 0                             # whole turns
+    # the workspace stays bounded
+    assert ws(1 << 20, 1 << 20, (1 << 31) - 1, 8) == 0
+
+
 def test_prefill_bwd_refusals(L):
     def call(**kw):
         a = dict(dout=P, q=P, qs=384, kv=P, kvs=512, r=P, rs=64, out=P, lse=P, cq=P, ck=P, B=2, Tq=10, Tk=12, H=2,

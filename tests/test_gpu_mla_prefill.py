@@ -250,6 +250,12 @@ def test_both_sides_of_the_block_size_rule(dev, H):
     _sampled(dev, [(300, 300), (212, 700)], H, [0, 3, H // 2, H - 1], True, seed=H)
 
 
+@pytest.mark.parametrize("H", [192, 193])
+def test_one_and_a_half_blocks_per_compute_unit(dev, H):
+    # (two blocks of 256 queries, by the average, on 256 compute units: blocks of 128 up to here, of 256 from here on)
+    _sampled(dev, [(300, 300), (212, 700)], H, [0, 3, 100, H - 1], True, seed=H)
+
+
 def test_blocks_of_256_queries_with_gaps_and_in_a_graph(dev):
     H = 128
     (q, kv, kr, dout, tq, tk), ref = _sampled(dev, MIXED, H, [5], True, seed=1)
