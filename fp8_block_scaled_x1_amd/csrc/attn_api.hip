@@ -14,7 +14,7 @@
 namespace {
 
 constexpr int64_t kI32 = (int64_t)1 << 31;
-constexpr int kTile = 64;
+constexpr int kTile = fp8bs::kMlaDecodeTile;
 
 bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 bool off4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }

@@ -65,6 +65,7 @@ struct MlaDecode {
   float* part_ml;         // [2 groups + B][rows][2]
 };
 
+constexpr int kMlaDecodeTile = 64;      // tokens
 // Rows per workgroup: 64 halve the tiles' traffic against 32 (128 rows of 128
 // requests: 156 us, with 32 each 200 us); where there are no more than 32, the
 // waves of the others only load (32 rows of 8 requests, FP8: 77 us, with

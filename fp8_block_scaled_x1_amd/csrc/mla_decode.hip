@@ -56,7 +56,7 @@ namespace fp8bs {
 
 namespace {
 
-constexpr int kTile = 64;            // tokens per tile
+constexpr int kTile = kMlaDecodeTile;      // tokens per tile
 constexpr int kLatent = 512, kRope = 64, kKey = kLatent + kRope;
 constexpr int kThreads = 256;
 // The weights' reference only follows the running maximum once that is more
