@@ -118,7 +118,6 @@ constexpr int kJoinSlices = 16;      // workgroups of the join per block of 128 
 //
 // Bound by the matrix unit's rate at the clock that the power limit leaves: the
 // two long requests run at 1.0 PFLOP/s, 0.53 of the unit's cycles at 1.9 GHz.
-// Loads, LDS reads and exponentials are worth 8 to 11% each.
 // With SPLIT the tiles of a block are shared by several workgroups, which leave
 // FP32 partials (output, maximum, sum) for the join below.
 template <int NW, bool SPLIT>
@@ -244,10 +243,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
   int buf = 0;
   // Tile t, whose scores are in s; those of tile t+1 go to sn.
   auto step = [&](int t, f32x16 (&s)[2], f32x16 (&sn)[2]) {
-    if (t + NBUF - 1 < nt)
-      attn_wait<(NBUF - 3) * Load::kLoads>();
-    else
-      attn_wait<0>();
+    attn_wait<0>();
     attn_barrier();
     const int at = buf * kFwdTile, next = buf + 1 == NBUF ? 0 : buf + 1, prev = buf == 0 ? NBUF - 1 : buf - 1;
     const bool load = loaded < nt;
@@ -411,6 +407,16 @@ __global__ __launch_bounds__(256) void mla_fwd_join_kernel(const MlaPrefill p, i
   }
 }
 
+// A number as a type, for a function whose code depends on it.
+template <int N>
+struct Const {
+  static constexpr int value = N;
+};
+
+constexpr int kBq = 64;
+constexpr int kQNope = kBq * 256, kQRope = kBq * 128, kDo = kBq * 256;
+constexpr int kBwdTile = kQNope + kQRope + kDo + 2 * kBq * 4;
+
 // Gradients of keys and values: 32 keys are a pair of waves' work, which share
 // a SIMD, while 32 queries at a time pass, in tiles of 64 (Q, dO, lse, D). The
 // first of the pair forms the scores and the weights, hands the weights (FP32)
@@ -423,15 +429,6 @@ __global__ __launch_bounds__(256) void mla_fwd_join_kernel(const MlaPrefill p, i
 // 0.81 ms, 0.85 PFLOP/s; 20 products of 32 cycles a wave and step leave the
 // matrix unit 0.39 busy at 2.2 GHz, the rest is what a step's chain waits for:
 // products, exponentials, LDS and the barrier between the two waves.
-template <int N>
-struct Const {
-  static constexpr int value = N;
-};
-
-constexpr int kBq = 64;
-constexpr int kQNope = kBq * 256, kQRope = kBq * 128, kDo = kBq * 256;
-constexpr int kBwdTile = kQNope + kQRope + kDo + 2 * kBq * 4;
-
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void mla_dkv_kernel(const MlaPrefill p,
                                                                                             int units) {
   constexpr int BK = 128, NBUF = 3, kLoads = 2 + 2 + 1 + 1, kAhead = 6;
