@@ -619,19 +619,18 @@ __global__ __launch_bounds__(256 * kTeams) __attribute__((amdgpu_waves_per_eu(2)
 // the shared form, the prefix's with the request's own). W waves per row, lane
 // l columns 8l .. 8l+7; all pieces' maxima are read at once, so every load of
 // a piece's output is under way before the first is needed.
-struct Pieces {      // of one row in one problem: part(i), i < n
-  const MlaDecode* p;
-  int n, row;
+struct Pieces {      // of one row in one problem: at(i), i < n
+  int rows, n, row;
   int64_t first;      // the first piece's slot; the others lie 2 slots apart from `rest`
   int64_t rest;
   bool done;          // the row's result is written already
-  __device__ __forceinline__ int64_t at(int i) const { return (i == 0 ? first : rest + 2 * (int64_t)i) * p->rows + row; }
+  __device__ __forceinline__ int64_t at(int i) const { return (i == 0 ? first : rest + 2 * (int64_t)i) * rows + row; }
 };
 
 __device__ __forceinline__ Pieces pieces_of(const MlaDecode& p, int64_t o) {
   const int lane = threadIdx.x & 63;
   const int b = (int)(o / p.rows);
-  Pieces r{&p, 0, (int)(o - (int64_t)b * p.rows), 0, 0, false};
+  Pieces r{p.rows, 0, (int)(o - (int64_t)b * p.rows), 0, 0, false};
   int before = 0, all = 0, own = 0;      // tiles before the request, of all, its own
   for (int b0 = 0; b0 < p.B; b0 += 64) {
     const int n = b0 + lane < p.B ? tiles_of(clamp_len(p, b0 + lane)) : 0, incl = wave_scan(n);
