@@ -3,7 +3,9 @@
 
 Every function has the name of the C entry point it calls, checks the tensors
 it is given, allocates the outputs and the workspace with torch and calls the
-library on the current torch stream of the inputs' device.
+library on the current torch stream of the inputs' device. Results carry no
+autograd graph, whatever their inputs require: fp8bs_mla_prefill_bwd gives the
+gradients (examples/latent_attention.py wraps the two in an autograd function).
 """
 
 import ctypes

@@ -39,10 +39,10 @@
 // KB into LDS 1.4 us; two tiles fill the LDS, so a tile's phases (scores,
 // exchange, weights, values) follow each other for all waves, with only the
 // next tile's loads beside them. 192 requests of 32 heads behind 16000 common
-// tokens: 0.27 ms, 0.8 PFLOP/s. From HBM a tile costs 4.0 us: 128 requests of
+// tokens: 0.27 ms, 0.8 PFLOP/s. From HBM a tile costs 3.7 us: 128 requests of
 // 300 to 4500 tokens on 128 heads, 387 MB: 0.16 ms with the join. FP8 cache, 32
-// rows: 256 MB in 70 us, 3.7 TB/s, bound by the codes' conversion and the same
-// phases.
+// rows: 256 MB in 64 us, 4.0 TB/s, bound by the codes' conversion and the same
+// phases, half of the waves only loading.
 //
 // Roundings below 32 bits: probabilities (times the scale, FP8) to BF16 for
 // the matrix unit (relative 2^-8 at most each, on the terms of a mean), and the output.
