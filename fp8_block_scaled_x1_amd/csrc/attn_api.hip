@@ -2,30 +2,11 @@
 // validation, then the launches on the caller's stream. Declarations and the
 // meaning of every argument are in include/fp8bs_attn.h.
 
-#include <hip/hip_runtime.h>
-#include <math.h>
-#include <stdint.h>
-
-#include <algorithm>
-
-#include "attn_internal.h"
-#include "fp8bs_attn.h"
+#include "attn_host.h"
 
 namespace {
 
-constexpr int64_t kI32 = (int64_t)1 << 31;
-constexpr int kTile = fp8bs::kMlaDecodeTile;
-
-bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
-bool off4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
-int status_of(hipError_t e) { return e == hipSuccess ? FP8BS_OK : FP8BS_ERR_LAUNCH; }
-hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
-bool bad_scale(float s) { return !(s > 0.f) || !isfinite(s); }
-
-// A launch has fewer than 2^32 threads.
-bool launch_too_large(int64_t workgroups, int threads) { return workgroups > (((int64_t)1 << 32) - 1) / threads; }
-
-int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
+constexpr DecodeShape kShape{fp8bs::kMlaDecodeTile, fp8bs::kMlaDecodeBlockRows};
 
 int prefill_sizes(int B, int64_t Tq, int64_t Tk, int H, int64_t q_stride, int64_t kv_stride, int64_t rope_stride,
                   float scale) {
@@ -42,88 +23,13 @@ int prefill_sizes(int B, int64_t Tq, int64_t Tk, int H, int64_t q_stride, int64_
   return FP8BS_OK;
 }
 
-// ---- absorbed form ----
-
-// Sizes of one problem (the requests' own tokens, or the prefix) and its
-// share of the workspace.
-struct DecodeSizes {
-  int B;                        // requests
-  int64_t rows, all_rows;       // of a request, of all
-  int64_t max_len;
-  int groups;
-  int64_t row_blocks;
-  int64_t pieces;               // partials of a request's rows
-  int64_t bytes_out() const { return align256(4 * pieces * rows * 512); }
-  int64_t bytes() const { return bytes_out() + align256(4 * pieces * rows * 2); }
-};
-
-int decode_sizes(int B, int64_t rows, int64_t all_rows, int64_t width, int page, bool joined, DecodeSizes& s) {
-  if (width > kI32 / page - kTile) return FP8BS_ERR_TOO_LARGE;
-  s.B = B;
-  s.rows = rows;
-  s.all_rows = all_rows;
-  s.max_len = width * page;
-  const int64_t tiles = (int64_t)B * ((s.max_len + kTile - 1) / kTile);
-  if (tiles >= kI32) return FP8BS_ERR_TOO_LARGE;
-  s.row_blocks = (rows + fp8bs::kMlaDecodeBlockRows - 1) / fp8bs::kMlaDecodeBlockRows;
-  s.groups = fp8bs::mla_decode_groups(s.row_blocks, tiles);
-  s.pieces = 2 * (int64_t)s.groups + (joined ? B : 0);
-  return FP8BS_OK;
-}
-
-int decode_plan(int B, int T, int H, int64_t width, int page, int64_t prefix_pages, DecodeSizes& own,
-                DecodeSizes& prefix) {
-  if (B < 0 || T < 1 || H < 1 || width < 0 || page < 1 || prefix_pages < 0) return FP8BS_ERR_SHAPE;
-  const int64_t rows = (int64_t)T * H, all = B * rows;
-  if (rows >= 1 << 24 || launch_too_large((all + 3) / 4, 256)) return FP8BS_ERR_TOO_LARGE;      // the join: a wave a row
-  int st = decode_sizes(B, rows, all, width, page, prefix_pages > 0, own);
-  if (st != FP8BS_OK || prefix_pages == 0) return st;
-  // the prefix: every block of everyone's rows is a request over the same tokens
-  const int block = (int)std::max<int64_t>(1, std::min<int64_t>(all, fp8bs::kMlaDecodeBlockRows));
-  return decode_sizes((int)((all + block - 1) / block), block, all, prefix_pages, page, true, prefix);
-}
-
-void fill(fp8bs::MlaDecode& p, const uint16_t* q, const void* cache, const float* scales, const uint16_t* rope,
-          int64_t pages, int page, const int32_t* table, int64_t width, const int32_t* lens, const DecodeSizes& s,
-          float scale, uint16_t* out, float* lse, bool join, char*& ws) {
-  p.q = q;
-  p.cache = static_cast<const char*>(cache);
-  p.scales = reinterpret_cast<const char*>(scales);
-  p.rope = reinterpret_cast<const char*>(rope);
-  p.table = table;
-  p.lens = lens;
-  p.table_stride = width;
-  p.len_stride = 1;
-  p.B = s.B;
-  p.rows = (int)s.rows;
-  p.all_rows = s.all_rows;
-  p.pages = (int)pages;
-  p.page = page;
-  p.max_len = (int)s.max_len;
-  // tok / page for 0 <= tok < 2^31: with 2^L the next power of two, the
-  // multiplier floor(2^(31+L) / page) + 1 errs by at most 2^L in 2^(31+L)
-  int L = 0;
-  while (((int64_t)1 << L) < page) ++L;
-  p.page_shift = 31 + L;
-  p.page_magic = (uint32_t)(((uint64_t)1 << (31 + L)) / (uint64_t)page + 1);
-  p.scale_log2 = scale * 1.4426950408889634f;
-  p.row_blocks = (int)s.row_blocks;
-  p.groups = s.groups;
-  p.join = join;
-  p.out = out;
-  p.lse = lse;
-  p.part = reinterpret_cast<float*>(ws);
-  p.part_ml = reinterpret_cast<float*>(ws + s.bytes_out());
-  ws += s.bytes();
-}
-
 int decode(const uint16_t* q, int kind, const void* cache, const float* scales, const uint16_t* rope, int64_t pages,
            int page, const int32_t* prefix_table, int64_t prefix_pages, const int32_t* prefix_len,
            const int32_t* table, int64_t width, const int32_t* lens, int B, int T, int H, float scale, uint16_t* out,
            float* lse, void* workspace, void* stream) {
   if (kind != FP8BS_CACHE_BF16 && kind != FP8BS_CACHE_FP8) return FP8BS_ERR_MODE;
   DecodeSizes own{}, prefix{};
-  const int st = decode_plan(B, T, H, width, page, prefix_pages, own, prefix);
+  const int st = decode_plan(kShape, B, T, H, width, page, prefix_pages, own, prefix);
   if (st != FP8BS_OK) return st;
   if (pages < 0) return FP8BS_ERR_SHAPE;
   if (pages >= kI32) return FP8BS_ERR_TOO_LARGE;
@@ -237,7 +143,7 @@ int fp8bs_mla_prefill_bwd(const uint16_t* dout, const uint16_t* q, int64_t q_str
 
 int64_t fp8bs_mla_decode_workspace_bytes(int B, int T, int H, int64_t table_width, int page, int64_t prefix_pages) {
   DecodeSizes own{}, prefix{};
-  const int st = decode_plan(B, T, H, table_width, page, prefix_pages, own, prefix);
+  const int st = decode_plan(kShape, B, T, H, table_width, page, prefix_pages, own, prefix);
   if (st != FP8BS_OK) return st;
   return own.bytes() + (prefix_pages > 0 ? prefix.bytes() : 0);
 }

@@ -47,10 +47,7 @@
 // Roundings below 32 bits: probabilities (times the scale, FP8) to BF16 for
 // the matrix unit (relative 2^-8 at most each, on the terms of a mean), and the output.
 
-#include <atomic>
-
-#include "attn_internal.h"
-#include "mla_tiles.h"
+#include "mla_paged.h"
 
 namespace fp8bs {
 
@@ -58,7 +55,6 @@ namespace {
 
 constexpr int kTile = kMlaDecodeTile;      // tokens per tile
 constexpr int kLatent = 512, kRope = 64, kKey = kLatent + kRope;
-constexpr int kThreads = 256;
 // The weights' reference only follows the running maximum once that is more
 // than 2^8 above it: weights up to 2^8 cost no precision in FP32 or BF16, and
 // the accumulators are rescaled a few times per request instead of per tile.
@@ -72,99 +68,6 @@ struct Tile {
   static constexpr int kScaleBytes = FP8 ? kTile * 16 : 0;        // [group][token]
   static constexpr int kBytes = kLatentBytes + kRopeBytes + kScaleBytes;
 };
-
-// The tiles of a request, and the request a tile belongs to.
-struct Cursor {
-  int b;        // request
-  int len;      // its tokens
-  int tile;     // tile inside it
-  int tiles;    // its tiles
-  int left;     // tiles left in the group's range, this one included
-};
-
-__device__ __forceinline__ int clamp_len(const MlaDecode& p, int b) { return min(max(p.lens[b * p.len_stride], 0), p.max_len); }
-
-__device__ __forceinline__ void advance(const MlaDecode& p, Cursor& c) {
-  --c.left;
-  if (++c.tile < c.tiles || c.left <= 0) return;
-  do {
-    ++c.b;
-    c.len = c.b < p.B ? __builtin_amdgcn_readfirstlane(clamp_len(p, c.b)) : 0;
-  } while (c.len == 0 && c.b < p.B);
-  c.tile = 0;
-  c.tiles = (c.len + kTile - 1) / kTile;
-}
-
-__device__ __forceinline__ int wave_scan(int v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int x = __shfl_up(v, d, 64);
-    if (lane >= d) v += x;
-  }
-  return v;
-}
-
-// The groups' ranges of `total` tiles: consecutive, of equal length but for one
-// tile, the longer ones (and, if there are fewer tiles than groups, those that
-// have any) first.
-struct Ranges {
-  int each, longer;
-  __device__ __forceinline__ Ranges(int total, int groups)
-      : each(total / groups), longer(total - total / groups * groups) {}
-  __device__ __forceinline__ int start(int g) const { return g * each + min(g, longer); }
-  __device__ __forceinline__ int of(int t) const {      // the group of tile t
-    const int head = longer * (each + 1);
-    return t < head ? t / (each + 1) : longer + (t - head) / max(each, 1);
-  }
-};
-
-__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
-
-// The range of group g as a cursor on its first tile (left = 0: it has none).
-__device__ __forceinline__ Cursor first_tile(const MlaDecode& p, int g) {
-  const int lane = threadIdx.x & 63;
-  // tiles of all requests; up to 64 requests are read once
-  int len = 0, incl = 0, total = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 64) {
-    len = b0 + lane < p.B ? clamp_len(p, b0 + lane) : 0;
-    incl = wave_scan(tiles_of(len));
-    total += __builtin_amdgcn_readlane(incl, 63);
-  }
-  const Ranges r(total, p.groups);
-  const int t = r.start(g), left = r.start(g + 1) - t;
-  if (left <= 0) return Cursor{0, 0, 0, 0, 0};
-  int base = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 64) {
-    if (p.B > 64) {
-      len = b0 + lane < p.B ? clamp_len(p, b0 + lane) : 0;
-      incl = wave_scan(tiles_of(len));
-    }
-    const uint64_t hit = __ballot(t < base + incl);
-    if (hit) {
-      const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
-      Cursor c;
-      c.b = b0 + l;
-      c.len = __builtin_amdgcn_readlane(len, l);
-      c.tiles = tiles_of(c.len);
-      c.tile = t - base - (__builtin_amdgcn_readlane(incl, l) - c.tiles);
-      c.left = left;
-      return c;
-    }
-    base += __builtin_amdgcn_readlane(incl, 63);
-  }
-  return Cursor{0, 0, 0, 0, 0};
-}
-
-// The flat cache token (page * page size + slot) of token `tok`, given its
-// page's entry in the block table.
-__device__ __forceinline__ int page_of(const MlaDecode& p, int tok) {
-  return (int)(((uint64_t)(uint32_t)tok * p.page_magic) >> p.page_shift);
-}
-
-// Token of the tile's row `lane`. Tokens past the end repeat the last one:
-// always cached, and masked by its position.
-__device__ __forceinline__ int row_token(const Cursor& c, int lane) { return min(c.tile * kTile + lane, c.len - 1); }
 
 __device__ __forceinline__ const char* lane_ptr(const char* base, int64_t off, int from) {
   const uint64_t a = (uint64_t)(base + off);
@@ -188,7 +91,7 @@ struct Loader {
   const int64_t flat;
   const int chunk;
   __device__ __forceinline__ static int64_t flat_of(const MlaDecode& p, const Cursor& c, int lane, int entry) {
-    const int tok = row_token(c, lane);
+    const int tok = row_token<kTile>(c, lane);
     return (int64_t)min(max(entry, 0), p.pages - 1) * p.page + (tok - page_of(p, tok) * p.page);
   }
   __device__ __forceinline__ Loader(const MlaDecode& p_, const Cursor& c, int r0_, int lane_, int entry, uint32_t lds_)
@@ -289,7 +192,7 @@ __global__ __launch_bounds__(256 * kTeams) __attribute__((amdgpu_waves_per_eu(2)
   const int xcd = block % kAttnXcds;
   const int wg = xcd * per + min(xcd, rest) + block / kAttnXcds;
   const int g = wg / p.row_blocks;
-  Cursor cur = first_tile(p, g);
+  Cursor cur = first_tile<kTile>(p, g);
   if (cur.left == 0) return;
 
   const uint32_t lds_tiles = lds_offset(tiles);
@@ -299,12 +202,12 @@ __global__ __launch_bounds__(256 * kTeams) __attribute__((amdgpu_waves_per_eu(2)
   Cursor nxt = cur;      // the tile that is loaded next
   Cursor ent = cur;      // the tile whose block-table entries are fetched next
   auto fetch_entries = [&] {
-    const int* src = p.table + (int64_t)ent.b * p.table_stride + page_of(p, row_token(ent, lane));
+    const int* src = p.table + (int64_t)ent.b * p.table_stride + page_of(p, row_token<kTile>(ent, lane));
     if constexpr (NBUF == 2)
       entry = *src;
     else
       dma4(src, lds_entries);
-    advance(p, ent);
+    advance<kTile>(p, ent);
   };
   auto start_next = [&](int to) {      // the loads of the tile `nxt`, into buffer `to`
     if constexpr (NBUF > 2) {
@@ -313,7 +216,7 @@ __global__ __launch_bounds__(256 * kTeams) __attribute__((amdgpu_waves_per_eu(2)
     }
     const int e = opaque(entry);      // waited for here, before the next fetch is under way
     const Cursor c = nxt;
-    advance(p, nxt);
+    advance<kTile>(p, nxt);
     if (ent.left > 0) fetch_entries();
     return Load(p, c, wave * kRows, lane, e, lds_tiles + to * T::kBytes);
   };
@@ -377,7 +280,7 @@ __global__ __launch_bounds__(256 * kTeams) __attribute__((amdgpu_waves_per_eu(2)
       auto step = [&] {
         last = cur.tile + 1 == cur.tiles || cur.left == 1;
         if (last) return;
-        advance(p, cur);
+        advance<kTile>(p, cur);
         buf = buf + 1 == NBUF ? 0 : buf + 1;
       };
       // any wave's wish to raise the reference: the answer is the same for all
@@ -610,154 +513,9 @@ __global__ __launch_bounds__(256 * kTeams) __attribute__((amdgpu_waves_per_eu(2)
       }
     }
     first = false;
-    advance(p, cur);
+    advance<kTile>(p, cur);
     buf = buf + 1 == NBUF ? 0 : buf + 1;
   }
-}
-
-// Joins the partials of the rows whose request was cut between groups (and, in
-// the shared form, the prefix's with the request's own). W waves per row, lane
-// l columns 8l .. 8l+7; all pieces' maxima are read at once, so every load of
-// a piece's output is under way before the first is needed.
-struct Pieces {      // of one row in one problem: at(i), i < n
-  int rows, n, row;
-  int64_t first;      // the first piece's slot; the others lie 2 slots apart from `rest`
-  int64_t rest;
-  bool done;          // the row's result is written already
-  __device__ __forceinline__ int64_t at(int i) const { return (i == 0 ? first : rest + 2 * (int64_t)i) * rows + row; }
-};
-
-__device__ __forceinline__ Pieces pieces_of(const MlaDecode& p, int64_t o) {
-  const int lane = threadIdx.x & 63;
-  const int b = (int)(o / p.rows);
-  Pieces r{p.rows, 0, (int)(o - (int64_t)b * p.rows), 0, 0, false};
-  int before = 0, all = 0, own = 0;      // tiles before the request, of all, its own
-  for (int b0 = 0; b0 < p.B; b0 += 64) {
-    const int n = b0 + lane < p.B ? tiles_of(clamp_len(p, b0 + lane)) : 0, incl = wave_scan(n);
-    if (b >= b0 && b < b0 + 64) {
-      own = __builtin_amdgcn_readlane(n, b - b0);
-      before = all + __builtin_amdgcn_readlane(incl, b - b0) - own;
-    }
-    all += __builtin_amdgcn_readlane(incl, 63);
-  }
-  if (own == 0) return r;
-  const Ranges ranges(all, p.groups);
-  const int g0 = ranges.of(before), g1 = ranges.of(before + own - 1);
-  if (g0 == g1) {
-    r.done = !p.join;
-    r.n = 1;
-    r.first = 2 * (int64_t)p.groups + b;
-  } else {
-    r.n = g1 - g0 + 1;
-    r.first = 2 * (int64_t)g0 + (ranges.start(g0) < before ? 1 : 0);
-    r.rest = 2 * (int64_t)g0;
-  }
-  return r;
-}
-
-template <int W>
-__global__ __launch_bounds__(kThreads) void mla_join_kernel(const MlaDecode p, const MlaDecode prefix) {
-  constexpr int kRowsPerBlock = kThreads / 64 / W, kBatch = 4;
-  __shared__ float2 ml[W > 1 ? W : 1];
-  __shared__ __align__(16) float sums[W > 1 ? W : 1][512];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wave % W;
-  const int64_t o = (int64_t)blockIdx.x * kRowsPerBlock + wave / W;
-  if (o >= p.all_rows) return;
-  const Pieces own = pieces_of(p, o);
-  if (own.done) return;
-  Pieces pre{};
-  if (p.join) pre = pieces_of(prefix, o);
-  const int n = own.n + pre.n;
-  // this wave's pieces: every W-th
-  float m = neg_inf(), l = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int i0 = w; i0 < n; i0 += 64 * W) {
-    const int i = i0 + lane * W;      // lane's piece
-    const bool mine = i < own.n;
-    float2 x = make_float2(neg_inf(), 0.f);
-    if (i < n) x = *reinterpret_cast<const float2*>((mine ? p.part_ml : prefix.part_ml) + 2 * (mine ? own.at(i) : pre.at(i - own.n)));
-    float mn = x.x;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) mn = max_nan(mn, __shfl_xor(mn, d, 64));
-    mn = max_nan(mn, m);
-    const float ref = mn == neg_inf() ? 0.f : mn;
-    const float old = exp2_fast(m - ref), weight = exp2_fast(x.x - ref);
-    float add = x.y * weight;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) add += __shfl_xor(add, d, 64);
-    l = fmaf(l, old, add);
-    m = mn;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) acc[k] *= old;
-    const int count = min(64, (n - i0 + W - 1) / W);
-    for (int k0 = 0; k0 < count; k0 += kBatch) {
-      f32x4 v[kBatch][2];
-      float wt[kBatch];
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int kc = min(k0 + k, count - 1), j = i0 + kc * W;
-        const bool a = j < own.n;
-        const float* src = (a ? p.part : prefix.part) + (a ? own.at(j) : pre.at(j - own.n)) * kLatent + 8 * lane;
-        v[k][0] = *reinterpret_cast<const f32x4*>(src);
-        v[k][1] = *reinterpret_cast<const f32x4*>(src + 4);
-        const float got = __shfl(weight, kc, 64);
-        wt[k] = k0 + k < count ? got : 0.f;
-      }
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          acc[j] = fmaf(v[k][0][j], wt[k], acc[j]);
-          acc[4 + j] = fmaf(v[k][1][j], wt[k], acc[4 + j]);
-        }
-    }
-  }
-  if constexpr (W > 1) {
-    if (lane == 0) ml[w] = make_float2(m, l);
-    __syncthreads();
-    float mn = neg_inf();
-#pragma unroll
-    for (int k = 0; k < W; ++k) mn = max_nan(mn, ml[k].x);
-    const float ref = mn == neg_inf() ? 0.f : mn, x = exp2_fast(m - ref);
-    l = 0.f;
-#pragma unroll
-    for (int k = 0; k < W; ++k) l = fmaf(ml[k].y, exp2_fast(ml[k].x - ref), l);
-    m = mn;
-    f32x4 a, b;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      a[j] = acc[j] * x;
-      b[j] = acc[4 + j] * x;
-    }
-    *reinterpret_cast<f32x4*>(&sums[w][8 * lane]) = a;
-    *reinterpret_cast<f32x4*>(&sums[w][8 * lane + 4]) = b;
-    __syncthreads();
-    if (w > 0) return;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      acc[j] = 0.f;
-#pragma unroll
-      for (int k = 0; k < W; ++k) acc[j] += sums[k][8 * lane + j];
-    }
-  }
-  const float inv = inverse_of(l);
-  bf16x8 v;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = (__bf16)(acc[i] * inv);
-  *reinterpret_cast<bf16x8*>(p.out + o * kLatent + 8 * lane) = v;
-  if (lane == 0) p.lse[o] = lse_of(m, l);
-}
-
-int compute_units() {
-  static std::atomic<int> cached[64] = {};
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-  if (cached[dev] == 0) {
-    int n = 0;
-    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) n = 256;
-    cached[dev] = n;
-  }
-  return cached[dev];
 }
 
 // A BF16 tile has 74 KB, so two fit; of the FP8 tiles (41 KB) three do, which
@@ -803,9 +561,9 @@ hipError_t launch_mla_decode(const MlaDecode& own, const MlaDecode* prefix, bool
   // 156. Behind a prefix of 8000, of 32 requests 512 rows 50.7 and 60.0, 1024 of
   // 64 65.9 and 66.7, 2048 of 128 93.1 and 92.2.
   if (own.all_rows <= (prefix ? 2048 : 512))
-    hipLaunchKernelGGL(mla_join_kernel<4>, dim3((unsigned)own.all_rows), dim3(kThreads), 0, stream, own, head);
+    hipLaunchKernelGGL((mla_join_kernel<4, kTile>), dim3((unsigned)own.all_rows), dim3(kJoinThreads), 0, stream, own, head);
   else
-    hipLaunchKernelGGL(mla_join_kernel<1>, dim3((unsigned)((own.all_rows + 3) / 4)), dim3(kThreads), 0, stream, own, head);
+    hipLaunchKernelGGL((mla_join_kernel<1, kTile>), dim3((unsigned)((own.all_rows + 3) / 4)), dim3(kJoinThreads), 0, stream, own, head);
   return hipGetLastError();
 }
 
