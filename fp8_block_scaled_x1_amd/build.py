@@ -16,7 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfp8bs.so")
 SOURCES = ["api.hip", "quant.hip", "gemm.hip", "moe.hip", "attn_api.hip", "mla_prefill.hip", "mla_decode.hip",
-           "verify.hip"]
+           "verify.hip", "serve_api.hip", "mla_cache.hip", "mla_decode4.hip", "moe_tokens.hip", "logprobs.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

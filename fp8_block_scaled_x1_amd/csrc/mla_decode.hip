@@ -553,17 +553,7 @@ hipError_t launch_mla_decode(const MlaDecode& own, const MlaDecode* prefix, bool
     launch_tiles<true>(two, fp8, stream);
   else if (prefix || own.max_len > 0)
     launch_tiles<false>(two, fp8, stream);
-  // Few rows have many pieces each: a workgroup per row. Many rows have one or
-  // two, and a wave per row has less to set up; behind a prefix they all have
-  // the prefix's as well. Whole calls of 3000 to 6000 tokens, workgroup and wave
-  // per row: 512 rows of one request 33.5 and 36.4 us, 768 of one 38.0 and 37.4,
-  // 1024 of one 43.4 and 38.2, of 8 requests 48.2 and 46.8; 16384 rows 178 and
-  // 156. Behind a prefix of 8000, of 32 requests 512 rows 50.7 and 60.0, 1024 of
-  // 64 65.9 and 66.7, 2048 of 128 93.1 and 92.2.
-  if (own.all_rows <= (prefix ? 2048 : 512))
-    hipLaunchKernelGGL((mla_join_kernel<4, kTile>), dim3((unsigned)own.all_rows), dim3(kJoinThreads), 0, stream, own, head);
-  else
-    hipLaunchKernelGGL((mla_join_kernel<1, kTile>), dim3((unsigned)((own.all_rows + 3) / 4)), dim3(kJoinThreads), 0, stream, own, head);
+  launch_mla_join<kTile>(own, head, prefix != nullptr, stream);
   return hipGetLastError();
 }
 

@@ -245,6 +245,21 @@ __global__ __launch_bounds__(kJoinThreads) void mla_join_kernel(const MlaDecode 
   if (lane == 0) p.lse[o] = lse_of(m, l);
 }
 
+template <int TILE>
+void launch_mla_join(const MlaDecode& own, const MlaDecode& head, bool behind_prefix, hipStream_t stream) {
+  // Few rows have many pieces each: a workgroup per row. Many rows have one or
+  // two, and a wave per row has less to set up; behind a prefix they all have
+  // the prefix's as well. Whole calls of 3000 to 6000 tokens, workgroup and wave
+  // per row: 512 rows of one request 33.5 and 36.4 us, 768 of one 38.0 and 37.4,
+  // 1024 of one 43.4 and 38.2, of 8 requests 48.2 and 46.8; 16384 rows 178 and
+  // 156. Behind a prefix of 8000, of 32 requests 512 rows 50.7 and 60.0, 1024 of
+  // 64 65.9 and 66.7, 2048 of 128 93.1 and 92.2.
+  if (own.all_rows <= (behind_prefix ? 2048 : 512))
+    hipLaunchKernelGGL((mla_join_kernel<4, TILE>), dim3((unsigned)own.all_rows), dim3(kJoinThreads), 0, stream, own, head);
+  else
+    hipLaunchKernelGGL((mla_join_kernel<1, TILE>), dim3((unsigned)((own.all_rows + 3) / 4)), dim3(kJoinThreads), 0, stream, own, head);
+}
+
 inline int compute_units() {
   static std::atomic<int> cached[64] = {};
   int dev = 0;

@@ -15,7 +15,7 @@
  * and gives the same bits for the same inputs. Sizes whose launch would pass
  * 2^32 - 1 threads are refused (FP8BS_ERR_TOO_LARGE). Pointers are 16-byte
  * aligned unless said otherwise; int32 and float32 side arrays (offsets,
- * lengths, tables, expert ids and weights, lse and so on) 4-byte.
+ * lengths, tables, expert ids and weights, lse, norm and so on) 4-byte.
  */
 #ifndef FP8BS_SERVE_H
 #define FP8BS_SERVE_H
@@ -62,7 +62,7 @@ extern "C" {
  * or whose table entry is not in [0, pages), is not written. No two tokens of
  * a call may go to one slot (pages that requests share are only read); what
  * such a slot then holds is not defined. All other slots keep what they hold.
- * Strides: multiples of 8, at least a token's numbers. page >= 1; pages * page
+ * Strides: multiples of 8, at least a token's numbers, below 2^31. page >= 1; pages * page
  * below 2^31.
  */
 FP8BS_API int fp8bs_mla_cache_write(const uint16_t* latent, int64_t latent_stride, const uint16_t* rope,
@@ -125,7 +125,7 @@ FP8BS_API int64_t fp8bs_mla_decode_fp4_workspace_bytes(int B, int T, int H, int6
  * each 128-wide partial sum scaled as it is added. Each chosen expert's
  * weights are read once. Inputs finite; a code 0x7F or 0xFF is a NaN.
  * 0 <= T <= 64, 1 <= topk <= 64, 1 <= E <= 1024; K and F multiples of 128, at
- * least 128 (FP8BS_ERR_TOO_LARGE above 2^20). workspace: at least
+ * least 128 (FP8BS_ERR_TOO_LARGE above 2^16). workspace: at least
  * fp8bs_moe_tokens_workspace_bytes(T, topk, F) bytes.
  */
 FP8BS_API int fp8bs_moe_tokens(const uint16_t* x, int T, int64_t K, const int32_t* topk_ids,
@@ -136,27 +136,30 @@ FP8BS_API int64_t fp8bs_moe_tokens_workspace_bytes(int T, int topk, int64_t F);
 
 /*
  * Log probabilities of given tokens: for every row x of logits and y = targets[t],
- *   lse = log sum_i exp(x_i), logprob = x_y - lse, entropy = lse - sum_i p_i x_i (p = exp(x - lse)),
+ *   m = max_i x_i, n = log sum_i exp(x_i - m), logprob = (x_y - m) - n,
+ *   entropy = n - sum_i p_i (x_i - m) (p_i = exp(x_i - m - n)),
  *   rank = how many entries come before y when ordered by (larger logit, smaller index),
- *   top_ids, top_logprobs: the first `top` entries in that order, x_i - lse.
+ *   top_ids, top_logprobs: the first `top` entries in that order, (x_i - m) - n.
  *   logits  [T][V] float32 or BF16 (dtype), `stride` numbers from row to row
  *   targets [T] int32: outside [0, V) (no token): logprob 0, rank -1
- *   logprob, entropy, lse [T] float32   rank [T] int32
+ *   logprob, entropy [T] float32   rank [T] int32
+ *   norm    [T][2] float32: m and n (their sum is the log of the sum of exp(x_i))
  *   top_ids [T][top] int32, top_logprobs [T][top] float32 (NULL where top is 0)
- * Entries of -inf have no probability. A row of nothing else has lse = -inf,
- * logprob and top_logprobs -inf and entropy 0. A NaN or +inf in a row gives NaN in its
- * logprob (of a token), entropy and lse; its rank and alternatives are then some, within range.
- * T >= 0, 1 <= V <= 2^20, 0 <= top <= min(V, 64), stride >= V. logits aligned
+ * Entries of -inf have no probability. A row of nothing else has m = -inf and
+ * n = 0, logprob and top_logprobs -inf and entropy 0. A NaN or +inf in a row
+ * gives NaN in its logprob (of a token), entropy and n; its rank and
+ * alternatives are then some, within range.
+ * T >= 0, 1 <= V <= 2^20, 0 <= top <= min(V, 64), V <= stride < 2^31. logits aligned
  * to its type. workspace: fp8bs_logprobs_workspace_bytes(T, V, top) bytes.
  */
 FP8BS_API int fp8bs_logprobs(const void* logits, int dtype, int64_t stride, const int32_t* targets,
-                      int64_t T, int64_t V, int top, float* logprob, float* entropy, float* lse,
+                      int64_t T, int64_t V, int top, float* logprob, float* entropy, float* norm,
                       int32_t* rank, int32_t* top_ids, float* top_logprobs, void* workspace,
                       void* stream);
 FP8BS_API int64_t fp8bs_logprobs_workspace_bytes(int64_t T, int64_t V, int top);
 
 /*
- * Its gradient: with lse and entropy as fp8bs_logprobs wrote them and
+ * Its gradient: with norm and entropy as fp8bs_logprobs wrote them and
  * d_logprob, d_entropy [T] float32 the gradients of logprob and entropy,
  *   d_logits_i = d_logprob * ([i == y] - p_i) - d_entropy * p_i * (log p_i + entropy)
  * (without the first term where targets[t] is no token), in FP32, rounded once
@@ -165,7 +168,7 @@ FP8BS_API int64_t fp8bs_logprobs_workspace_bytes(int64_t T, int64_t V, int top);
  *   d_logits [T][V], of dtype, contiguous, aligned to its type
  */
 FP8BS_API int fp8bs_logprobs_bwd(const void* logits, int dtype, int64_t stride, const int32_t* targets,
-                      const float* lse, const float* entropy, const float* d_logprob,
+                      const float* norm, const float* entropy, const float* d_logprob,
                       const float* d_entropy, int64_t T, int64_t V, void* d_logits, void* stream);
 
 /* FP8BS_SERVE_VERSION of the loaded library. */

@@ -1,0 +1,220 @@
+"""Log probabilities, entropy, ranks and alternatives on the GPU against the
+float64 oracle: whole numbers equal, the others within the bounds of FP32; the
+gradient against the formula and against differences."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import serve as os_
+
+import fp8_block_scaled_x1_amd as fb
+
+pytestmark = pytest.mark.gpu
+NAMES = ("logprob", "entropy", "norm", "rank", "top_ids", "top_logprobs")
+DTYPES = [torch.float32, torch.bfloat16]
+
+
+def _logits(T, V, seed, dtype, std=3.0, pad=0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn((T, V + pad), generator=g) * std).to(dtype)[:, :V]
+
+
+def _inside(got, want, bound, what):
+    got = got.double().cpu().numpy()
+    with np.errstate(invalid="ignore"):
+        bad = ~((np.isneginf(want) & np.isneginf(got)) | (np.abs(got - want) <= bound))
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} outside, first at {tuple(np.argwhere(bad)[0])}: " \
+                          f"{got[bad][0]} against {want[bad][0]} +- {bound[bad][0]}"
+
+
+def _on(dev, x):
+    """The same view of a copy on the GPU, rows as far apart."""
+    base = torch.empty((x.shape[0], x.stride(0) if x.shape[0] > 1 else x.shape[1]), dtype=x.dtype, device=dev)
+    y = base[:, :x.shape[1]]
+    y.copy_(x)
+    return y
+
+
+def _check(dev, x, targets, top):
+    targets = torch.as_tensor(targets, dtype=torch.int32)
+    xd = _on(dev, x)
+    got = dict(zip(NAMES, fb.fp8bs_logprobs(xd, targets.to(dev), top)))
+    want, bound = os_.logprobs(x.double().numpy(), targets.numpy(), top)
+    for n in ("rank", "top_ids"):
+        assert np.array_equal(got[n].cpu().numpy(), want[n]), f"{n}: {got[n].cpu().numpy()} against {want[n]}"
+    for n in bound:
+        _inside(got[n], want[n], bound[n], n)
+    g = torch.Generator().manual_seed(5)
+    dl, dh = torch.randn(len(x), generator=g), torch.randn(len(x), generator=g)
+    grad = fb.fp8bs_logprobs_bwd(xd, targets.to(dev), got["norm"], got["entropy"], dl.to(dev), dh.to(dev))
+    w, b = os_.logprobs_bwd(x.double().numpy(), targets.numpy(), dl.numpy(), dh.numpy(), torch.finfo(x.dtype).eps / 2)
+    assert grad.dtype == x.dtype and grad.is_contiguous()
+    _inside(grad, w, b, "gradient")
+    return got
+
+
+def _targets(T, V, seed):
+    return np.random.default_rng(seed).integers(0, V, T)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("V", [1, 2, 3, 7, 64, 255, 256, 1000, 8191, 8192, 8193, 16385, 40000])
+def test_vocabularies(dev, V, dtype):
+    _check(dev, _logits(5, V, V, dtype), _targets(5, V, V), min(V, 20))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("top", [0, 1, 2, 33, 63, 64])
+@pytest.mark.parametrize("V", [64, 9000])
+def test_alternatives(dev, top, V, dtype):
+    _check(dev, _logits(4, V, top, dtype), _targets(4, V, top), top)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("pad", [1, 3, 8, 96])
+def test_rows_apart(dev, pad, dtype):
+    _check(dev, _logits(6, 8200 + pad, pad, dtype, pad=pad), _targets(6, 8200, pad), 5)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_ties_go_to_the_lowest_index(dev, dtype):
+    x = torch.zeros((4, 17000), dtype=dtype)
+    x[1, ::7] = 1.0
+    x[2] = torch.arange(17000) % 3
+    x[3, 16000:16010] = -0.0                 # equal to 0
+    x[3, 100] = -1.0
+    _check(dev, x, [16999, 14, 5, 16005], 64)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_masked_entries(dev, dtype):
+    x = _logits(6, 20000, 4, dtype)
+    inf = float("inf")
+    x[0, 1:] = -inf                          # one entry left
+    x[1, :] = -inf                           # none
+    x[2, :19990] = -inf                      # fewer than alternatives asked for, all in the last chunk
+    x[3, ::2] = torch.finfo(dtype).min       # the type's lowest value
+    x[4, :] = torch.finfo(dtype).min
+    x[5, 8192:] = -inf
+    _check(dev, x, [0, 3, 5, 2, 7, 9000], 20)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_far_apart_and_large(dev, dtype):
+    x = _logits(4, 9000, 6, dtype, std=100.0)
+    x[1] += 10000.0
+    x[2] -= 10000.0
+    x[3] = 0.0
+    _check(dev, x, [1, 2, 3, 4], 10)
+
+
+def test_targets_that_are_no_token(dev):
+    got = _check(dev, _logits(4, 500, 7, torch.float32), [-1, 500, -100, 499], 3)
+    assert got["rank"].tolist()[:3] == [-1, -1, -1] and got["logprob"][:3].tolist() == [0, 0, 0]
+
+
+@pytest.mark.parametrize("V", [300, 20000])
+def test_nan_and_infinity_stay_in_their_rows(dev, V):
+    x = _logits(5, V, 8, torch.float32)
+    y = _targets(5, V, 8)
+    clean = _check(dev, x, y, 7)
+    x[1, V - 5] = float("nan")
+    x[3, 17] = float("inf")
+    args = x.to(dev), torch.as_tensor(y, dtype=torch.int32, device=dev)
+    got = dict(zip(NAMES, fb.fp8bs_logprobs(*args, 7)))
+    for n in NAMES:
+        assert torch.equal(got[n][[0, 2, 4]], clean[n][[0, 2, 4]]), n
+    for n in ("logprob", "entropy"):
+        assert torch.isnan(got[n][[1, 3]]).all(), n
+    assert torch.isnan(got["norm"][[1, 3], 1]).all()
+    assert ((got["top_ids"] >= 0) & (got["top_ids"] < V)).all() and ((got["rank"] >= 0) & (got["rank"] < V)).all()
+    one = torch.ones(5, device=dev)
+    grad = fb.fp8bs_logprobs_bwd(*args, got["norm"], got["entropy"], one, one)
+    assert torch.isnan(grad[[1, 3]]).any(1).all() and torch.isfinite(grad[[0, 2, 4]]).all()
+
+
+def test_adversarial_order(dev):
+    # one thread's entries above all others, then everything ascending and descending
+    x = _logits(3, 8192, 9, torch.float32)
+    x[0, 40:44] += 100.0
+    x[1] = torch.arange(8192).float()
+    x[2] = -torch.arange(8192).float()
+    _check(dev, x, [41, 8191, 8191], 64)
+
+
+def test_one_row_and_many(dev):
+    _check(dev, _logits(1, 129280, 10, torch.float32), [77], 20)
+    _check(dev, _logits(700, 50, 10, torch.bfloat16), _targets(700, 50, 10), 5)
+
+
+def test_largest_vocabulary(dev):
+    _check(dev, _logits(1, 1 << 20, 11, torch.bfloat16), [1 << 19], 64)
+
+
+def test_gradient_is_that_of_differences(dev):
+    # in 64 bits by central differences of the definition
+    T, V, eps = 3, 11, 1e-4
+    x, y = _logits(T, V, 12, torch.float32), _targets(T, V, 12)
+    dl, dh = np.array([0.7, -1.3, 0.2]), np.array([0.5, 0.1, -2.0])
+
+    def value(z):
+        r, _ = os_.logprobs(z, y, 0)
+        return r["logprob"] * dl + r["entropy"] * dh
+
+    want = np.zeros((T, V))
+    for i in range(V):
+        z = x.double().numpy()
+        up, down = z.copy(), z.copy()
+        up[:, i] += eps
+        down[:, i] -= eps
+        want[:, i] = (value(up) - value(down)) / (2 * eps)
+    args = x.to(dev), torch.as_tensor(y, dtype=torch.int32, device=dev)
+    _, entropy, norm, *_ = fb.fp8bs_logprobs(*args)
+    grad = fb.fp8bs_logprobs_bwd(*args, norm, entropy, *(torch.from_numpy(a).float().to(dev) for a in (dl, dh)))
+    # third derivatives of a few units times eps^2 / 6, and FP32
+    assert np.abs(grad.double().cpu().numpy() - want).max() <= 1e-6 + 2e-5
+
+
+@pytest.mark.parametrize("top", [0, 8])
+def test_same_bits_in_a_graph_and_on_a_stream(dev, top):
+    x, y = _logits(9, 30000, 13, torch.float32).to(dev), torch.as_tensor(_targets(9, 30000, 13), dtype=torch.int32, device=dev)
+    d = torch.randn(2, 9, device=dev)
+
+    def step():
+        r = fb.fp8bs_logprobs(x, y, top)
+        return (*r, fb.fp8bs_logprobs_bwd(x, y, r[2], r[1], d[0], d[1]))
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        res = step()
+    for i in range(3):
+        x.copy_(torch.randn(9, 30000, device=dev))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(res, step()):
+            assert torch.equal(a, b)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        again = step()
+    torch.cuda.current_stream().wait_stream(side)
+    for a, b in zip(res, again):
+        assert torch.equal(a, b)
+
+
+def test_no_rows_and_refusals(dev):
+    y = torch.zeros(3, dtype=torch.int32, device=dev)
+    r = fb.fp8bs_logprobs(torch.zeros((0, 5), device=dev), y[:0], 2)
+    assert r[0].shape == (0,) and r[4].shape == (0, 2)
+    x = torch.zeros((3, 10), device=dev)
+    for error, args in [(TypeError, (x.half(), y)), (TypeError, (x, y.long())), (ValueError, (x, y[:2])), (ValueError, (x.t(), y)),
+                        (ValueError, (x[0], y)), (ValueError, (x[:1].expand(3, 10), y)), (ValueError, (x.cpu(), y))]:
+        with pytest.raises(error):
+            fb.fp8bs_logprobs(*args)
+    for top in (-1, 11, 65):
+        with pytest.raises(fb.Fp8bsError):
+            fb.fp8bs_logprobs(x, y, top)
+    with pytest.raises(ValueError):
+        fb.fp8bs_logprobs_bwd(x, y, x[:, :2].contiguous(), x[0, :3].clone(), x[0, :2].clone(), x[0, :3].clone())
