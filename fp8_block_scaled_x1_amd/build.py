@@ -30,9 +30,10 @@ HIPCC_FLAGS = [
     "-Wno-unused-command-line-argument",
 ]
 
-# MFMA results straight into ordinary registers: these kernels fit in 256 of
-# them, and the accumulation registers would cost a copy per use
-FILE_FLAGS = {"mla_decode.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+# MFMA results straight into ordinary registers: these kernels' results fit in
+# 256 of them, and the accumulation registers would cost a copy per use
+FILE_FLAGS = {"mla_decode.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+              "mla_decode4.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 
 def hipcc():

@@ -2,21 +2,24 @@
 // formulas, the ranges of tiles, the partial results and their join are those
 // of the kernel over the BF16 and FP8 caches.
 //
-// A tile is 128 tokens, 32 a wave, and the waves of a workgroup do not meet
-// before the end of a request's part of the range: a wave holds its 32 rows'
-// queries (144 registers) and the whole of its output (256) and has its own
-// tiles in LDS. Codes go to LDS as they are (400 bytes a token by direct
-// loads, three tiles deep) and are read twice. For the scores a lane is a token
-// and reads 32 codes, one group, at a time: the converter makes exact BF16
-// operands of codes and the group's power of two. For the output a lane is 16
-// columns, half a group, of 8 tokens: the converter gives two columns of one
-// token, and a byte permutation pairs tokens. Scores are formed as keys x
-// queries, so a lane's weights are the operand of the product with the values.
+// A workgroup has 32 rows; its four waves have one SIMD each and 512 registers.
+// Scores: a wave forms those of 16 of a tile's 64 tokens and holds all of the
+// rows' queries. A lane is a token and a quarter of its groups: it loads its
+// codes from global memory (400 bytes a token, three tiles ahead, in
+// registers), and the converter turns 8 codes and their group's power of two
+// into an exact BF16 operand. Conversions run at a quarter of the rate of other
+// vector instructions, so an operand is formed once: it goes to the score
+// product and, as it is, to the tile's place in LDS, which the value product
+// reads transposed. Values: a wave adds all 64 tokens into its 128 columns.
+// Tiles alternate between two places, so a tile's values and the next tile's
+// scores are formed together and the waves meet once a tile; conversions,
+// matrix instructions and LDS fill each other's waits.
 //
 // Roundings below 32 bits: the weights to BF16 for the matrix unit (2^-9
 // relative, on the terms of a mean) and the output.
 
 #include <type_traits>
+#include <utility>
 
 #include "mla_paged.h"
 #include "serve_internal.h"
@@ -26,57 +29,73 @@ namespace fp8bs {
 namespace {
 
 constexpr int kTile = kFp4Tile, kWaves = 4, kWaveTokens = kTile / kWaves;
+static_assert(kTile == 64 && kWaveTokens == 16, "a wave's tokens are the rows of a 16x16x32 product");
 constexpr int kLatent = 512, kKey = 576;
-constexpr int kBufs = 3;
-constexpr int kCodeBytes = kWaveTokens * 256, kRopeBytes = kWaveTokens * 128, kScaleBytes = kWaveTokens * 16;
-constexpr int kBufBytes = kCodeBytes + kRopeBytes + kScaleBytes;
-constexpr int kCodeLoads = 8, kRopeLoads = 4, kLoads = kCodeLoads + kRopeLoads + 1;
+constexpr int kAhead = 3;                                  // tiles in registers
+constexpr int kRowBytes = 2 * kLatent;
+// A tile in LDS: latent numbers, weights (as the value product's operand), row maxima and wishes of the waves.
+constexpr int kWeightsAt = kTile * kRowBytes, kStatAt = kWeightsAt + kTile * 32 * 2;
+constexpr int kTileBytes = kStatAt + kWaves * 256;
 // The weights' reference follows the running maximum once that is more than
 // 2^8 above it (weights up to 2^8 cost no precision in FP32 or BF16).
 constexpr float kSlack = 8.f;
-// Output registers that the waves add up at a time, through the buffers of the tile that is done.
-constexpr int kJoinRegs = 2;
-static_assert(kJoinRegs * 64 * 64 <= kBufBytes, "a register of 16 blocks from 64 lanes");
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// The next tile of the range; lengths by scalar loads (the kernel writes none
+// of them), which leave the tiles' loads in flight alone.
+__device__ __forceinline__ void next_tile(const MlaDecode& p, Cursor& c) {
+  typedef const __attribute__((address_space(4))) int32_t* scalar_ptr;
+  --c.left;
+  if (++c.tile < c.tiles || c.left <= 0) return;
+  const scalar_ptr lens = (scalar_ptr)(uintptr_t)p.lens;
+  do {
+    ++c.b;
+    c.len = c.b < p.B ? min(max(lens[__builtin_amdgcn_readfirstlane(c.b * p.len_stride)], 0), p.max_len) : 0;
+  } while (c.len == 0 && c.b < p.B);
+  c.tile = 0;
+  c.tiles = tiles_of<kTile>(c.len);
+}
 
 struct Problems {
   MlaDecode p[2];
   int split;
 };
 
-__device__ __forceinline__ float pow2_byte(uint32_t word, int shift) { return __uint_as_float(((word >> shift) & 0xFFu) << 23); }
-
 template <int SEL>
 __device__ __forceinline__ uint32_t cvt2(uint32_t codes, float s) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, SEL));
 }
 // Eight codes of one token and group as an operand.
-__device__ __forceinline__ bf16x8 cvt8(uint32_t codes, float s) {
-  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-  return __builtin_bit_cast(bf16x8, u32x4{cvt2<0>(codes, s), cvt2<1>(codes, s), cvt2<2>(codes, s), cvt2<3>(codes, s)});
+__device__ __forceinline__ u32x4 cvt8(uint32_t codes, float s) {
+  return u32x4{cvt2<0>(codes, s), cvt2<1>(codes, s), cvt2<2>(codes, s), cvt2<3>(codes, s)};
 }
 
-// A wave's loads of its 32 tokens of a tile: lane l (and l + 32) holds token
-// l's slot. The 16-byte chunks of a token's codes lie permuted by its number
-// in the tile, those of its rotary numbers by half of it, so that a column of
-// chunks touches every LDS bank once.
-struct Loader {
-  const MlaDecode& p;
-  const int lane, slot;
-  const uint32_t lds;
-  __device__ __forceinline__ void issue(int n) const {
-    if (n < kCodeLoads) {
-      const int tok = 4 * n + (lane >> 4);
-      const int64_t s = __shfl(slot, tok, 64);
-      dma16(p.cache + s * 256 + (((lane & 15) ^ (tok & 15)) << 4), lds + 1024 * n);
-    } else if (n < kCodeLoads + kRopeLoads) {
-      const int i = n - kCodeLoads, tok = 8 * i + (lane >> 3);
-      const int64_t s = __shfl(slot, tok, 64);
-      dma16(p.rope + s * 128 + (((lane & 7) ^ ((tok >> 1) & 7)) << 4), lds + kCodeBytes + 1024 * i);
-    } else if (lane < kWaveTokens) {
-      dma16(p.scales + (int64_t)slot * 16, lds + kCodeBytes + kRopeBytes);
-    }
-  }
+__device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// A lane's part of its token: groups q, 4 + q, 8 + q and 12 + q (q = lane / 16),
+// 16 of the rotary numbers, and the token's 16 exponents.
+struct Raw {
+  u32x4 codes[4];
+  bf16x8 rope[2];
+  u32x4 exps;
 };
+
+// The 16-byte chunks of a token's numbers in LDS are permuted by the token, so
+// that 8 tokens at one chunk (written) and 4 at two (read) touch every bank once.
+__device__ __forceinline__ int swz(int r) { return ((r & 3) << 1) | ((r >> 2) & 1) | (r & 8); }
+
+// The value of the lane 16 away within a half, combined with this lane's (both get the result).
+__device__ __forceinline__ float quarter_max(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return max_nan(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float quarter_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
 
 template <bool TWO>
 __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(1, 1))) void mla_decode_fp4_kernel(
@@ -84,12 +103,12 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(1, 
   const bool second = TWO && (int)blockIdx.x >= problems.split;
   const MlaDecode& p = problems.p[second];
   const int block = blockIdx.x - (second ? problems.split : 0);
-  __shared__ __align__(1024) char tiles[kWaves * (kBufs * kBufBytes + 256)];      // then a wave's block-table entries
-  __shared__ float2 stats[kWaves][32];
+  __shared__ __align__(1024) char tiles[2 * kTileBytes];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int half = lane >> 5, row32 = lane & 31;
+  const int tok16 = lane & 15, q4 = lane >> 4;
+  const TileLane L(lane);
 
   // workgroup -> (group, row block), an XCD's consecutive, row blocks of a group first
   const int blocks = p.groups * p.row_blocks, per = blocks / kAttnXcds, rest = blocks % kAttnXcds;
@@ -99,222 +118,289 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(1, 
   Cursor cur = first_tile<kTile>(p, g);
   if (cur.left == 0) return;
 
-  char* const mine = tiles + wave * kBufs * kBufBytes;
-  const int* const entries = reinterpret_cast<const int*>(tiles + kWaves * kBufs * kBufBytes + 256 * wave);
-  const uint32_t lds_mine = lds_offset(mine), lds_entries = lds_offset(entries);
   Cursor nxt = cur;      // the tile that is loaded next
   Cursor ent = cur;      // the tile whose block-table entries are fetched next
-  auto token_of = [&](const Cursor& c) { return min(c.tile * kTile + kWaveTokens * wave + row32, c.len - 1); };
-  auto fetch_entries = [&] {
-    dma4(p.table + (int64_t)ent.b * p.table_stride + page_of(p, token_of(ent)), lds_entries);
-    advance<kTile>(p, ent);
+  auto token_of = [&](const Cursor& c) { return min(c.tile * kTile + kWaveTokens * wave + tok16, c.len - 1); };
+  // Past the range's end its last tile is loaded again: loads under a condition
+  // would make the waits for earlier ones wait for these too.
+  int entry;
+  auto fetch_entry = [&] {
+    entry = p.table[(int64_t)ent.b * p.table_stride + page_of(p, token_of(ent))];
+    if (ent.left > 1) next_tile(p, ent);
   };
-  auto start_next = [&](int to) {      // the loads of the tile `nxt`, into buffer `to`
-    const int entry = entries[lane], tok = token_of(nxt);
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    const Loader ld{p, lane, opaque(min(max(entry, 0), p.pages - 1) * p.page + (tok - page_of(p, tok) * p.page)),
-                    lds_mine + to * kBufBytes};
-    advance<kTile>(p, nxt);
-    if (ent.left > 0) fetch_entries();
-    return ld;
+  int64_t slot = 0;      // of the tile that is being loaded
+  auto next_slot = [&] {      // of the tile `nxt`, whose entries are here
+    const int tok = token_of(nxt);
+    slot = min(max(entry, 0), p.pages - 1) * p.page + (tok - page_of(p, tok) * p.page);
+    if (nxt.left > 1) next_tile(p, nxt);
+    fetch_entry();
   };
-  fetch_entries();
+  auto load_part = [&](Raw& r, int n) {      // 0 .. 3: codes, 4, 5: rotary numbers, 6: exponents
+    if (n < 4)
+      r.codes[n] = *reinterpret_cast<const u32x4*>(p.cache + slot * 256 + 16 * q4 + 64 * n);
+    else if (n < 6)
+      r.rope[n - 4] = *reinterpret_cast<const bf16x8*>(p.rope + slot * 128 + 16 * q4 + 64 * (n - 4));
+    else
+      r.exps = *reinterpret_cast<const u32x4*>(p.scales + slot * 16);
+  };
+  Raw raw[kAhead];
+  fetch_entry();
 #pragma unroll
-  for (int i = 0; i < kBufs - 1; ++i) {
-    attn_wait<0>();
-    if (nxt.left > 0) {
-      const Loader ld = start_next(i);
+  for (int i = 0; i < kAhead; ++i) {
+    next_slot();
 #pragma unroll
-      for (int n = 0; n < kLoads; ++n) ld.issue(n);
-    }
+    for (int n = 0; n < 7; ++n) load_part(raw[i], n);
   }
 
-  // LDS offsets of this lane
-  const int key0 = row32 * 256 + ((half ^ (row32 & 15)) << 4);
-  const int rope0 = kCodeBytes + row32 * 128 + ((half ^ ((row32 >> 1) & 7)) << 4);
-  const int scale0 = kCodeBytes + kRopeBytes + row32 * 16;
-  const int val0 = 4 * half * 256 + (((row32 >> 1) ^ (4 * half)) << 4) + 8 * (row32 & 1);
-  const int vscale0 = kCodeBytes + kRopeBytes + 4 * half * 16 + (row32 >> 1);
+  // LDS offsets of this lane in a tile: where it writes its token's numbers
+  // (16-byte chunk 4 * q4 + s of each 256 bytes, permuted by the token), and
+  // where it reads its columns transposed
+  const int put0 = (kWaveTokens * wave + tok16) * kRowBytes + (((4 * q4) ^ swz(tok16)) << 4);
+  const int val0 = L.trow * kRowBytes + 256 * wave + L.tbyte + ((L.tchunk ^ swz(L.trow)) << 4);
+  const int weight0 = kWeightsAt + 1024 * wave + (tok16 + 32 * (q4 & 1)) * 16 + 8 * (q4 >> 1);
 
-  const int row = (wg - g * p.row_blocks) * 32 + row32;
-  const int late = p.tokens - 1 - min(row, p.rows - 1) / p.heads;        // newest tokens hidden from it
+  const int row0 = (wg - g * p.row_blocks) * 32;
+  const int row = row0 + L.row;      // of the lane's outputs
+  int late[2];                       // newest tokens hidden from the rows of its scores
+#pragma unroll
+  for (int h = 0; h < 2; ++h) late[h] = p.tokens - 1 - min(row0 + 16 * h + tok16, p.rows - 1) / p.heads;
 
-  bf16x8 qf[36];
-  f32x16 acc[16];
-  float m, l;
+  bf16x8 qf[2][18];
+  f32x16 acc[4];
+  float m[2], mo, l[2];      // reference of the rows of the lane's scores, of its outputs; sums of its weights
   bool first = true;
-  int buf = 0;
+  int at = 0;                // offset of the tile whose values come next
 
-  while (cur.left > 0) {      // a request's part of the range
-    const bool whole = cur.tile == 0 && cur.left >= cur.tiles;
-    const uint16_t* qr = p.q + min((int64_t)cur.b * p.rows + min(row, p.rows - 1), p.all_rows - 1) * kKey;
+  auto start_piece = [&] {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) qf[i] = *reinterpret_cast<const bf16x8*>(qr + 64 * (i >> 2) + 32 * half + 8 * (i & 3));
+    for (int h = 0; h < 2; ++h) {
+      const uint16_t* qr =
+          p.q + min((int64_t)cur.b * p.rows + min(row0 + 16 * h + tok16, p.rows - 1), p.all_rows - 1) * kKey;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) qf[32 + i] = *reinterpret_cast<const bf16x8*>(qr + kLatent + 16 * i + 8 * half);
-    m = neg_inf();
-    l = 0.f;
+      for (int i = 0; i < 16; ++i)
+        qf[h][i] = *reinterpret_cast<const bf16x8*>(qr + 128 * (i >> 2) + 32 * q4 + 8 * (i & 3));
 #pragma unroll
-    for (int j = 0; j < 16; ++j) acc[j] = zero16();
-    operands_loaded();
-
-    for (bool last = false; !last;) {
-      if (cur.left > 1)      // the next tile's loads may stay in flight
-        attn_wait<kLoads>();
-      else
-        attn_wait<0>();
-      const char* tl = mine + buf * kBufBytes;
-      const int tok0 = cur.tile * kTile + kWaveTokens * wave;
-      if (nxt.left > 0) {
-        const Loader ld = start_next(buf == 0 ? kBufs - 1 : buf - 1);
-#pragma unroll
-        for (int n = 0; n < kLoads; ++n) ld.issue(n);
-      }
-      if (tok0 < cur.len) {
-        const uint4 sw = *reinterpret_cast<const uint4*>(tl + scale0);
-        const uint32_t sc[4] = {sw.x >> (8 * half), sw.y >> (8 * half), sw.z >> (8 * half), sw.w >> (8 * half)};
-        f32x16 s = zero16();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s = mfma32(lds_bf16x8(tl + (rope0 ^ (i << 5))), qf[32 + i], s);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const uint4 c = *reinterpret_cast<const uint4*>(tl + (key0 ^ (q << 5)));
-          const float f = pow2_byte(sc[q >> 1], 16 * (q & 1));
-          s = mfma32(cvt8(c.x, f), qf[4 * q], s);
-          s = mfma32(cvt8(c.y, f), qf[4 * q + 1], s);
-          s = mfma32(cvt8(c.z, f), qf[4 * q + 2], s);
-          s = mfma32(cvt8(c.w, f), qf[4 * q + 3], s);
-        }
-        if (tok0 + kWaveTokens > cur.len - (p.tokens - 1)) {
-          const int seen = cur.len - late - tok0;
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (drow(i, half) >= seen) s[i] = neg_inf();
-        }
-        float top = s[0];
-#pragma unroll
-        for (int i = 1; i < 16; ++i) top = max_nan(top, s[i]);
-        top = half_max(top) * p.scale_log2;
-        if (__any(top > m + kSlack)) {
-          const float mn = max_nan(m, top), alpha = mn == neg_inf() ? 1.f : exp2_fast(m - mn);
-          m = mn;
-          l *= alpha;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) acc[j] *= alpha;
-        }
-        const float ref = m == neg_inf() ? 0.f : m;      // nothing visible yet: every weight is 0
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          s[i] = exp2_fast(fmaf(s[i], p.scale_log2, -ref));
-          l += s[i];
-        }
-#pragma unroll
-        for (int a = 0; a < 2; ++a) {      // 16 tokens
-          const bf16x8 pb = pack8(s, a);
-          uint2 c[8];
-          float f[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int r = 8 * (e >> 2) + (e & 3);
-            c[e] = *reinterpret_cast<const uint2*>(tl + (val0 ^ (r << 4)) + (16 * a + r) * 256);
-            f[e] = __uint_as_float((uint32_t)*reinterpret_cast<const uint8_t*>(tl + vscale0 + (16 * a + r) * 16) << 23);
-          }
-          auto pair_of = [&](auto sel, bool upper) {
-            constexpr int SEL = decltype(sel)::value;
-            uint32_t lo[4], hi[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t x = cvt2<SEL>(upper ? c[2 * k].y : c[2 * k].x, f[2 * k]);
-              const uint32_t y = cvt2<SEL>(upper ? c[2 * k + 1].y : c[2 * k + 1].x, f[2 * k + 1]);
-              lo[k] = __builtin_amdgcn_perm(y, x, 0x05040100u);
-              hi[k] = __builtin_amdgcn_perm(y, x, 0x07060302u);
-            }
-            typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-            const int j = 2 * SEL + (upper ? 8 : 0);
-            acc[j] = mfma32(__builtin_bit_cast(bf16x8, u32x4{lo[0], lo[1], lo[2], lo[3]}), pb, acc[j]);
-            acc[j + 1] = mfma32(__builtin_bit_cast(bf16x8, u32x4{hi[0], hi[1], hi[2], hi[3]}), pb, acc[j + 1]);
-          };
-          pair_of(std::integral_constant<int, 0>{}, false);
-          pair_of(std::integral_constant<int, 1>{}, false);
-          pair_of(std::integral_constant<int, 2>{}, false);
-          pair_of(std::integral_constant<int, 3>{}, false);
-          pair_of(std::integral_constant<int, 0>{}, true);
-          pair_of(std::integral_constant<int, 1>{}, true);
-          pair_of(std::integral_constant<int, 2>{}, true);
-          pair_of(std::integral_constant<int, 3>{}, true);
-        }
-      }
-      last = cur.tile + 1 == cur.tiles || cur.left == 1;
-      if (!last) {
-        advance<kTile>(p, cur);
-        buf = buf + 1 == kBufs ? 0 : buf + 1;
-      }
+      for (int i = 0; i < 2; ++i) qf[h][16 + i] = *reinterpret_cast<const bf16x8*>(qr + kLatent + 32 * i + 8 * q4);
+      m[h] = neg_inf();
+      l[h] = 0.f;
     }
+    // (no instruction: the queries stay in the accumulation registers, which the products read as well)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 18; ++i) {
+        u32x4 v = __builtin_bit_cast(u32x4, qf[h][i]);
+        asm("" : "+a"(v));
+        qf[h][i] = __builtin_bit_cast(bf16x8, v);
+      }
+    mo = neg_inf();
+#pragma unroll
+    for (int d = 0; d < 4; ++d) acc[d] = zero16();
+  };
 
-    // the waves' sums, against the largest of their references
-    l = half_sum(l);
-    if (half == 0) stats[wave][row32] = make_float2(m, l);
-    attn_barrier();
-    float mm = neg_inf();
+  // What a tile goes through. Scores: those of the wave's 16 tokens, whose
+  // numbers go to the tile's place `to`; as the registers of r are done with,
+  // the loads of the tile three further on follow into them, one at a time (a
+  // wave that issues its loads in one go stands still until the address unit
+  // has taken them all). Weights against the reference. Values: of the tile at
+  // `from`, the one before, 16 products of which half go beside the scores and
+  // half beside the weights.
+  f32x4 s[2];
+  float top[2], sum[2];
+  auto weigh = [&](int to) {
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) mm = max_nan(mm, stats[w][row32].x);
-    const float ref = mm == neg_inf() ? 0.f : mm, part = exp2_fast(m - ref);
-    // a thread sums 4 columns of a row: lane `from` of every wave has that row
-    const int from = threadIdx.x >> 2, c4 = threadIdx.x & 3, orow = (wg - g * p.row_blocks) * 32 + (from & 31);
-    float om = neg_inf(), ol = 0.f;
+    for (int h = 0; h < 2; ++h) {
+      const float ref = m[h] == neg_inf() ? 0.f : m[h];      // nothing visible yet: every weight is 0
+      f32x4 e;
+      bf16x4 b;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) om = max_nan(om, stats[w][from & 31].x);
+      for (int j = 0; j < 4; ++j) {
+        e[j] = exp2_fast(fmaf(s[h][j], p.scale_log2, -ref));
+        b[j] = (__bf16)e[j];
+      }
+      sum[h] = (e[0] + e[1]) + (e[2] + e[3]);
+      *reinterpret_cast<bf16x4*>(tiles + to + weight0 + 256 * h) = b;
+    }
+  };
+  auto tile_work = [&](auto with_scores, auto with_values, Raw& r, const Cursor& c, int to, int from) {
+    constexpr bool S = decltype(with_scores)::value, V = decltype(with_values)::value;
+    const int put = opaque(put0 + to), val = opaque(val0 + from);
+    bf16x8 pb[4];
+    constexpr int kFetch = 4;      // operands of the values under way
+    bf16x8 v[kFetch];
+    auto fetch = [&](int i) {
+      const int t = 16 * (i >> 2), d = i & 3;
+      v[i % kFetch] = join(lds_tr16(tiles + (val ^ (d << 6)) + t * kRowBytes),
+                           lds_tr16(tiles + (val ^ (d << 6) ^ 128) + (t + 8) * kRowBytes));
+    };
+    auto value = [&](auto index) {
+      constexpr int I = decltype(index)::value;
+      acc[I & 3] = mfma32(v[I % kFetch], pb[I >> 2], acc[I & 3]);
+      if constexpr (I + kFetch < 16) fetch(I + kFetch);
+    };
+    if constexpr (V) {
+      const char* w = tiles + opaque(from + kWeightsAt + 16 * lane);
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w)
-      ol = fmaf(stats[w][from & 31].y, exp2_fast(stats[w][from & 31].x - (om == neg_inf() ? 0.f : om)), ol);
-    const bool stored = orow < p.rows && (int64_t)cur.b * p.rows + orow < p.all_rows;
-    const bool final_result = whole && !p.join;
-    const int64_t o = final_result ? (int64_t)cur.b * p.rows + orow
-                                   : (whole ? 2 * (int64_t)p.groups + cur.b : 2 * (int64_t)g + (first ? 0 : 1)) * p.rows + orow;
-    const float inv = inverse_of(ol);
-    char* const slab = mine + buf * kBufBytes;
+      for (int a = 0; a < 4; ++a) pb[a] = lds_bf16x8(w + 1024 * a);
 #pragma unroll
-    for (int i0 = 0; i0 < 16; i0 += kJoinRegs) {
+      for (int i = 0; i < kFetch; ++i) fetch(i);
+    }
+    float f[4];
+    auto score = [&](auto index) {      // 32 of the key's columns
+      constexpr int I = decltype(index)::value, P = I >> 2, C = I & 3;
+      const u32x4 k = cvt8(r.codes[P][C], f[P]);
+      *reinterpret_cast<u32x4*>(tiles + (put ^ (C << 4)) + 256 * P) = k;
 #pragma unroll
-      for (int i = 0; i < kJoinRegs; ++i)
+      for (int h = 0; h < 2; ++h) s[h] = mfma16(__builtin_bit_cast(bf16x8, k), qf[h][I], s[h]);
+    };
+    if constexpr (S) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          f32x4 v;
+      for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(((r.exps[i] >> (8 * q4)) & 0xFFu) << 23);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = acc[4 * c + j][i0 + i] * part;
-          *reinterpret_cast<f32x4*>(slab + 4096 * i + 64 * lane + ((c ^ ((lane >> 2) & 3)) << 4)) = v;
+      for (int h = 0; h < 2; ++h) s[h] = f32x4{0.f, 0.f, 0.f, 0.f};
+      next_slot();
+    }
+    auto group = [&](auto index) {
+      constexpr int I = decltype(index)::value;
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (V) value(index);
+      if constexpr (S) {
+        score(std::integral_constant<int, 2 * I>{});
+        score(std::integral_constant<int, 2 * I + 1>{});
+        if constexpr (I < 2) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) s[h] = mfma16(r.rope[I], qf[h][16 + I], s[h]);
         }
+        if constexpr (I == 0) load_part(r, 6);
+        if constexpr (I == 2 || I == 4) load_part(r, 4 + (I >> 2));
+        if constexpr (I & 1) load_part(r, I >> 1);
+      }
+    };
+    [&]<int... I>(std::integer_sequence<int, I...>) { (group(std::integral_constant<int, I>{}), ...); }
+    (std::make_integer_sequence<int, 8>{});
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (S) {
+      if ((c.tile + 1) * kTile > c.len - (p.tokens - 1)) {
+        const int tok0 = c.tile * kTile + kWaveTokens * wave + 4 * q4;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (tok0 + j >= c.len - late[h]) s[h][j] = neg_inf();
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        top[h] = half_max(quarter_max(max_nan(max_nan(s[h][0], s[h][1]), max_nan(s[h][2], s[h][3])))) * p.scale_log2;
+      weigh(to);
+      float* const stat = reinterpret_cast<float*>(tiles + to + kStatAt);
+      if (q4 < 2) stat[64 * wave + lane] = q4 ? top[1] : top[0];
+      if (lane == 0) stat[64 * wave + 32] = 0.f;
+      if (top[0] > m[0] + kSlack || top[1] > m[1] + kSlack) stat[64 * wave + 32] = 1.f;
+    }
+    if constexpr (V) {
+      [&]<int... I>(std::integer_sequence<int, I...>) { (value(std::integral_constant<int, I + 8>{}), ...); }
+      (std::make_integer_sequence<int, 8>{});
+    }
+  };
+
+  // The waves meet at a tile's weights. If one wishes the reference raised, all do (the answer is the same for all).
+  auto meet = [&](int to) {
+    const float* const stat = reinterpret_cast<const float*>(tiles + to + kStatAt);
+    attn_barrier();
+    if (__any(stat[64 * (lane & 3) + 32] != 0.f)) {
+      float n[2] = {m[0], m[1]}, no = mo;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        n[0] = max_nan(n[0], stat[64 * w + tok16]);
+        n[1] = max_nan(n[1], stat[64 * w + 16 + tok16]);
+        no = max_nan(no, stat[64 * w + L.row]);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        l[h] *= n[h] == neg_inf() ? 1.f : exp2_fast(m[h] - n[h]);
+        m[h] = n[h];
+      }
+      const float alpha = no == neg_inf() ? 1.f : exp2_fast(mo - no);
+      mo = no;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) acc[d] *= alpha;
+      weigh(to);
       attn_barrier();
+    }
 #pragma unroll
-      for (int i = 0; i < kJoinRegs; ++i) {
-        f32x4 v{0.f, 0.f, 0.f, 0.f};
+    for (int h = 0; h < 2; ++h) l[h] += sum[h];
+  };
+
+  auto finish_piece = [&](bool whole) {
+    float* const stat = reinterpret_cast<float*>(tiles + at + kStatAt);
+    attn_barrier();      // everyone has read the maxima there
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w)
-          v += *reinterpret_cast<const f32x4*>(tiles + (w * kBufs + buf) * kBufBytes + 4096 * i + 64 * from +
-                                               ((c4 ^ ((from >> 2) & 3)) << 4));
-        const int col = 16 * drow(i0 + i, from >> 5) + 4 * c4;
-        if (stored) {
-          if (final_result) {
+    for (int h = 0; h < 2; ++h) l[h] = half_sum(quarter_sum(l[h]));
+    if (q4 < 2) stat[64 * wave + lane] = q4 ? l[1] : l[0];
+    attn_barrier();
+    float total = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) total += stat[64 * w + L.row];
+    if (row < p.rows && (int64_t)cur.b * p.rows + row < p.all_rows) {
+      if (whole && !p.join) {
+        const int64_t o = (int64_t)cur.b * p.rows + row;
+        const float inv = inverse_of(total);
+        uint16_t* op = p.out + o * kLatent + 128 * wave + 4 * L.half;
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
             bf16x4 b;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) b[j] = (__bf16)(v[j] * inv);
-            *reinterpret_cast<bf16x4*>(p.out + o * kLatent + col) = b;
-          } else {
-            *reinterpret_cast<f32x4*>(p.part + o * kLatent + col) = v;
+            for (int j = 0; j < 4; ++j) b[j] = (__bf16)(acc[d][4 * i + j] * inv);
+            *reinterpret_cast<bf16x4*>(op + 32 * d + 8 * i) = b;
           }
-        }
+        if (wave == 0 && L.half == 0) p.lse[o] = lse_of(mo, total);
+      } else {
+        const int64_t o = (whole ? 2 * (int64_t)p.groups + cur.b : 2 * (int64_t)g + (first ? 0 : 1)) * p.rows + row;
+        float* op = p.part + o * kLatent + 128 * wave + 4 * L.half;
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            f32x4 v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = acc[d][4 * i + j];
+            *reinterpret_cast<f32x4*>(op + 32 * d + 8 * i) = v;
+          }
+        if (wave == 0 && L.half == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * o) = make_float2(mo, total);
       }
-      attn_barrier();
     }
-    if (stored && from < 32 && c4 == 0) {
-      if (final_result)
-        p.lse[o] = lse_of(om, ol);
-      else
-        *reinterpret_cast<float2*>(p.part_ml + 2 * o) = make_float2(om, ol);
+  };
+
+  // The range, tile by tile: `r` holds the tile whose scores come next. After
+  // the last one of a request's part its values are added alone.
+  constexpr std::true_type yes{};
+  constexpr std::false_type no{};
+  bool whole = cur.tile == 0 && cur.left >= cur.tiles, fresh = true;
+  auto step = [&](Raw& r) {      // returns whether a tile follows
+    // (the other place also where nothing is in this one: someone may still read the sums of the last request there)
+    if (fresh) {
+      start_piece();
+      tile_work(yes, no, r, cur, at ^ kTileBytes, 0);
+      fresh = false;
+    } else {
+      tile_work(yes, yes, r, cur, at ^ kTileBytes, at);
     }
-    first = false;
-    advance<kTile>(p, cur);
-    buf = buf + 1 == kBufs ? 0 : buf + 1;
+    at ^= kTileBytes;
+    meet(at);
+    const bool last = cur.tile + 1 == cur.tiles || cur.left == 1;
+    if (last) {
+      tile_work(no, yes, r, cur, 0, at);
+      finish_piece(whole);
+      first = false;
+      fresh = true;
+    }
+    next_tile(p, cur);
+    if (last) whole = cur.left >= cur.tiles;
+    return cur.left > 0;
+  };
+  while (step(raw[0]) && step(raw[1]) && step(raw[2])) {
   }
 }
 

@@ -30,7 +30,7 @@ struct MlaCache {
 hipError_t launch_mla_cache_write(const MlaCache& c, hipStream_t stream);
 hipError_t launch_mla_cache_read(const MlaCache& c, hipStream_t stream);
 
-constexpr int kFp4Tile = 128;           // tokens of a workgroup's tile, 32 a wave
+constexpr int kFp4Tile = 64;            // tokens of a tile
 constexpr int kFp4BlockRows = 32;
 hipError_t launch_mla_decode_fp4(const MlaDecode& own, const MlaDecode* prefix, hipStream_t stream);
 

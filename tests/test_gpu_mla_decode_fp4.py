@@ -86,12 +86,12 @@ def _check(dev, page, lens, T, H, seed=0, qstd=0.5):
 
 
 def _groups(B, T, H, width, page):
-    """Workgroup ranges that the tiles of 128 tokens are shared by, from the workspace."""
+    """Workgroup ranges that the tiles of 64 tokens are shared by, from the workspace."""
     return fb.serve_lib().fp8bs_mla_decode_fp4_workspace_bytes(B, T, H, width, page, 0) // (2 * T * H * 514 * 4)
 
 
 def _tiles(lens):
-    return sum(-(-n // 128) for n in lens)
+    return sum(-(-n // 64) for n in lens)
 
 
 @pytest.mark.parametrize("lens", [[1], [2], [31], [32], [33], [127], [128], [129], [257], [1000]], ids=str)
