@@ -28,7 +28,7 @@ _SIGNATURES = {
                                     _vp, _vp, _vp],
     "fp8bs_mla_decode_fp4_workspace_bytes": [_i, _i, _i, _i64, _i, _i64],
     "fp8bs_moe_tokens": [_vp, _i, _i64, _vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i64, _vp, _vp, _vp],
-    "fp8bs_moe_tokens_workspace_bytes": [_i, _i, _i64],
+    "fp8bs_moe_tokens_workspace_bytes": [_i, _i, _i64, _i64],
     "fp8bs_logprobs": [_vp, _i, _i64, _vp, _i64, _i64, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
     "fp8bs_logprobs_workspace_bytes": [_i64, _i64, _i],
     "fp8bs_logprobs_bwd": [_vp, _i, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp],
@@ -184,7 +184,7 @@ def fp8bs_moe_tokens(x, topk_ids, weights, w_up, s_up, w_down, s_down):
             _ptr(s_up, "s_up", _f32, (E, F // 64, K // 128), device), _ptr(w_down, "w_down", _u8, (E, K, F), device),
             _ptr(s_down, "s_down", _f32, (E, K // 128, F // 128), device), E, F)
     out = torch.empty((T, K), dtype=_bf16, device=device)
-    ws = _workspace(_bytes("fp8bs_moe_tokens_workspace_bytes", T, topk, F), device)
+    ws = _workspace(_bytes("fp8bs_moe_tokens_workspace_bytes", T, topk, K, F), device)
     _call("fp8bs_moe_tokens", device, *args, out.data_ptr(), ws.data_ptr())
     return out
 

@@ -4,18 +4,22 @@
 //   up    h = bf16(silu(G_e x) * (U_e x)) for every (expert, token) that meet
 //   down  out_t = bf16(sum over t's experts of w * D_e h)
 //
-// For a few tokens the layer is the reading of its weights, so every wave
-// streams 16-row strips of them straight into registers, in the order in which
-// the matrix unit wants them (a lane: 32 consecutive bytes of a row's 128, the
-// inner index numbered to match), turns the codes into BF16 (exact) and
-// multiplies them with the tokens' numbers, which come from L2. A 128-wide
-// partial sum is scaled by its block's scale as it is added (FP32).
+// For a few tokens the layer is the reading of its weights. A wave streams 32
+// rows of them, 128 codes (a scale's reach) at a time and several such pieces
+// ahead in registers, every load eight whole 128-byte rows: in the order that
+// the matrix unit wants, 16 rows side by side, every lane of a load is a cache
+// line of its own and the address unit takes three times as long. The lanes
+// trade through 4 KB of LDS that only the wave uses, turn the codes into BF16
+// (exact) and multiply them with the tokens' numbers, which come from L2. A
+// 128-wide partial sum is scaled by its block's scale as it is added (FP32).
 //
 // up: a workgroup is 16 columns of h of one expert (16 rows of G and of U), its
 // waves share the inner dimension and add their sums through LDS. down: a
-// workgroup is 16 columns of the output for all experts and tokens, so the sum
-// over a token's experts needs no second pass and no atomics; its waves share
-// the list of (expert, 128-wide chunk). Sums run in a fixed order.
+// workgroup is 32 columns of the output for all tokens and a share of the
+// (expert, 128 wide piece) pairs, which its waves share in turn; a token that
+// an expert was not chosen by adds nothing. The last workgroup of the same
+// columns to be done adds the shares' sums, in order: which one that is depends
+// on chance, the result does not.
 //
 // Which experts are chosen is found by every workgroup from the ids (at most
 // 4096 of them): a bitmap in LDS, and a lane per token that looks for the
@@ -28,48 +32,56 @@ namespace fp8bs {
 
 namespace {
 
-constexpr int kChunkK = 128;      // inner numbers that share a scale
-constexpr int kStrip = 16;        // rows of weights
-constexpr int kTiles = kMoeMaxTokens / 16;
-constexpr int kUpWaves = 4, kDownWaves = 8;
+constexpr int kPiece = 128;       // inner numbers that share a scale
+constexpr int kMaxTiles = kMoeMaxTokens / 16;
+constexpr int kUpWaves = 4, kDownWaves = 8, kJoinThreads = 256;
+constexpr int kDeep = 4;          // pieces of weights under way
+constexpr int kStripBytes = 32 * kPiece;
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 __device__ __forceinline__ f32x4 zero4() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
 
-// The ids of all slots and a bit per chosen expert.
-struct Routing {
-  int32_t ids[kMoeMaxTokens * kMoeMaxTopk];
-  uint32_t bits[kMoeMaxExperts / 32];
-};
-
-template <int THREADS>
-__device__ __forceinline__ void load_routing(const MoeTokens& m, Routing& r) {
-  if (threadIdx.x < kMoeMaxExperts / 32) r.bits[threadIdx.x] = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < m.T * m.topk; i += THREADS) {
-    const int e = m.ids[i];
-    r.ids[i] = e;
-    if (e >= 0 && e < m.E) atomicOr(&r.bits[e >> 5], 1u << (e & 31));
-  }
-  __syncthreads();
+// Bytes of the routing, a multiple of 16.
+__host__ __device__ __forceinline__ int routing_bytes_of(const MoeTokens& m) {
+  return (kMoeMaxExperts / 32 + m.T * m.topk + 3) / 4 * 16;
 }
 
+// The ids of all slots and a bit per chosen expert, in LDS.
+struct Routing {
+  uint32_t* bits;
+  int32_t* ids;
+  __device__ __forceinline__ Routing(const MoeTokens& m, char* lds, int threads)
+      : bits(reinterpret_cast<uint32_t*>(lds)), ids(reinterpret_cast<int32_t*>(lds) + kMoeMaxExperts / 32) {
+    if (threadIdx.x < kMoeMaxExperts / 32) bits[threadIdx.x] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < m.T * m.topk; i += threads) {
+      const int e = m.ids[i];
+      ids[i] = e;
+      if (e >= 0 && e < m.E) atomicOr(&bits[e >> 5], 1u << (e & 31));
+    }
+    __syncthreads();
+  }
+};
 // Lane l of the first 32: the chosen experts of word l (`word`), how many come
 // before it; returns how many there are. Every lane of the wave takes part.
 __device__ __forceinline__ int count_chosen(const Routing& r, uint32_t& word, int& before) {
   const int lane = threadIdx.x & 63;
   word = lane < kMoeMaxExperts / 32 ? r.bits[lane] : 0;
   const int own = __popc(word);
+  // inclusive sums of each row of 16 lanes, then the first row's total to the second
   int v = own;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int x = __shfl_up(v, d, 64);
-    if (lane >= d) v += x;
-  }
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);      // from the lane 1, 2, 4, 8 below
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  const int row0 = __builtin_amdgcn_readlane(v, 15);
+  if (lane >= 16) v += row0;
   before = v - own;
-  return __builtin_amdgcn_readlane(v, 63);
+  return __builtin_amdgcn_readlane(v, 31);
 }
 
 __device__ __forceinline__ int nth_bit(uint32_t word, int n) {
@@ -96,34 +108,80 @@ __device__ __forceinline__ Member member_of(const MoeTokens& m, const Routing& r
   return x;
 }
 
-// 32 codes of a row (the lane's share of a chunk) and their four operands.
-struct Codes {
-  uint4 a, b;
-  __device__ __forceinline__ void load(const uint8_t* p) {
-    a = *reinterpret_cast<const uint4*>(p);
-    b = *reinterpret_cast<const uint4*>(p + 16);
+// A piece of 32 rows as it is loaded: load i has rows 8i .. 8i+7, eight lanes a row.
+struct Piece {
+  u32x4 w[4];
+};
+// The wave's 4 KB of LDS; the 16-byte chunks of a row are permuted by the row,
+// so that 8 rows at one chunk touch every bank once.
+struct Trade {
+  char* put;      // of this lane: row lane / 8, chunk lane % 8
+  const char* get;
+  int c0;         // of row lane % 16: chunks 2q and 2q + 1, q = lane / 16
+  __device__ __forceinline__ explicit Trade(char* lds) {
+    const int lane = threadIdx.x & 63;
+    put = lds + (lane >> 3) * kPiece + (((lane & 7) ^ (lane >> 3)) << 4);
+    get = lds + (lane & 15) * kPiece;
+    c0 = ((2 * (lane >> 4)) ^ (lane & 7)) << 4;
   }
-  __device__ __forceinline__ bf16x8 operand(int s) const {
-    return s == 0 ? e4m3_to_bf16(a.x, a.y) : s == 1 ? e4m3_to_bf16(a.z, a.w) : s == 2 ? e4m3_to_bf16(b.x, b.y) : e4m3_to_bf16(b.z, b.w);
+  __device__ __forceinline__ void write(const Piece& p) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x4*>(put + 1024 * i) = p.w[i];
+  }
+  // The lane's 32 codes of row 16 * a + lane % 16: the inner numbers 32q + 8s .. of operand s.
+  __device__ __forceinline__ void read(int a, bf16x8 (&o)[4]) const {
+    const u32x4 x = *reinterpret_cast<const u32x4*>(get + 2048 * a + c0), y = *reinterpret_cast<const u32x4*>(get + 2048 * a + (c0 ^ 16));
+    o[0] = e4m3_to_bf16(x[0], x[1]);
+    o[1] = e4m3_to_bf16(x[2], x[3]);
+    o[2] = e4m3_to_bf16(y[0], y[1]);
+    o[3] = e4m3_to_bf16(y[2], y[3]);
   }
 };
 
+// A tile of 16 tokens' numbers of one piece: lane l has token l % 16.
+struct Numbers {
+  bf16x8 b[4];
+  __device__ __forceinline__ void load(const uint16_t* p) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) b[s] = *reinterpret_cast<const bf16x8*>(p + 8 * s);
+  }
+};
+
+template <int TILES>
 __global__ __launch_bounds__(64 * kUpWaves) void moe_up_kernel(const MoeTokens m) {
-  __shared__ Routing routing;
+  extern __shared__ __align__(16) char lds[];      // routing; the waves' strips, then their sums
   __shared__ int tok[kMoeMaxTokens], slot_of[kMoeMaxTokens];
-  __shared__ __align__(16) float sums[kUpWaves][kTiles][2][64][4];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int strips = m.F / kStrip;
+  const int strips = m.F / 16;
   const int rank = blockIdx.x / strips, strip = blockIdx.x - rank * strips;
 
-  load_routing<64 * kUpWaves>(m, routing);
+  const Routing routing(m, lds, 64 * kUpWaves);
+  char* const area = lds + routing_bytes_of(m);
   uint32_t word;
   int before;
   if (rank >= count_chosen(routing, word, before)) return;
   const uint64_t hit = __ballot(rank >= before && rank < before + __popc(word));
   const int hl = __ffsll((unsigned long long)hit) - 1;
   const int e = __builtin_amdgcn_readfirstlane(32 * hl + nth_bit(__shfl(word, hl, 64), rank - __shfl(before, hl, 64)));
+
+  const int pieces = m.K / kPiece;
+  const int n = (pieces - wave + kUpWaves - 1) / kUpWaves;      // this wave's: wave, wave + 4, ..
+  const uint8_t* gate = m.w_up + ((int64_t)e * 2 * m.F + strip * 16 + (lane >> 3)) * m.K + 16 * (lane & 7);
+  const uint8_t* up = gate + (int64_t)m.F * m.K;
+  // (past the wave's last piece that one again: loads under a condition would make the waits for earlier ones wait for these too)
+  auto piece_at = [&](int i) { return wave + kUpWaves * max(0, min(i, n - 1)); };
+  auto load = [&](Piece& p, int i) {
+    const int64_t at = min(piece_at(i), pieces - 1) * kPiece;
+    p.w[0] = *reinterpret_cast<const u32x4*>(gate + at);
+    p.w[1] = *reinterpret_cast<const u32x4*>(gate + at + 8 * (int64_t)m.K);
+    p.w[2] = *reinterpret_cast<const u32x4*>(up + at);
+    p.w[3] = *reinterpret_cast<const u32x4*>(up + at + 8 * (int64_t)m.K);
+  };
+  Piece ring[kDeep];
+#pragma unroll
+  for (int i = 0; i < kDeep; ++i) load(ring[i], i);
+
   const Member mine = member_of<false>(m, routing, e);
   const uint64_t members = __ballot(mine.slot >= 0);
   const int count = (int)__popcll(members);
@@ -134,46 +192,66 @@ __global__ __launch_bounds__(64 * kUpWaves) void moe_up_kernel(const MoeTokens m
   }
   __syncthreads();
 
-  const int tiles = (count + 15) / 16, chunks = m.K / kChunkK;
-  const int inner = 32 * (lane >> 4);
-  const uint16_t* x[kTiles];
+  const int tiles = (count + 15) / 16;
+  const uint16_t* x[TILES];
 #pragma unroll
-  for (int i = 0; i < kTiles; ++i) x[i] = m.x + (int64_t)tok[min(16 * i + (lane & 15), count - 1)] * m.K + inner;
-  const int row = strip * kStrip + (lane & 15);
-  const uint8_t* gate = m.w_up + ((int64_t)e * 2 * m.F + row) * m.K + inner;
-  const uint8_t* up = gate + (int64_t)m.F * m.K;
-  const float* sg = m.s_up + ((int64_t)e * 2 * m.F / kChunkK + strip * kStrip / kChunkK) * chunks;
-  const float* su = sg + (int64_t)(m.F / kChunkK) * chunks;
+  for (int i = 0; i < TILES; ++i) x[i] = m.x + (int64_t)tok[min(16 * i + (lane & 15), count - 1)] * m.K + 32 * (lane >> 4);
+  const float* sg = m.s_up + ((int64_t)e * 2 * m.F / kPiece + strip * 16 / kPiece) * pieces;
+  const float* su = sg + (int64_t)(m.F / kPiece) * pieces;
+  const Trade trade(area + kStripBytes * wave);
+  Numbers b[2][TILES];
+  auto load_x = [&](Numbers (&to)[TILES], int i) {
+    const int at = min(piece_at(i), pieces - 1) * kPiece;
+#pragma unroll
+    for (int j = 0; j < TILES; ++j)
+      if (j == 0 || j < tiles) to[j].load(x[j] + at);
+  };
+  load_x(b[0], 0);
 
-  f32x4 ag[kTiles], au[kTiles];
+  f32x4 ag[TILES], au[TILES];
 #pragma unroll
-  for (int i = 0; i < kTiles; ++i) ag[i] = au[i] = zero4();
-#pragma unroll 2
-  for (int c = wave; c < chunks; c += kUpWaves) {
-    Codes g, u;
-    g.load(gate + c * kChunkK);
-    u.load(up + c * kChunkK);
+  for (int i = 0; i < TILES; ++i) ag[i] = au[i] = zero4();
+  auto step = [&](int i, Piece& p, const Numbers (&now)[TILES], Numbers (&next)[TILES]) {
+    const int c = min(piece_at(i), pieces - 1);
     const float fg = sg[c], fu = su[c];
+    trade.write(p);
+    load(p, i + kDeep);
+    load_x(next, i + 1);
+    bf16x8 g[4], u[4];
+    trade.read(0, g);
+    trade.read(1, u);
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-      if (i < tiles) {
+    for (int j = 0; j < TILES; ++j) {
+      if (j == 0 || j < tiles) {
         f32x4 pg = zero4(), pu = zero4();
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-          const bf16x8 b = *reinterpret_cast<const bf16x8*>(x[i] + c * kChunkK + 8 * s);
-          pg = mfma16(g.operand(s), b, pg);
-          pu = mfma16(u.operand(s), b, pu);
+          pg = mfma16(g[s], now[j].b[s], pg);
+          pu = mfma16(u[s], now[j].b[s], pu);
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          ag[i][j] = fmaf(fg, pg[j], ag[i][j]);
-          au[i][j] = fmaf(fu, pu[j], au[i][j]);
+        for (int k = 0; k < 4; ++k) {
+          ag[j][k] = fmaf(fg, pg[k], ag[j][k]);
+          au[j][k] = fmaf(fu, pu[k], au[j][k]);
         }
       }
     }
+  };
+  static_assert(kDeep == 4, "the ring is unrolled");
+  for (int i = 0; i < n; i += kDeep) {
+    step(i, ring[0], b[0], b[1]);
+    if (i + 1 >= n) break;
+    step(i + 1, ring[1], b[1], b[0]);
+    if (i + 2 >= n) break;
+    step(i + 2, ring[2], b[0], b[1]);
+    if (i + 3 >= n) break;
+    step(i + 3, ring[3], b[1], b[0]);
   }
+  typedef float Sums[TILES][2][64][4];
+  Sums* const sums = reinterpret_cast<Sums*>(area);
+  __syncthreads();      // the strips are done with
 #pragma unroll
-  for (int i = 0; i < kTiles; ++i)
+  for (int i = 0; i < TILES; ++i)
     if (i < tiles) {
       *reinterpret_cast<f32x4*>(sums[wave][i][0][lane]) = ag[i];
       *reinterpret_cast<f32x4*>(sums[wave][i][1][lane]) = au[i];
@@ -191,19 +269,20 @@ __global__ __launch_bounds__(64 * kUpWaves) void moe_up_kernel(const MoeTokens m
       u += sums[w][i][1][from][col & 3];
     }
     const float h = g / (1.f + exp2_fast(-g * kLog2e)) * u;
-    reinterpret_cast<__bf16*>(m.h)[(int64_t)slot_of[at] * m.F + strip * kStrip + col] = (__bf16)h;
+    reinterpret_cast<__bf16*>(m.h)[(int64_t)slot_of[at] * m.F + strip * 16 + col] = (__bf16)h;
   }
 }
 
+template <int TILES>
 __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(const MoeTokens m) {
-  __shared__ Routing routing;
+  extern __shared__ __align__(16) char lds[];      // routing; the waves' strips, then their sums
   __shared__ uint16_t chosen[kMoeMaxExperts];
-  __shared__ __align__(16) float sums[kDownWaves][kTiles][64][4];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int strip = blockIdx.x;
+  const int strips = m.K / 32, share = blockIdx.x / strips, strip = blockIdx.x - share * strips;
 
-  load_routing<64 * kDownWaves>(m, routing);
+  const Routing routing(m, lds, 64 * kDownWaves);
+  char* const area = lds + routing_bytes_of(m);
   uint32_t word;
   int before;
   const int experts = count_chosen(routing, word, before);
@@ -211,72 +290,174 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(const MoeToke
     for (; word; word &= word - 1) chosen[before++] = (uint16_t)(32 * lane + __ffs((int)word) - 1);
   __syncthreads();
 
-  const int tiles = (m.T + 15) / 16, chunks = m.F / kChunkK;
-  const int inner = 32 * (lane >> 4), row = strip * kStrip + (lane & 15);
-  const int units = experts * chunks;      // at most 1024 * 512
-  const int begin = (int)((int64_t)units * wave / kDownWaves), end = (int)((int64_t)units * (wave + 1) / kDownWaves);
-  f32x4 acc[kTiles];
+  const int tiles = (m.T + 15) / 16, pieces = m.F / kPiece;
+  const int units = experts * pieces, parts = m.shares * kDownWaves, part = share * kDownWaves + wave;
+  const int begin = (int)((int64_t)units * part / parts), end = (int)((int64_t)units * (part + 1) / parts);
+  f32x4 acc[TILES][2];
 #pragma unroll
-  for (int i = 0; i < kTiles; ++i) acc[i] = zero4();
-  for (int unit = begin; unit < end;) {
-    const int n = unit / chunks, c0 = unit - n * chunks, c1 = min(chunks, c0 + end - unit);
-    unit += c1 - c0;
-    const int e = __builtin_amdgcn_readfirstlane((int)chosen[n]);
-    const Member mine = member_of<true>(m, routing, e);
-    const uint64_t members = __ballot(mine.slot >= 0);
-    const uint16_t* h[kTiles];
-    float w[kTiles];
-    bool in[kTiles];
+  for (int i = 0; i < TILES; ++i) acc[i][0] = acc[i][1] = zero4();
+  if (begin < end) {
+    struct At {      // a unit: piece c of the n-th chosen expert
+      int n, c;
+    };
+    auto next = [&](At& a, int unit) {      // the one after `unit`; the last one stays
+      if (unit + 1 >= end) return;
+      if (++a.c == pieces) {
+        a.c = 0;
+        ++a.n;
+      }
+    };
+    const uint8_t* down = m.w_down + (int64_t)(strip * 32 + (lane >> 3)) * m.F + 16 * (lane & 7);
+    auto load = [&](Piece& p, const At& a) {
+      const int e = __builtin_amdgcn_readfirstlane((int)chosen[a.n]);
+      const uint8_t* at = down + (int64_t)e * m.K * m.F + a.c * kPiece;
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-      // tokens that did not choose the expert read one that did, and add nothing
-      const int of = 16 * i + (lane & 15);
-      const uint32_t some = (uint32_t)(members >> (16 * i)) & 0xFFFFu;
-      in[i] = (members >> of) & 1;
-      w[i] = __shfl(mine.weight, of, 64);
-      const int other = some ? 16 * i + __ffs((int)some) - 1 : 0;
-      h[i] = m.h + (int64_t)__shfl(mine.slot, in[i] ? of : other, 64) * m.F + inner;
+      for (int i = 0; i < 4; ++i) p.w[i] = *reinterpret_cast<const u32x4*>(at + 8 * i * (int64_t)m.F);
+    };
+    const Trade trade(area + kStripBytes * wave);
+    At ahead{begin / pieces, 0};
+    ahead.c = begin - ahead.n * pieces;
+    At now = ahead;
+    int to_load = begin;
+    Piece ring[kDeep];
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) {
+      load(ring[i], ahead);
+      next(ahead, to_load++);
     }
-    const uint8_t* down = m.w_down + ((int64_t)e * m.K + row) * m.F + inner;
-    const float* sd = m.s_down + ((int64_t)e * (m.K / kChunkK) + strip * kStrip / kChunkK) * chunks;
-#pragma unroll 2
-    for (int c = c0; c < c1; ++c) {
-      Codes d;
-      d.load(down + c * kChunkK);
-      const float f = sd[c];
+    uint64_t members = 0;
+    const uint16_t* h[TILES];
+    float w[TILES];
+    bool in[TILES];
+    const float* sd = nullptr;
+    Numbers b[2][TILES];
+    auto load_h = [&](Numbers (&to)[TILES], int c) {
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) {
+      for (int i = 0; i < TILES; ++i)
+        if (i < tiles && ((members >> (16 * i)) & 0xFFFF)) to[i].load(h[i] + c * kPiece);
+    };
+    auto enter = [&](Numbers (&to)[TILES]) {      // the expert of unit `now`
+      const int e = __builtin_amdgcn_readfirstlane((int)chosen[now.n]);
+      const Member mine = member_of<true>(m, routing, e);
+      members = __ballot(mine.slot >= 0);
+#pragma unroll
+      for (int i = 0; i < TILES; ++i) {
+        // tokens that did not choose the expert read one that did, and add nothing
+        const int of = 16 * i + (lane & 15);
+        const uint32_t some = (uint32_t)(members >> (16 * i)) & 0xFFFFu;
+        in[i] = (members >> of) & 1;
+        w[i] = __shfl(mine.weight, of, 64);
+        const int other = some ? 16 * i + __ffs((int)some) - 1 : 0;
+        h[i] = m.h + (int64_t)__shfl(mine.slot, in[i] ? of : other, 64) * m.F + 32 * (lane >> 4);
+      }
+      sd = m.s_down + ((int64_t)e * (m.K / kPiece) + strip * 32 / kPiece) * pieces;
+      load_h(to, now.c);
+    };
+    enter(b[0]);
+    auto step = [&](int unit, Piece& p, Numbers (&cur)[TILES], Numbers (&nxt)[TILES]) {
+      const float f = sd[now.c];
+      trade.write(p);
+      load(p, ahead);
+      next(ahead, to_load++);
+      const bool stays = now.c + 1 < pieces;
+      if (stays) load_h(nxt, now.c + 1);
+      bf16x8 d[2][4];
+      trade.read(0, d[0]);
+      trade.read(1, d[1]);
+#pragma unroll
+      for (int i = 0; i < TILES; ++i) {
         if (i < tiles && ((members >> (16 * i)) & 0xFFFF)) {
-          f32x4 part = zero4();
-#pragma unroll
-          for (int s = 0; s < 4; ++s)
-            part = mfma16(d.operand(s), *reinterpret_cast<const bf16x8*>(h[i] + c * kChunkK + 8 * s), part);
           const float fw = f * w[i];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = in[i] ? fmaf(fw, part[j], acc[i][j]) : acc[i][j];
+          for (int a = 0; a < 2; ++a) {
+            f32x4 sum = zero4();
+#pragma unroll
+            for (int s = 0; s < 4; ++s) sum = mfma16(d[a][s], cur[i].b[s], sum);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][a][j] = in[i] ? fmaf(fw, sum[j], acc[i][a][j]) : acc[i][a][j];
+          }
         }
       }
+      next(now, unit);
+      if (!stays && unit + 1 < end) enter(nxt);
+    };
+    for (int unit = begin; unit < end; unit += kDeep) {
+      step(unit, ring[0], b[0], b[1]);
+      if (unit + 1 >= end) break;
+      step(unit + 1, ring[1], b[1], b[0]);
+      if (unit + 2 >= end) break;
+      step(unit + 2, ring[2], b[0], b[1]);
+      if (unit + 3 >= end) break;
+      step(unit + 3, ring[3], b[1], b[0]);
     }
   }
+  typedef float Sums[TILES][2][64][4];
+  Sums* const sums = reinterpret_cast<Sums*>(area);
+  __syncthreads();      // the strips are done with
 #pragma unroll
-  for (int i = 0; i < kTiles; ++i)
-    if (i < tiles) *reinterpret_cast<f32x4*>(sums[wave][i][lane]) = acc[i];
+  for (int i = 0; i < TILES; ++i)
+    if (i < tiles) {
+      *reinterpret_cast<f32x4*>(sums[wave][i][0][lane]) = acc[i][0];
+      *reinterpret_cast<f32x4*>(sums[wave][i][1][lane]) = acc[i][1];
+    }
   __syncthreads();
-  for (int at = threadIdx.x; at < 16 * m.T; at += 64 * kDownWaves) {
-    const int t = at >> 4, col = at & 15;
+  // a thread: a token and one of the strip's columns
+  auto sum_of = [&](int t, int col) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kDownWaves; ++w) v += sums[w][t >> 4][16 * (col >> 2) + (t & 15)][col & 3];
-    reinterpret_cast<__bf16*>(m.out)[(int64_t)t * m.K + strip * kStrip + col] = (__bf16)v;
+    for (int w = 0; w < kDownWaves; ++w) v += sums[w][t >> 4][col >> 4][16 * ((col >> 2) & 3) + (t & 15)][col & 3];
+    return v;
+  };
+  __bf16* const out = reinterpret_cast<__bf16*>(m.out) + strip * 32;
+  if (m.shares == 1) {
+    for (int at = threadIdx.x; at < 32 * m.T; at += 64 * kDownWaves) out[(int64_t)(at >> 5) * m.K + (at & 31)] = (__bf16)sum_of(at >> 5, at & 31);
+    return;
   }
+  float* const mine = m.part + (int64_t)share * m.T * m.K + strip * 32;
+  for (int at = threadIdx.x; at < 32 * m.T; at += 64 * kDownWaves) mine[(int64_t)(at >> 5) * m.K + (at & 31)] = sum_of(at >> 5, at & 31);
+}
+
+// The shares' sums, in order: a thread has four numbers.
+__global__ __launch_bounds__(kJoinThreads) void moe_join_kernel(const MoeTokens m) {
+  const int64_t all = (int64_t)m.T * m.K, at = ((int64_t)blockIdx.x * kJoinThreads + threadIdx.x) * 4;
+  if (at >= all) return;
+  f32x4 v = *reinterpret_cast<const f32x4*>(m.part + at);
+  for (int i = 1; i < m.shares; ++i) v += *reinterpret_cast<const f32x4*>(m.part + i * all + at);
+  bf16x4 b;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) b[j] = (__bf16)v[j];
+  *reinterpret_cast<bf16x4*>(m.out + at) = b;
+}
+
+template <int TILES>
+void launch_tiles(const MoeTokens& m, hipStream_t stream) {
+  const int most = m.T * m.topk < m.E ? m.T * m.topk : m.E;
+  // the waves' strips, later their sums
+  constexpr size_t sums = sizeof(float) * TILES * 2 * 64 * 4, area = sums > kStripBytes ? sums : (size_t)kStripBytes;
+  hipLaunchKernelGGL(moe_up_kernel<TILES>, dim3((unsigned)(most * (m.F / 16))), dim3(64 * kUpWaves),
+                     routing_bytes_of(m) + kUpWaves * area, stream, m);
+  hipLaunchKernelGGL(moe_down_kernel<TILES>, dim3((unsigned)(m.shares * (m.K / 32))), dim3(64 * kDownWaves),
+                     routing_bytes_of(m) + kDownWaves * area, stream, m);
+  if (m.shares > 1)
+    hipLaunchKernelGGL(moe_join_kernel, dim3((unsigned)(((int64_t)m.T * m.K / 4 + kJoinThreads - 1) / kJoinThreads)), dim3(kJoinThreads), 0, stream, m);
 }
 
 }  // namespace
 
+// Shares of the second kernel's work, where the output has fewer strips of
+// columns than three quarters of the compute units.
+int moe_shares(int64_t K) {
+  const int64_t strips = K / 32;
+  return (int)((192 + strips - 1) / strips);
+}
+
 hipError_t launch_moe_tokens(const MoeTokens& m, hipStream_t stream) {
-  const int most = m.T * m.topk < m.E ? m.T * m.topk : m.E;
-  hipLaunchKernelGGL(moe_up_kernel, dim3((unsigned)(most * (m.F / kStrip))), dim3(64 * kUpWaves), 0, stream, m);
-  hipLaunchKernelGGL(moe_down_kernel, dim3((unsigned)(m.K / kStrip)), dim3(64 * kDownWaves), 0, stream, m);
+  if (m.T <= 16)
+    launch_tiles<1>(m, stream);
+  else if (m.T <= 32)
+    launch_tiles<2>(m, stream);
+  else
+    launch_tiles<4>(m, stream);
   return hipGetLastError();
 }
 

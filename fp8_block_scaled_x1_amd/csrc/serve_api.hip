@@ -150,25 +150,25 @@ int fp8bs_mla_decode_fp4_shared(const uint16_t* q, const uint8_t* cache, const u
                  table_width, lens, B, T, H, scale, out, lse, workspace, stream);
 }
 
-int64_t fp8bs_moe_tokens_workspace_bytes(int T, int topk, int64_t F) {
-  if (T < 0 || T > fp8bs::kMoeMaxTokens || topk < 1 || topk > fp8bs::kMoeMaxTopk || F < 128 || F % 128)
+int64_t fp8bs_moe_tokens_workspace_bytes(int T, int topk, int64_t K, int64_t F) {
+  if (T < 0 || T > fp8bs::kMoeMaxTokens || topk < 1 || topk > fp8bs::kMoeMaxTopk || K < 128 || K % 128 || F < 128 || F % 128)
     return FP8BS_ERR_SHAPE;
-  if (F > 1 << 16) return FP8BS_ERR_TOO_LARGE;
-  return (int64_t)2 * T * topk * F;
+  if (K > 1 << 16 || F > 1 << 16) return FP8BS_ERR_TOO_LARGE;
+  return align256((int64_t)2 * T * topk * F) + 4 * fp8bs::moe_shares(K) * T * K;
 }
 
 int fp8bs_moe_tokens(const uint16_t* x, int T, int64_t K, const int32_t* topk_ids, const float* weights, int topk,
                      const uint8_t* w_up, const float* s_up, const uint8_t* w_down, const float* s_down, int E,
                      int64_t F, uint16_t* out, void* workspace, void* stream) {
-  const int64_t bytes = fp8bs_moe_tokens_workspace_bytes(T, topk, F);
+  const int64_t bytes = fp8bs_moe_tokens_workspace_bytes(T, topk, K, F);
   if (bytes < 0) return (int)bytes;
-  if (E < 1 || E > fp8bs::kMoeMaxExperts || K < 128 || K % 128) return FP8BS_ERR_SHAPE;
-  if (K > 1 << 16) return FP8BS_ERR_TOO_LARGE;
+  if (E < 1 || E > fp8bs::kMoeMaxExperts) return FP8BS_ERR_SHAPE;
   if (T == 0) return FP8BS_OK;
   if (!x || !topk_ids || !weights || !w_up || !s_up || !w_down || !s_down || !out || !workspace)
     return FP8BS_ERR_NULL_PTR;
   if (off16(x) || off16(w_up) || off16(w_down) || off16(out) || off16(workspace)) return FP8BS_ERR_ALIGN;
   if (off4(topk_ids) || off4(weights) || off4(s_up) || off4(s_down)) return FP8BS_ERR_ALIGN;
+  char* ws = static_cast<char*>(workspace);
   fp8bs::MoeTokens m{};
   m.x = x;
   m.ids = topk_ids;
@@ -177,13 +177,15 @@ int fp8bs_moe_tokens(const uint16_t* x, int T, int64_t K, const int32_t* topk_id
   m.s_up = s_up;
   m.w_down = w_down;
   m.s_down = s_down;
-  m.h = static_cast<uint16_t*>(workspace);
+  m.h = reinterpret_cast<uint16_t*>(ws);
+  m.part = reinterpret_cast<float*>(ws + align256((int64_t)2 * T * topk * F));
   m.out = out;
   m.T = T;
   m.topk = topk;
   m.E = E;
   m.K = (int)K;
   m.F = (int)F;
+  m.shares = fp8bs::moe_shares(K);
   return status_of(fp8bs::launch_moe_tokens(m, as_stream(stream)));
 }
 

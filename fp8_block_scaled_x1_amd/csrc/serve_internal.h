@@ -44,10 +44,12 @@ struct MoeTokens {
   const uint8_t* w_down;    // [E][K][F]
   const float* s_down;      // [E][K/128][F/128]
   uint16_t* h;              // [T*topk][F] BF16, row of the first slot in which a token names an expert
+  float* part;              // [shares][T][K] sums of a share of the second kernel's work
   uint16_t* out;            // [T][K]
-  int T, topk, E, K, F;
+  int T, topk, E, K, F, shares;
 };
 constexpr int kMoeMaxTokens = 64, kMoeMaxTopk = 64, kMoeMaxExperts = 1024;
+int moe_shares(int64_t K);
 hipError_t launch_moe_tokens(const MoeTokens& m, hipStream_t stream);
 
 struct Logprobs {

@@ -126,13 +126,13 @@ FP8BS_API int64_t fp8bs_mla_decode_fp4_workspace_bytes(int B, int T, int H, int6
  * weights are read once. Inputs finite; a code 0x7F or 0xFF is a NaN.
  * 0 <= T <= 64, 1 <= topk <= 64, 1 <= E <= 1024; K and F multiples of 128, at
  * least 128 (FP8BS_ERR_TOO_LARGE above 2^16). workspace: at least
- * fp8bs_moe_tokens_workspace_bytes(T, topk, F) bytes.
+ * fp8bs_moe_tokens_workspace_bytes(T, topk, K, F) bytes.
  */
 FP8BS_API int fp8bs_moe_tokens(const uint16_t* x, int T, int64_t K, const int32_t* topk_ids,
                       const float* weights, int topk, const uint8_t* w_up, const float* s_up,
                       const uint8_t* w_down, const float* s_down, int E, int64_t F, uint16_t* out,
                       void* workspace, void* stream);
-FP8BS_API int64_t fp8bs_moe_tokens_workspace_bytes(int T, int topk, int64_t F);
+FP8BS_API int64_t fp8bs_moe_tokens_workspace_bytes(int T, int topk, int64_t K, int64_t F);
 
 /*
  * Log probabilities of given tokens: for every row x of logits and y = targets[t],

@@ -122,7 +122,7 @@ def test_moe_refusals(L):
     for name in ("ids", "w", "su", "sd"):
         assert call(**{name: MIS}) == -3, name
     ws = L.fp8bs_moe_tokens_workspace_bytes
-    assert ws(5, 2, 128) >= 2 * 5 * 2 * 128 and ws(65, 2, 128) == -2 and ws(5, 2, 100) == -2 and ws(5, 2, 1 << 17) == -7
+    assert ws(5, 2, 256, 128) >= 2 * 5 * 2 * 128 and ws(65, 2, 256, 128) == -2 and ws(5, 2, 100, 128) == -2 and ws(5, 2, 256, 1 << 17) == -7
 
 
 def test_logprobs_refusals(L):
