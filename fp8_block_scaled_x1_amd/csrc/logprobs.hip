@@ -11,13 +11,20 @@
 // second launch joins a row's chunks, or the first one writes the row's result
 // where the row is one chunk.
 //
+// The exponentials are 2^(c x - c m), c = log2 e, one fused multiply-add each:
+// what c m loses by its own rounding is a factor of all of them, known exactly
+// and taken back from the sums. An entry comes before the token if it is larger,
+// or equal and ahead of it, so in a chunk that the token is not in one
+// comparison tells, counted by the scalar unit.
+//
 // Best entries: an entry's key is its value in an order of whole numbers, then
 // the lowest index, so keys differ. A wave takes the top-th largest of its
-// lanes' own largest keys as a bound, found bit by bit with ballots: at least
-// `top` entries of the wave reach it, and only lanes that reach it hold any
-// that do, so at most 32 * top. Those of all waves go to LDS, where an entry's
-// place is the number of larger ones. Which slot of the list an entry gets
-// depends on chance, its place does not.
+// lanes' own largest values as a bound, found bit by bit with ballots: at least
+// `top` entries of the wave reach it. Those of all waves go to LDS, where an
+// entry's place is the number of larger keys. Which slot of the list an entry
+// gets depends on chance, its place does not. Where so many entries are equal
+// that there are several times `top`, the bound is taken by keys: then only
+// `top` lanes of a wave, so 32 * top entries, reach it.
 
 #include "attn_common.h"
 #include "serve_internal.h"
@@ -42,48 +49,59 @@ __device__ __forceinline__ float number(const void* p, int64_t i) {
 }
 
 // Numbers of a 16-byte access, and the chunk's groups of them per thread: group
-// k of thread i begins at entry VEC * (i + kThreads * k).
+// k of thread i begins at entry VEC * (i + kThreads * k). A group that the end
+// of the row cuts (of `n` entries, at least VEC of them in the row) is read from
+// VEC before the end: its first entries are the group before's.
 template <bool BF16>
 struct Layout {
-  static constexpr int VEC = BF16 ? 8 : 4, GROUPS = kPer / VEC;
-  __device__ __forceinline__ static int at(int k) { return VEC * ((int)threadIdx.x + kThreads * k); }
+  static constexpr int VEC = BF16 ? 8 : 4, GROUPS = kPer / VEC, SIZE = BF16 ? 2 : 4;
+  __device__ __forceinline__ static int nominal(int k) { return VEC * ((int)threadIdx.x + kThreads * k); }
+  template <bool FULL>
+  __device__ __forceinline__ static int at(int k, int n) { return FULL ? nominal(k) : min(nominal(k), n - VEC); }
 };
 
-// The thread's entries of the chunk of `n` entries at row + first; those past
-// its end read as -inf.
 template <bool BF16>
-__device__ __forceinline__ void load_chunk(const void* row, int64_t first, int n, float (&x)[kPer]) {
+__device__ __forceinline__ u32x4 load16(const char* p) {
+  if constexpr (BF16)
+    return *reinterpret_cast<const u32x4_by2*>(p);
+  else
+    return *reinterpret_cast<const u32x4_by4*>(p);
+}
+template <bool BF16>
+__device__ __forceinline__ void store16(char* p, u32x4 d) {
+  if constexpr (BF16)
+    *reinterpret_cast<u32x4_by2*>(p) = d;
+  else
+    *reinterpret_cast<u32x4_by4*>(p) = d;
+}
+
+// The thread's entries of a chunk at `base`.
+template <bool BF16, bool FULL>
+__device__ __forceinline__ void load_raw(const char* base, int n, u32x4 (&d)[Layout<BF16>::GROUPS]) {
   using L = Layout<BF16>;
-  const char* base = reinterpret_cast<const char*>(row) + first * (BF16 ? 2 : 4);
-  if (n >= kLpChunk) {
-    u32x4 d[L::GROUPS];
 #pragma unroll
-    for (int k = 0; k < L::GROUPS; ++k) {
-      if constexpr (BF16)
-        d[k] = *reinterpret_cast<const u32x4_by2*>(base + 2 * L::at(k));
-      else
-        d[k] = *reinterpret_cast<const u32x4_by4*>(base + 4 * L::at(k));
-    }
-#pragma unroll
-    for (int k = 0; k < L::GROUPS; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (BF16) {
-          x[8 * k + 2 * i] = __uint_as_float(d[k][i] << 16);
-          x[8 * k + 2 * i + 1] = __uint_as_float(d[k][i] & 0xFFFF0000u);
-        } else {
-          x[4 * k + i] = __uint_as_float(d[k][i]);
-        }
-      }
-    return;
-  }
+  for (int k = 0; k < L::GROUPS; ++k) d[k] = load16<BF16>(base + (int64_t)L::SIZE * L::template at<FULL>(k, n));
+}
+template <bool BF16>
+__device__ __forceinline__ void numbers_of(const u32x4 (&d)[Layout<BF16>::GROUPS], float (&x)[kPer]) {
+  using L = Layout<BF16>;
 #pragma unroll
   for (int k = 0; k < L::GROUPS; ++k)
 #pragma unroll
-    for (int i = 0; i < L::VEC; ++i) {
-      const int at = L::at(k) + i;
-      x[L::VEC * k + i] = at < n ? number<BF16>(base, at) : neg_inf();
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (BF16) {
+        x[8 * k + 2 * i] = __uint_as_float(d[k][i] << 16);
+        x[8 * k + 2 * i + 1] = __uint_as_float(d[k][i] & 0xFFFF0000u);
+      } else {
+        x[4 * k + i] = __uint_as_float(d[k][i]);
+      }
     }
+}
+template <bool BF16, bool FULL>
+__device__ __forceinline__ void load_chunk(const char* base, int n, float (&x)[kPer]) {
+  u32x4 d[Layout<BF16>::GROUPS];
+  load_raw<BF16, FULL>(base, n, d);
+  numbers_of<BF16>(d, x);
 }
 
 // Ascending with the value, -0 as 0.
@@ -106,29 +124,17 @@ __device__ __forceinline__ T wave_sum(T v) {
   return v;
 }
 
-// The n-th largest of the wave's keys (n <= 64; lanes without one hold 0).
-__device__ __forceinline__ uint64_t nth_key(uint64_t key, int n) {
-  const uint32_t hi = (uint32_t)(key >> 32), lo = (uint32_t)key;
+// The n-th largest of the wave's values (n <= 64), counted with those that `above` more lanes are known to exceed.
+__device__ __forceinline__ uint32_t nth_value(uint32_t v, int n, bool counts = true, int above = 0) {
   uint32_t h = 0;
-  int above = 0;      // keys whose upper half is larger than h in the bits so far settled
 #pragma unroll 1
   for (int b = 31; b >= 0; --b) {
     const uint32_t c = h | (1u << b);
-    const int count = (int)__popcll(__ballot(hi >= c));
+    const int count = above + (int)__popcll(__ballot(counts && v >= c));
     if (count >= n) h = c;
-    if (count == n) return (uint64_t)h << 32;
-  }
-  above = (int)__popcll(__ballot(hi > h));
-  uint32_t l = 0;
-  const bool tied = hi == h;
-#pragma unroll 1
-  for (int b = 31; b >= 0; --b) {
-    const uint32_t c = l | (1u << b);
-    const int count = above + (int)__popcll(__ballot(tied && lo >= c));
-    if (count >= n) l = c;
     if (count == n) break;
   }
-  return ((uint64_t)h << 32) | l;
+  return h;
 }
 
 struct Sums {      // of a part of a row
@@ -143,6 +149,39 @@ __device__ __forceinline__ void add_part(Sums& s, const Sums& x) {
   s.w = ea * (s.w + scaled(s.l, a)) + eb * (x.w + scaled(x.l, b));
   s.l = s.l * ea + x.l * eb;
   s.m = m;
+}
+
+// Sums of exp(x_i - m) and of that times (x_i - m); `usual`: the same for the
+// wave, and |m| < 2^100 if it is set.
+__device__ __forceinline__ void sums_against(const float (&x)[kPer], float m, bool usual, float& l, float& w) {
+  l = w = 0.f;
+  if (usual) {
+    const float m2 = m * kLog2e, lost = fmaf(m, kLog2e, -m2);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const float d = fmaf(x[i], kLog2e, -m2), e = exp2_fast(d);
+      l += e;
+      w = fmaf(e, fmaxf(d, -1000.f), w);      // (0 * -inf; a NaN shows in l)
+    }
+    const float back = exp2_fast(-lost);
+    w = fmaf(-lost, l, w) * back * kLn2;
+    l *= back;
+  } else {      // far from anything usual (-inf and NaN among them): differences first
+    const float ref = m == neg_inf() ? 0.f : m;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const float d = x[i] - ref, e = exp2_fast(d * kLog2e);
+      l += e;
+      w += e == 0.f ? 0.f : e * d;
+    }
+  }
+}
+
+// Entries of a chunk that all lie ahead of the token, or all behind it, come
+// before it if they reach this: its value, or the next larger one (0 and -0 are equal).
+__device__ __forceinline__ float least_before(float xy, bool ahead) {
+  const uint32_t u = __float_as_uint(xy + 0.f);
+  return ahead ? xy : __uint_as_float(u == 0 ? 1u : (u >> 31) ? u - 1u : u + 1u);
 }
 
 // What the log probability of a logit x is taken against: (x - m) - n.
@@ -167,15 +206,12 @@ __device__ __forceinline__ Norm finish_row(const Logprobs& p, int64_t t, const S
   return o;
 }
 
-// Places of the `count` keys in `list` (LDS) in descending order: put(place, key) for the first `top`.
-template <typename Put>
-__device__ __forceinline__ void place_keys(const uint64_t* list, int count, int top, Put&& put) {
-  for (int i = threadIdx.x; i < count; i += kThreads) {
-    const uint64_t key = list[i];
-    int place = 0;
-    for (int j = 0; j < count; ++j) place += list[j] > key;
-    if (place < top) put(place, key);
-  }
+// How many of a list's keys are larger.
+__device__ __forceinline__ int keys_before(uint64_t key, const uint64_t* list, int count) {
+  int n = 0;
+#pragma unroll 8
+  for (int j = 0; j < count; ++j) n += list[j] > key;
+  return n;
 }
 
 __device__ __forceinline__ void put_top(const Logprobs& p, int64_t t, const Norm& o, int place, uint64_t key) {
@@ -183,93 +219,245 @@ __device__ __forceinline__ void put_top(const Logprobs& p, int64_t t, const Norm
   p.top_logprobs[t * p.top + place] = logprob_of(o, value_of((uint32_t)(key >> 32)));
 }
 
-template <bool BF16, bool TOP>
-__global__ __launch_bounds__(kThreads) void logprobs_chunk_kernel(const Logprobs p, int chunks) {
-  extern __shared__ __align__(16) uint64_t list[];      // kThreads / 64 * kPer * top
-  __shared__ float wmax[kThreads / 64];
-  __shared__ float4 wsum[kThreads / 64];
-  __shared__ Norm norm;
-  __shared__ int count;
+struct ChunkShared {
+  float wmax[kThreads / 64];
+  uint32_t wbound[kThreads / 64];
+  float4 wsum[kThreads / 64];
+  Norm norm;
+  int count[kThreads / 64], overflow;
+};
+
+// With alternatives: a workgroup has one chunk of a row.
+template <bool BF16, bool FULL>
+__device__ __forceinline__ void chunk_of_row(const Logprobs& p, int64_t t, int chunk, int chunks, uint64_t* list, ChunkShared& sh) {
+  using L = Layout<BF16>;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t = blockIdx.x / chunks;
-  const int chunk = (int)(blockIdx.x - t * chunks), first = chunk * kLpChunk, n = min(p.V - first, kLpChunk);
+  const int first = chunk * kLpChunk, n = FULL ? kLpChunk : p.V - first;
   const int y = p.targets[t];
   const bool token = y >= 0 && y < p.V;
   float x[kPer];
-  load_chunk<BF16>(p.logits, t * p.stride + first, n, x);
-  const float xy = token ? number<BF16>(p.logits, t * p.stride + y) : __builtin_inff();
-
-  float m = x[0];
+  const char* base = reinterpret_cast<const char*>(p.logits) + (t * p.stride + first) * L::SIZE;
+  if (FULL || p.V >= L::VEC) {
+    load_chunk<BF16, FULL>(base, n, x);
+  } else {      // fewer entries than an access has
 #pragma unroll
-  for (int i = 1; i < kPer; ++i) m = max_nan(m, x[i]);
-  m = wave_max_nan(m);
-  if (lane == 0) wmax[wave] = m;
-  if (TOP && threadIdx.x == 0) count = 0;
+    for (int i = 0; i < kPer; ++i) x[i] = i < L::VEC && threadIdx.x == 0 && i < n ? number<BF16>(base, i) : neg_inf();
+  }
+  const float xy = token ? number<BF16>(p.logits, t * p.stride + y) : __builtin_inff();
+  // index in the chunk of entry i of group k, and whether it is the thread's
+  auto index = [&](int k, int i) { return (FULL || p.V >= L::VEC ? L::template at<FULL>(k, n) : L::nominal(k)) + i; };
+  auto own = [&](int k, int i) { return FULL || (index(k, i) >= L::nominal(k) && index(k, i) < n); };
+  if constexpr (!FULL) {
+#pragma unroll
+    for (int k = 0; k < L::GROUPS; ++k)
+#pragma unroll
+      for (int i = 0; i < L::VEC; ++i) x[L::VEC * k + i] = own(k, i) ? x[L::VEC * k + i] : neg_inf();
+  }
+
+  float mine = x[0];
+#pragma unroll
+  for (int i = 1; i < kPer; ++i) mine = max_nan(mine, x[i]);
+  float m = wave_max_nan(mine);
+  const uint32_t best = order_of(mine);
+  uint32_t bound = nth_value(best, p.top);
+  if (lane == 0) {
+    sh.wmax[wave] = m;
+    sh.wbound[wave] = bound;
+  }
+  if (threadIdx.x == 0) sh.overflow = 0;
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kThreads / 64; ++k) m = max_nan(m, wmax[k]);
-  const float ref = m == neg_inf() ? 0.f : m;
-  float l = 0.f, w = 0.f;
-  int before = 0;
-#pragma unroll
-  for (int k = 0; k < Layout<BF16>::GROUPS; ++k)
-#pragma unroll
-    for (int i = 0; i < Layout<BF16>::VEC; ++i) {
-      const float v = x[Layout<BF16>::VEC * k + i], d = v - ref, e = exp2_fast(d * kLog2e);
-      l += e;
-      w += e == 0.f ? 0.f : e * d;
-      before += v > xy || (v == xy && first + Layout<BF16>::at(k) + i < y);
-    }
+  for (int k = 0; k < kThreads / 64; ++k) {
+    m = max_nan(m, sh.wmax[k]);
+    bound = max(bound, sh.wbound[k]);
+  }
+
+  float l, w;
+  sums_against(x, m, fabsf(m) < 0x1p100f, l, w);
   l = wave_sum(l);
   w = wave_sum(w);
-  before = wave_sum(before);
-  if (lane == 0) wsum[wave] = make_float4(l, w, __int_as_float(before), 0.f);
-
-  if constexpr (TOP) {
-    // the lane's largest key
-    uint64_t best = 0;
+  int before = 0;      // of the wave: entries that come before the token
+  if (FULL && (y < first || y >= first + kLpChunk)) {
+    const float least = least_before(xy, y >= first + kLpChunk);
 #pragma unroll
-    for (int k = 0; k < Layout<BF16>::GROUPS; ++k)
+    for (int i = 0; i < kPer; ++i) before += (int)__popcll(__ballot(x[i] >= least));
+  } else {
 #pragma unroll
-      for (int i = 0; i < Layout<BF16>::VEC; ++i) {
-        const int at = Layout<BF16>::at(k) + i;
-        const uint64_t key = at < n ? key_of(x[Layout<BF16>::VEC * k + i], first + at) : 0;
-        best = key > best ? key : best;
-      }
-    const uint64_t bound = nth_key(best, p.top);
+    for (int k = 0; k < L::GROUPS; ++k)
 #pragma unroll
-    for (int k = 0; k < Layout<BF16>::GROUPS; ++k)
-#pragma unroll
-      for (int i = 0; i < Layout<BF16>::VEC; ++i) {
-        const int at = Layout<BF16>::at(k) + i;
-        const uint64_t key = at < n ? key_of(x[Layout<BF16>::VEC * k + i], first + at) : 0;
-        if (key != 0 && key >= bound) list[atomicAdd(&count, 1)] = key;
+      for (int i = 0; i < L::VEC; ++i) {
+        const float v = x[L::VEC * k + i];
+        before += (int)__popcll(__ballot(v > xy || (v == xy && own(k, i) && first + index(k, i) < y)));
       }
   }
+  if (lane == 0) sh.wsum[wave] = make_float4(l, w, __int_as_float(before), 0.f);
+
+  // The wave's entries that `reaches`(k, i) names, to its part of the list.
+  uint64_t* const own_list = list + wave * kPer * p.top;
+  auto put = [&](int most, auto&& reaches) {
+    int at = 0;
+#pragma unroll
+    for (int k = 0; k < L::GROUPS; ++k)
+#pragma unroll
+      for (int i = 0; i < L::VEC; ++i) {
+        const bool mine = reaches(k, i);
+        const uint64_t all = __ballot(mine);
+        if (all == 0) continue;
+        const int slot = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0));
+        if (mine && slot < most) own_list[slot] = key_of(x[L::VEC * k + i], first + index(k, i));
+        at += (int)__popcll(all);
+      }
+    if (lane == 0) sh.count[wave] = at;
+    if (at > most) sh.overflow = 1;
+  };
+  const int few = min(2 * p.top + 32, kPer * p.top);
+  if (__any(best >= bound)) {
+    const float least = value_of(bound);
+    put(few, [&](int k, int i) { return !(x[L::VEC * k + i] < least) && own(k, i); });
+  } else if (lane == 0) {
+    sh.count[wave] = 0;
+  }
   __syncthreads();
+  if (sh.overflow) {      // the same for all
+    __syncthreads();
+    uint64_t best = 0;
+#pragma unroll
+    for (int k = 0; k < L::GROUPS; ++k)
+#pragma unroll
+      for (int i = 0; i < L::VEC; ++i) {
+        const uint64_t key = own(k, i) ? key_of(x[L::VEC * k + i], first + index(k, i)) : 0;
+        best = key > best ? key : best;
+      }
+    const uint32_t hi = (uint32_t)(best >> 32), lo = (uint32_t)best, h = nth_value(hi, p.top);
+    const uint64_t bound = ((uint64_t)h << 32) | nth_value(lo, p.top, hi == h, (int)__popcll(__ballot(hi > h)));
+    put(kPer * p.top, [&](int k, int i) { return own(k, i) && key_of(x[L::VEC * k + i], first + index(k, i)) >= bound; });
+    __syncthreads();
+  }
   Sums s{m, 0.f, 0.f};
+  int count = 0;
   before = 0;
 #pragma unroll
   for (int k = 0; k < kThreads / 64; ++k) {
-    s.l += wsum[k].x;
-    s.w += wsum[k].y;
-    before += __float_as_int(wsum[k].z);
+    count += sh.count[k];
+    s.l += sh.wsum[k].x;
+    s.w += sh.wsum[k].y;
+    before += __float_as_int(sh.wsum[k].z);
   }
-  if (chunks == 1) {
-    if (threadIdx.x == 0) norm = finish_row<BF16>(p, t, s, before);
-    if constexpr (TOP) {
-      __syncthreads();
-      const Norm o = norm;
-      place_keys(list, count, p.top, [&](int place, uint64_t key) { put_top(p, t, o, place, key); });
+  auto place = [&](auto&& to) {
+    for (int i = lane; i < sh.count[wave]; i += 64) {
+      const uint64_t key = own_list[i];
+      int before = 0;
+      for (int k = 0; k < kThreads / 64; ++k) before += keys_before(key, list + k * kPer * p.top, sh.count[k]);
+      if (before < p.top) to(before, key);
     }
+  };
+  if (chunks == 1) {
+    if (threadIdx.x == 0) sh.norm = finish_row<BF16>(p, t, s, before);
+    __syncthreads();
+    const Norm o = sh.norm;
+    place([&](int place, uint64_t key) { put_top(p, t, o, place, key); });
     return;
   }
   const int64_t o = t * chunks + chunk;
   if (threadIdx.x == 0) p.part[o] = make_float4(s.m, s.l, s.w, __int_as_float(before));
-  if constexpr (TOP) {
-    place_keys(list, count, p.top, [&](int place, uint64_t key) { p.part_top[o * p.top + place] = key; });
-    for (int i = count + threadIdx.x; i < p.top; i += kThreads) p.part_top[o * p.top + i] = 0;
+  place([&](int place, uint64_t key) { p.part_top[o * p.top + place] = key; });
+  for (int i = count + threadIdx.x; i < p.top; i += kThreads) p.part_top[o * p.top + i] = 0;
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(kThreads) void logprobs_chunk_kernel(const Logprobs p, int chunks) {
+  extern __shared__ __align__(16) uint64_t list[];      // [waves][kPer * top]
+  __shared__ ChunkShared sh;
+  const int64_t t = blockIdx.x / chunks;
+  const int chunk = (int)(blockIdx.x - t * chunks);
+  if ((chunk + 1) * kLpChunk <= p.V)
+    chunk_of_row<BF16, true>(p, t, chunk, chunks, list, sh);
+  else
+    chunk_of_row<BF16, false>(p, t, chunk, chunks, list, sh);
+}
+
+// Without alternatives: a workgroup goes over `per` consecutive chunks of a row
+// with the next chunk's loads under way, and a thread keeps its own maximum and
+// sums, so the waves meet at the end only.
+template <bool BF16>
+__global__ __launch_bounds__(kThreads) void logprobs_stream_kernel(const Logprobs p, int chunks, int per, int splits) {
+  using L = Layout<BF16>;
+  __shared__ float4 wsum[kThreads / 64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = blockIdx.x / splits;
+  const int split = (int)(blockIdx.x - t * splits), begin = split * per, end = min(chunks, begin + per);
+  const char* row = reinterpret_cast<const char*>(p.logits) + t * p.stride * L::SIZE;
+  const bool few = p.V < L::VEC;      // fewer entries than an access has
+  auto load = [&](int chunk, u32x4 (&d)[L::GROUPS]) {
+    const int first = chunk * kLpChunk;
+    if (!few) load_raw<BF16, false>(row + (int64_t)first * L::SIZE, min(p.V - first, kLpChunk), d);
+  };
+  u32x4 raw[2][L::GROUPS];
+  load(begin, raw[0]);
+  const int y = p.targets[t];
+  const bool token = y >= 0 && y < p.V;
+  const float xy = token ? number<BF16>(row, y) : __builtin_inff();
+  Sums mine{neg_inf(), 0.f, 0.f};
+  int before = 0;      // of the wave: entries that come before the token
+  auto work = [&](int chunk, const u32x4 (&now)[L::GROUPS], u32x4 (&next)[L::GROUPS]) {
+    load(min(chunk + 1, end - 1), next);
+    const int first = chunk * kLpChunk, n = min(p.V - first, kLpChunk);
+    float x[kPer];
+    if (!few) {
+      numbers_of<BF16>(now, x);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) x[i] = i < L::VEC && threadIdx.x == 0 && i < n ? number<BF16>(row, i) : neg_inf();
+    }
+    auto index = [&](int k, int i) { return (few ? L::nominal(k) : L::template at<false>(k, n)) + i; };
+    auto own = [&](int k, int i) { return index(k, i) >= L::nominal(k) && index(k, i) < n; };
+    if (n < kLpChunk) {
+#pragma unroll
+      for (int k = 0; k < L::GROUPS; ++k)
+#pragma unroll
+        for (int i = 0; i < L::VEC; ++i) x[L::VEC * k + i] = own(k, i) ? x[L::VEC * k + i] : neg_inf();
+    }
+    Sums c{x[0], 0.f, 0.f};
+#pragma unroll
+    for (int i = 1; i < kPer; ++i) c.m = max_nan(c.m, x[i]);
+    c.m = max_nan(c.m, mine.m);
+    sums_against(x, c.m, __all(fabsf(c.m) < 0x1p100f), c.l, c.w);
+    add_part(mine, c);
+    if (n == kLpChunk && (y < first || y >= first + kLpChunk)) {
+      const float least = least_before(xy, y >= first + kLpChunk);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) before += (int)__popcll(__ballot(x[i] >= least));
+    } else {
+#pragma unroll
+      for (int k = 0; k < L::GROUPS; ++k)
+#pragma unroll
+        for (int i = 0; i < L::VEC; ++i) {
+          const float v = x[L::VEC * k + i];
+          before += (int)__popcll(__ballot(v > xy || (v == xy && own(k, i) && first + index(k, i) < y)));
+        }
+    }
+  };
+  for (int chunk = begin; chunk < end; chunk += 2) {
+    work(chunk, raw[0], raw[1]);
+    if (chunk + 1 >= end) break;
+    work(chunk + 1, raw[1], raw[0]);
   }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const Sums o{__shfl_xor(mine.m, d, 64), __shfl_xor(mine.l, d, 64), __shfl_xor(mine.w, d, 64)};
+    add_part(mine, o);
+  }
+  if (lane == 0) wsum[wave] = make_float4(mine.m, mine.l, mine.w, __int_as_float(before));
+  __syncthreads();
+  if (threadIdx.x > 0) return;
+  for (int k = 1; k < kThreads / 64; ++k) {
+    add_part(mine, Sums{wsum[k].x, wsum[k].y, wsum[k].z});
+    before += __float_as_int(wsum[k].w);
+  }
+  if (splits == 1)
+    finish_row<BF16>(p, t, mine, before);
+  else
+    p.part[t * splits + split] = make_float4(mine.m, mine.l, mine.w, __int_as_float(before));
 }
 
 // A workgroup joins a row's chunks.
@@ -280,6 +468,9 @@ __global__ __launch_bounds__(kThreads) void logprobs_join_kernel(const Logprobs 
   __shared__ uint64_t bound;
   __shared__ int count;
   const int64_t t = blockIdx.x;
+  const uint64_t* from = TOP ? p.part_top + t * chunks * p.top : nullptr;
+  const int keys = TOP ? chunks * p.top : 0;
+  const uint64_t early = TOP && threadIdx.x < keys ? from[threadIdx.x] : 0;
   if (threadIdx.x < 64) {
     Sums s{neg_inf(), 0.f, 0.f};
     int before = 0;
@@ -295,99 +486,126 @@ __global__ __launch_bounds__(kThreads) void logprobs_join_kernel(const Logprobs 
     }
     before = wave_sum(before);
     if (threadIdx.x == 0) norm = finish_row<BF16>(p, t, s, before);
-  }
-  if constexpr (TOP) {
+  } else if (TOP && threadIdx.x < 128) {
     // what is worse than some chunk's last is none of the row's best
-    if (threadIdx.x == 0) {
-      bound = 1;
+    uint64_t most = 1;
+    for (int c = threadIdx.x - 64; c < chunks; c += 64) {
+      const uint64_t last = from[(int64_t)c * p.top + p.top - 1];
+      most = last > most ? last : most;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint64_t o = __shfl_xor((unsigned long long)most, d, 64);
+      most = o > most ? o : most;
+    }
+    if (threadIdx.x == 64) {
+      bound = most;
       count = 0;
     }
-    __syncthreads();
-    const uint64_t* from = p.part_top + t * chunks * p.top;
-    for (int c = threadIdx.x; c < chunks; c += kThreads)
-      atomicMax((unsigned long long*)&bound, (unsigned long long)from[(int64_t)c * p.top + p.top - 1]);
+  }
+  if constexpr (TOP) {
     __syncthreads();
     const uint64_t least = bound;
-    for (int i = threadIdx.x; i < chunks * p.top; i += kThreads) {
-      const uint64_t key = from[i];
+    for (int i = threadIdx.x; i < keys; i += kThreads) {
+      const uint64_t key = i == threadIdx.x ? early : from[i];
       if (key >= least) list[atomicAdd(&count, 1)] = key;
     }
     __syncthreads();
     const Norm o = norm;
-    place_keys(list, count, p.top, [&](int place, uint64_t key) { put_top(p, t, o, place, key); });
+    for (int i = threadIdx.x; i < count; i += kThreads) {
+      const uint64_t key = list[i];
+      const int place = keys_before(key, list, count);
+      if (place < p.top) put_top(p, t, o, place, key);
+    }
   }
 }
 
 // The gradient, a chunk of a row at a time: one read and one write of every
-// entry and an exponential between them.
-template <bool BF16>
-__global__ __launch_bounds__(kThreads) void logprobs_bwd_kernel(const Logprobs p, int chunks) {
+// entry and an exponential between them. (What two threads both hold of a cut
+// group, both write, the same.)
+template <bool BF16, bool FULL>
+__device__ __forceinline__ void gradient_of_chunk(const Logprobs& p, int64_t t, int chunk) {
   using L = Layout<BF16>;
-  const int64_t t = blockIdx.x / chunks;
-  const int chunk = (int)(blockIdx.x - t * chunks), first = chunk * kLpChunk, n = min(p.V - first, kLpChunk);
+  const int first = chunk * kLpChunk, n = FULL ? kLpChunk : p.V - first;
+  const char* from = reinterpret_cast<const char*>(p.logits) + (t * p.stride + first) * L::SIZE;
+  char* to = reinterpret_cast<char*>(p.d_logits) + (t * p.V + first) * L::SIZE;
+  const bool few = !FULL && p.V < L::VEC;      // fewer entries than an access has
   float x[kPer];
-  load_chunk<BF16>(p.logits, t * p.stride + first, n, x);
+  if (!few) {
+    load_chunk<BF16, FULL>(from, n, x);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) x[i] = i < L::VEC && threadIdx.x == 0 && i < n ? number<BF16>(from, i) : 0.f;
+  }
   const int y = p.targets[t];
   const bool token = y >= 0 && y < p.V;
   const Norm o{p.norm[2 * t], p.norm[2 * t + 1]};
   const float entropy = p.entropy[t], gl = token ? p.d_logprob[t] : 0.f, gh = p.d_entropy[t];
   const bool none = o.m == neg_inf();
-  const float shift = entropy * gh + gl;      // of p's factor
+  const float shift = fmaf(entropy, gh, gl);      // of p's factor
 #pragma unroll
-  for (int k = 0; k < L::GROUPS; ++k)
-#pragma unroll
-    for (int i = 0; i < L::VEC; ++i) {
-      float& v = x[L::VEC * k + i];
-      const float lp = (v - o.m) - o.n, e = exp2_fast(lp * kLog2e);
-      const float g = e == 0.f ? 0.f : -e * fmaf(gh, lp, shift);
-      v = none ? 0.f : g + (token && first + L::at(k) + i == y ? gl : 0.f);
-    }
-  char* base = reinterpret_cast<char*>(p.d_logits) + (t * p.V + first) * (BF16 ? 2 : 4);
-  if (n >= kLpChunk) {
-#pragma unroll
-    for (int k = 0; k < L::GROUPS; ++k) {
-      u32x4 d;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (BF16)
-          d[i] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)x[8 * k + 2 * i], (__bf16)x[8 * k + 2 * i + 1]});
-        else
-          d[i] = __float_as_uint(x[4 * k + i]);
-      }
-      if constexpr (BF16)
-        *reinterpret_cast<u32x4_by2*>(base + 2 * L::at(k)) = d;
-      else
-        *reinterpret_cast<u32x4_by4*>(base + 4 * L::at(k)) = d;
-    }
-    return;
+  for (int i = 0; i < kPer; ++i) {
+    const float lp = (x[i] - o.m) - o.n, e = exp2_fast(lp * kLog2e);
+    // (0 * -inf; a NaN stays one by e)
+    x[i] = none ? 0.f : -e * fmaf(gh, fmaxf(lp, -1000.f), shift);
   }
 #pragma unroll
-  for (int k = 0; k < L::GROUPS; ++k)
+  for (int k = 0; k < L::GROUPS; ++k) {
+    const int at = few ? L::nominal(k) : L::template at<FULL>(k, n), mine = y - first - at;
+    if (token && !none && mine >= 0 && mine < L::VEC) {
 #pragma unroll
-    for (int i = 0; i < L::VEC; ++i) {
-      const int at = L::at(k) + i;
-      if (at < n) {
-        if constexpr (BF16)
-          reinterpret_cast<__bf16*>(base)[at] = (__bf16)x[L::VEC * k + i];
-        else
-          reinterpret_cast<float*>(base)[at] = x[L::VEC * k + i];
-      }
+      for (int i = 0; i < L::VEC; ++i) x[L::VEC * k + i] += i == mine ? gl : 0.f;
     }
+    if (!FULL && L::nominal(k) >= n) continue;
+    if (few) {
+#pragma unroll
+      for (int i = 0; i < L::VEC; ++i)
+        if (i < n) {
+          if constexpr (BF16)
+            reinterpret_cast<__bf16*>(to)[i] = (__bf16)x[i];
+          else
+            reinterpret_cast<float*>(to)[i] = x[i];
+        }
+      continue;
+    }
+    u32x4 d;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (BF16)
+        d[i] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)x[8 * k + 2 * i], (__bf16)x[8 * k + 2 * i + 1]});
+      else
+        d[i] = __float_as_uint(x[4 * k + i]);
+    }
+    store16<BF16>(to + (int64_t)L::SIZE * at, d);
+  }
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(kThreads) void logprobs_bwd_kernel(const Logprobs p, int chunks) {
+  const int64_t t = blockIdx.x / chunks;
+  const int chunk = (int)(blockIdx.x - t * chunks);
+  if ((chunk + 1) * kLpChunk <= p.V)
+    gradient_of_chunk<BF16, true>(p, t, chunk);
+  else
+    gradient_of_chunk<BF16, false>(p, t, chunk);
 }
 
 template <bool BF16>
 void launch_forward(const Logprobs& p, hipStream_t stream) {
   const int chunks = (int)logprobs_chunks(p.V);
-  const dim3 grid((unsigned)(p.T * chunks)), rows((unsigned)p.T), block(kThreads);
+  const dim3 rows((unsigned)p.T), block(kThreads);
   if (p.top > 0) {
     const size_t lds = sizeof(uint64_t) * (kThreads / 64) * kPer * p.top;
-    hipLaunchKernelGGL((logprobs_chunk_kernel<BF16, true>), grid, block, lds, stream, p, chunks);
+    hipLaunchKernelGGL(logprobs_chunk_kernel<BF16>, dim3((unsigned)(p.T * chunks)), block, lds, stream, p, chunks);
     if (chunks > 1)
       hipLaunchKernelGGL((logprobs_join_kernel<BF16, true>), rows, block, sizeof(uint64_t) * chunks * p.top, stream, p, chunks);
-  } else {
-    hipLaunchKernelGGL((logprobs_chunk_kernel<BF16, false>), grid, block, 0, stream, p, chunks);
-    if (chunks > 1) hipLaunchKernelGGL((logprobs_join_kernel<BF16, false>), rows, block, 0, stream, p, chunks);
+    return;
   }
+  // few rows: a chunk per workgroup, many: a row, with eight workgroups per compute unit of a full device between them
+  const int64_t want = (2048 + p.T - 1) / p.T;
+  const int per = (int)((chunks + want - 1) / want), splits = (chunks + per - 1) / per;
+  hipLaunchKernelGGL(logprobs_stream_kernel<BF16>, dim3((unsigned)(p.T * splits)), block, 0, stream, p, chunks, per, splits);
+  if (splits > 1) hipLaunchKernelGGL((logprobs_join_kernel<BF16, false>), rows, block, 0, stream, p, splits);
 }
 
 }  // namespace
