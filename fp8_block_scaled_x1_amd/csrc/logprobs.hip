@@ -50,37 +50,52 @@ __device__ __forceinline__ float number(const void* p, int64_t i) {
 
 // Numbers of a 16-byte access, and the chunk's groups of them per thread: group
 // k of thread i begins at entry VEC * (i + kThreads * k). A group that the end
-// of the row cuts (of `n` entries, at least VEC of them in the row) is read from
-// VEC before the end: its first entries are the group before's.
+// of the row cuts (the chunk has `n` entries) is read from
+// VEC before the end: its first entries are the group before's. A chunk of fewer
+// than VEC entries is read entry by entry, by every thread.
 template <bool BF16>
 struct Layout {
   static constexpr int VEC = BF16 ? 8 : 4, GROUPS = kPer / VEC, SIZE = BF16 ? 2 : 4;
   __device__ __forceinline__ static int nominal(int k) { return VEC * ((int)threadIdx.x + kThreads * k); }
-  template <bool FULL>
-  __device__ __forceinline__ static int at(int k, int n) { return FULL ? nominal(k) : min(nominal(k), n - VEC); }
+  __device__ __forceinline__ static int at(int k, int n) { return n < VEC ? nominal(k) : min(nominal(k), n - VEC); }
 };
-
 template <bool BF16>
-__device__ __forceinline__ u32x4 load16(const char* p) {
+__device__ __forceinline__ u32x4 load16(const void* p) {
   if constexpr (BF16)
     return *reinterpret_cast<const u32x4_by2*>(p);
   else
     return *reinterpret_cast<const u32x4_by4*>(p);
 }
+
 template <bool BF16>
-__device__ __forceinline__ void store16(char* p, u32x4 d) {
+__device__ __forceinline__ void store16(void* p, u32x4 d) {
   if constexpr (BF16)
     *reinterpret_cast<u32x4_by2*>(p) = d;
   else
     *reinterpret_cast<u32x4_by4*>(p) = d;
 }
 
-// The thread's entries of a chunk at `base`.
-template <bool BF16, bool FULL>
+// The thread's groups of a chunk of `n` entries at `base`, as they are in memory
+// (entries that a row does not have: anything).
+template <bool BF16>
 __device__ __forceinline__ void load_raw(const char* base, int n, u32x4 (&d)[Layout<BF16>::GROUPS]) {
   using L = Layout<BF16>;
+  if (n >= L::VEC) {
 #pragma unroll
-  for (int k = 0; k < L::GROUPS; ++k) d[k] = load16<BF16>(base + (int64_t)L::SIZE * L::template at<FULL>(k, n));
+    for (int k = 0; k < L::GROUPS; ++k) d[k] = load16<BF16>(base + (int64_t)L::SIZE * L::at(k, n));
+  } else {
+    d[0] = u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < L::VEC; ++i) {
+      const uint32_t bits = __float_as_uint(number<BF16>(base, min(i, n - 1)));
+      if constexpr (BF16)
+        d[0][i / 2] |= i & 1 ? bits : bits >> 16;
+      else
+        d[0][i] = bits;
+    }
+#pragma unroll
+    for (int k = 1; k < L::GROUPS; ++k) d[k] = d[0];
+  }
 }
 template <bool BF16>
 __device__ __forceinline__ void numbers_of(const u32x4 (&d)[Layout<BF16>::GROUPS], float (&x)[kPer]) {
@@ -88,20 +103,25 @@ __device__ __forceinline__ void numbers_of(const u32x4 (&d)[Layout<BF16>::GROUPS
 #pragma unroll
   for (int k = 0; k < L::GROUPS; ++k)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (BF16) {
-        x[8 * k + 2 * i] = __uint_as_float(d[k][i] << 16);
-        x[8 * k + 2 * i + 1] = __uint_as_float(d[k][i] & 0xFFFF0000u);
-      } else {
+    for (int i = 0; i < L::VEC; ++i) {
+      if constexpr (BF16)
+        x[8 * k + i] = __uint_as_float(i & 1 ? d[k][i / 2] & 0xFFFF0000u : d[k][i / 2] << 16);
+      else
         x[4 * k + i] = __uint_as_float(d[k][i]);
-      }
     }
 }
-template <bool BF16, bool FULL>
-__device__ __forceinline__ void load_chunk(const char* base, int n, float (&x)[kPer]) {
-  u32x4 d[Layout<BF16>::GROUPS];
-  load_raw<BF16, FULL>(base, n, d);
+// As numbers, and -inf for what is not the thread's own.
+template <bool BF16>
+__device__ __forceinline__ void entries_of(const u32x4 (&d)[Layout<BF16>::GROUPS], int n, float (&x)[kPer]) {
+  using L = Layout<BF16>;
   numbers_of<BF16>(d, x);
+  if (n == kLpChunk) return;
+#pragma unroll
+  for (int k = 0; k < L::GROUPS; ++k) {
+    const int at = L::at(k, n), from = L::nominal(k) - at, to = n - at;
+#pragma unroll
+    for (int i = 0; i < L::VEC; ++i) x[L::VEC * k + i] = i >= from && i < to ? x[L::VEC * k + i] : neg_inf();
+  }
 }
 
 // Ascending with the value, -0 as 0.
@@ -177,11 +197,33 @@ __device__ __forceinline__ void sums_against(const float (&x)[kPer], float m, bo
   }
 }
 
-// Entries of a chunk that all lie ahead of the token, or all behind it, come
-// before it if they reach this: its value, or the next larger one (0 and -0 are equal).
-__device__ __forceinline__ float least_before(float xy, bool ahead) {
+// Of `n` entries from `first` on, as entries_of gave them: how many of the
+// wave's come before the token y with logit xy. They do if they reach a bound:
+// xy itself ahead of the token, the next larger value behind it (0 and -0 are equal).
+template <bool BF16>
+__device__ __forceinline__ int count_before(const float (&x)[kPer], int first, int n, int y, float xy) {
+  using L = Layout<BF16>;
   const uint32_t u = __float_as_uint(xy + 0.f);
-  return ahead ? xy : __uint_as_float(u == 0 ? 1u : (u >> 31) ? u - 1u : u + 1u);
+  const float larger = __uint_as_float(u == 0 ? 1u : (u >> 31) ? u - 1u : u + 1u);
+  int before = 0;
+  if (y < first || y >= first + kLpChunk) {
+    const float least = y < first ? larger : xy;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) before += (int)__popcll(__ballot(x[i] >= least));
+  } else {
+#pragma unroll
+    for (int k = 0; k < L::GROUPS; ++k) {
+      const int ahead = y - first - L::at(k, n);
+#pragma unroll
+      for (int i = 0; i < L::VEC; ++i) before += (int)__popcll(__ballot(x[L::VEC * k + i] >= (i < ahead ? xy : larger)));
+    }
+  }
+  if (xy == neg_inf() && n < kLpChunk && n >= L::VEC) {      // what a cut group holds of another's reached it as -inf
+    int other = 0;
+    for (int k = 0; k < L::GROUPS; ++k) other += max(0, min(min(L::nominal(k) - L::at(k, n), y - first - L::at(k, n)), (int)L::VEC));
+    before -= wave_sum(other);
+  }
+  return before;
 }
 
 // What the log probability of a logit x is taken against: (x - m) - n.
@@ -219,118 +261,99 @@ __device__ __forceinline__ void put_top(const Logprobs& p, int64_t t, const Norm
   p.top_logprobs[t * p.top + place] = logprob_of(o, value_of((uint32_t)(key >> 32)));
 }
 
-struct ChunkShared {
-  float wmax[kThreads / 64];
-  uint32_t wbound[kThreads / 64];
-  float4 wsum[kThreads / 64];
-  Norm norm;
-  int count[kThreads / 64], overflow;
-};
-
-// With alternatives: a workgroup has one chunk of a row.
-template <bool BF16, bool FULL>
-__device__ __forceinline__ void chunk_of_row(const Logprobs& p, int64_t t, int chunk, int chunks, uint64_t* list, ChunkShared& sh) {
+// With alternatives: a workgroup has one chunk of a row. The code is kept short
+// (what is rare reads the chunk again in loops): with 53 KB of it, all unrolled,
+// fetching it once cold took most of a call's time, 546 rows of 12943 67 us.
+template <bool BF16>
+__global__ __launch_bounds__(kThreads) void logprobs_chunk_kernel(const Logprobs p, int chunks) {
   using L = Layout<BF16>;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int first = chunk * kLpChunk, n = FULL ? kLpChunk : p.V - first;
+  extern __shared__ __align__(16) uint64_t list[];      // [waves][kPer * top]
+  __shared__ float wmax[kThreads / 64];
+  __shared__ uint32_t wbound[kThreads / 64];
+  __shared__ float4 wsum[kThreads / 64];
+  __shared__ int wcount[kThreads / 64], overflow;
+  __shared__ Norm norm;
+  const int64_t t = blockIdx.x / chunks;
+  const int chunk = (int)(blockIdx.x - t * chunks), lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int first = chunk * kLpChunk, n = min(p.V - first, kLpChunk);
   const int y = p.targets[t];
   const bool token = y >= 0 && y < p.V;
-  float x[kPer];
   const char* base = reinterpret_cast<const char*>(p.logits) + (t * p.stride + first) * L::SIZE;
-  if (FULL || p.V >= L::VEC) {
-    load_chunk<BF16, FULL>(base, n, x);
-  } else {      // fewer entries than an access has
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) x[i] = i < L::VEC && threadIdx.x == 0 && i < n ? number<BF16>(base, i) : neg_inf();
-  }
+  u32x4 raw[L::GROUPS];
+  load_raw<BF16>(base, n, raw);
   const float xy = token ? number<BF16>(p.logits, t * p.stride + y) : __builtin_inff();
-  // index in the chunk of entry i of group k, and whether it is the thread's
-  auto index = [&](int k, int i) { return (FULL || p.V >= L::VEC ? L::template at<FULL>(k, n) : L::nominal(k)) + i; };
-  auto own = [&](int k, int i) { return FULL || (index(k, i) >= L::nominal(k) && index(k, i) < n); };
-  if constexpr (!FULL) {
-#pragma unroll
-    for (int k = 0; k < L::GROUPS; ++k)
-#pragma unroll
-      for (int i = 0; i < L::VEC; ++i) x[L::VEC * k + i] = own(k, i) ? x[L::VEC * k + i] : neg_inf();
-  }
+  float x[kPer];
+  entries_of<BF16>(raw, n, x);
 
   float mine = x[0];
 #pragma unroll
   for (int i = 1; i < kPer; ++i) mine = max_nan(mine, x[i]);
   float m = wave_max_nan(mine);
-  const uint32_t best = order_of(mine);
-  uint32_t bound = nth_value(best, p.top);
+  uint32_t bound = nth_value(order_of(mine), p.top);
   if (lane == 0) {
-    sh.wmax[wave] = m;
-    sh.wbound[wave] = bound;
+    wmax[wave] = m;
+    wbound[wave] = bound;
   }
-  if (threadIdx.x == 0) sh.overflow = 0;
+  if (threadIdx.x == 0) overflow = 0;
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < kThreads / 64; ++k) {
-    m = max_nan(m, sh.wmax[k]);
-    bound = max(bound, sh.wbound[k]);
+    m = max_nan(m, wmax[k]);
+    bound = max(bound, wbound[k]);
   }
 
   float l, w;
   sums_against(x, m, fabsf(m) < 0x1p100f, l, w);
   l = wave_sum(l);
   w = wave_sum(w);
-  int before = 0;      // of the wave: entries that come before the token
-  if (FULL && (y < first || y >= first + kLpChunk)) {
-    const float least = least_before(xy, y >= first + kLpChunk);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) before += (int)__popcll(__ballot(x[i] >= least));
-  } else {
-#pragma unroll
-    for (int k = 0; k < L::GROUPS; ++k)
-#pragma unroll
-      for (int i = 0; i < L::VEC; ++i) {
-        const float v = x[L::VEC * k + i];
-        before += (int)__popcll(__ballot(v > xy || (v == xy && own(k, i) && first + index(k, i) < y)));
-      }
-  }
-  if (lane == 0) sh.wsum[wave] = make_float4(l, w, __int_as_float(before), 0.f);
+  int before = count_before<BF16>(x, first, n, y, xy);
+  if (lane == 0) wsum[wave] = make_float4(l, w, __int_as_float(before), 0.f);
 
-  // The wave's entries that `reaches`(k, i) names, to its part of the list.
+  // Candidates of the wave, to its part of the list: entry and index, then keys.
   uint64_t* const own_list = list + wave * kPer * p.top;
-  auto put = [&](int most, auto&& reaches) {
-    int at = 0;
+  const float least = value_of(bound);
+  const int few = min(2 * p.top + 32, kPer * p.top);
+  int at = 0;
+  if (least > neg_inf()) {      // else too many may reach it, or it is a NaN
 #pragma unroll
-    for (int k = 0; k < L::GROUPS; ++k)
+    for (int k = 0; k < L::GROUPS; ++k) {
+      const int index = first + L::at(k, n);
 #pragma unroll
       for (int i = 0; i < L::VEC; ++i) {
-        const bool mine = reaches(k, i);
-        const uint64_t all = __ballot(mine);
+        const bool reaches = !(x[L::VEC * k + i] < least);
+        const uint64_t all = __ballot(reaches);
         if (all == 0) continue;
         const int slot = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0));
-        if (mine && slot < most) own_list[slot] = key_of(x[L::VEC * k + i], first + index(k, i));
+        if (reaches && slot < few) own_list[slot] = ((uint64_t)(uint32_t)(index + i) << 32) | __float_as_uint(x[L::VEC * k + i]);
         at += (int)__popcll(all);
       }
-    if (lane == 0) sh.count[wave] = at;
-    if (at > most) sh.overflow = 1;
-  };
-  const int few = min(2 * p.top + 32, kPer * p.top);
-  if (__any(best >= bound)) {
-    const float least = value_of(bound);
-    put(few, [&](int k, int i) { return !(x[L::VEC * k + i] < least) && own(k, i); });
-  } else if (lane == 0) {
-    sh.count[wave] = 0;
+    }
+    __builtin_amdgcn_wave_barrier();      // (a wave's LDS accesses keep their order)
+    for (int i = lane; i < min(at, few); i += 64)
+      own_list[i] = key_of(__uint_as_float((uint32_t)own_list[i]), (int)(own_list[i] >> 32));
   }
+  if (lane == 0) wcount[wave] = at;
+  if (at > few || !(least > neg_inf())) overflow = 1;
   __syncthreads();
-  if (sh.overflow) {      // the same for all
-    __syncthreads();
+  if (overflow) {      // the same for all; the thread's entries now lie kThreads apart
+    auto key_at = [&](int i) { return i < n ? key_of(number<BF16>(base, i), first + i) : (uint64_t)0; };
     uint64_t best = 0;
-#pragma unroll
-    for (int k = 0; k < L::GROUPS; ++k)
-#pragma unroll
-      for (int i = 0; i < L::VEC; ++i) {
-        const uint64_t key = own(k, i) ? key_of(x[L::VEC * k + i], first + index(k, i)) : 0;
-        best = key > best ? key : best;
-      }
+#pragma unroll 8
+    for (int j = 0; j < kPer; ++j) {
+      const uint64_t key = key_at(threadIdx.x + kThreads * j);
+      best = key > best ? key : best;
+    }
     const uint32_t hi = (uint32_t)(best >> 32), lo = (uint32_t)best, h = nth_value(hi, p.top);
-    const uint64_t bound = ((uint64_t)h << 32) | nth_value(lo, p.top, hi == h, (int)__popcll(__ballot(hi > h)));
-    put(kPer * p.top, [&](int k, int i) { return own(k, i) && key_of(x[L::VEC * k + i], first + index(k, i)) >= bound; });
+    const uint64_t bound = max(((uint64_t)h << 32) | nth_value(lo, p.top, hi == h, (int)__popcll(__ballot(hi > h))), (uint64_t)1);
+    at = 0;
+#pragma unroll 8
+    for (int j = 0; j < kPer; ++j) {
+      const uint64_t key = key_at(threadIdx.x + kThreads * j), all = __ballot(key >= bound);
+      const int slot = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0));
+      if (key >= bound) own_list[slot] = key;      // at most `top` lanes of the wave reach it
+      at += (int)__popcll(all);
+    }
+    if (lane == 0) wcount[wave] = at;
     __syncthreads();
   }
   Sums s{m, 0.f, 0.f};
@@ -338,42 +361,31 @@ __device__ __forceinline__ void chunk_of_row(const Logprobs& p, int64_t t, int c
   before = 0;
 #pragma unroll
   for (int k = 0; k < kThreads / 64; ++k) {
-    count += sh.count[k];
-    s.l += sh.wsum[k].x;
-    s.w += sh.wsum[k].y;
-    before += __float_as_int(sh.wsum[k].z);
-  }
-  auto place = [&](auto&& to) {
-    for (int i = lane; i < sh.count[wave]; i += 64) {
-      const uint64_t key = own_list[i];
-      int before = 0;
-      for (int k = 0; k < kThreads / 64; ++k) before += keys_before(key, list + k * kPer * p.top, sh.count[k]);
-      if (before < p.top) to(before, key);
-    }
-  };
-  if (chunks == 1) {
-    if (threadIdx.x == 0) sh.norm = finish_row<BF16>(p, t, s, before);
-    __syncthreads();
-    const Norm o = sh.norm;
-    place([&](int place, uint64_t key) { put_top(p, t, o, place, key); });
-    return;
+    count += wcount[k];
+    s.l += wsum[k].x;
+    s.w += wsum[k].y;
+    before += __float_as_int(wsum[k].z);
   }
   const int64_t o = t * chunks + chunk;
-  if (threadIdx.x == 0) p.part[o] = make_float4(s.m, s.l, s.w, __int_as_float(before));
-  place([&](int place, uint64_t key) { p.part_top[o * p.top + place] = key; });
-  for (int i = count + threadIdx.x; i < p.top; i += kThreads) p.part_top[o * p.top + i] = 0;
-}
-
-template <bool BF16>
-__global__ __launch_bounds__(kThreads) void logprobs_chunk_kernel(const Logprobs p, int chunks) {
-  extern __shared__ __align__(16) uint64_t list[];      // [waves][kPer * top]
-  __shared__ ChunkShared sh;
-  const int64_t t = blockIdx.x / chunks;
-  const int chunk = (int)(blockIdx.x - t * chunks);
-  if ((chunk + 1) * kLpChunk <= p.V)
-    chunk_of_row<BF16, true>(p, t, chunk, chunks, list, sh);
-  else
-    chunk_of_row<BF16, false>(p, t, chunk, chunks, list, sh);
+  if (threadIdx.x == 0) {
+    if (chunks == 1)
+      norm = finish_row<BF16>(p, t, s, before);
+    else
+      p.part[o] = make_float4(s.m, s.l, s.w, __int_as_float(before));
+  }
+  if (chunks == 1) __syncthreads();
+  for (int i = lane; i < wcount[wave]; i += 64) {
+    const uint64_t key = own_list[i];
+    int place = 0;
+    for (int k = 0; k < kThreads / 64; ++k) place += keys_before(key, list + k * kPer * p.top, wcount[k]);
+    if (place >= p.top) continue;
+    if (chunks == 1)
+      put_top(p, t, norm, place, key);
+    else
+      p.part_top[o * p.top + place] = key;
+  }
+  if (chunks > 1)
+    for (int i = count + threadIdx.x; i < p.top; i += kThreads) p.part_top[o * p.top + i] = 0;
 }
 
 // Without alternatives: a workgroup goes over `per` consecutive chunks of a row
@@ -387,10 +399,9 @@ __global__ __launch_bounds__(kThreads) void logprobs_stream_kernel(const Logprob
   const int64_t t = blockIdx.x / splits;
   const int split = (int)(blockIdx.x - t * splits), begin = split * per, end = min(chunks, begin + per);
   const char* row = reinterpret_cast<const char*>(p.logits) + t * p.stride * L::SIZE;
-  const bool few = p.V < L::VEC;      // fewer entries than an access has
   auto load = [&](int chunk, u32x4 (&d)[L::GROUPS]) {
     const int first = chunk * kLpChunk;
-    if (!few) load_raw<BF16, false>(row + (int64_t)first * L::SIZE, min(p.V - first, kLpChunk), d);
+    load_raw<BF16>(row + (int64_t)first * L::SIZE, min(p.V - first, kLpChunk), d);
   };
   u32x4 raw[2][L::GROUPS];
   load(begin, raw[0]);
@@ -403,39 +414,14 @@ __global__ __launch_bounds__(kThreads) void logprobs_stream_kernel(const Logprob
     load(min(chunk + 1, end - 1), next);
     const int first = chunk * kLpChunk, n = min(p.V - first, kLpChunk);
     float x[kPer];
-    if (!few) {
-      numbers_of<BF16>(now, x);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) x[i] = i < L::VEC && threadIdx.x == 0 && i < n ? number<BF16>(row, i) : neg_inf();
-    }
-    auto index = [&](int k, int i) { return (few ? L::nominal(k) : L::template at<false>(k, n)) + i; };
-    auto own = [&](int k, int i) { return index(k, i) >= L::nominal(k) && index(k, i) < n; };
-    if (n < kLpChunk) {
-#pragma unroll
-      for (int k = 0; k < L::GROUPS; ++k)
-#pragma unroll
-        for (int i = 0; i < L::VEC; ++i) x[L::VEC * k + i] = own(k, i) ? x[L::VEC * k + i] : neg_inf();
-    }
+    entries_of<BF16>(now, n, x);
     Sums c{x[0], 0.f, 0.f};
 #pragma unroll
     for (int i = 1; i < kPer; ++i) c.m = max_nan(c.m, x[i]);
     c.m = max_nan(c.m, mine.m);
     sums_against(x, c.m, __all(fabsf(c.m) < 0x1p100f), c.l, c.w);
     add_part(mine, c);
-    if (n == kLpChunk && (y < first || y >= first + kLpChunk)) {
-      const float least = least_before(xy, y >= first + kLpChunk);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) before += (int)__popcll(__ballot(x[i] >= least));
-    } else {
-#pragma unroll
-      for (int k = 0; k < L::GROUPS; ++k)
-#pragma unroll
-        for (int i = 0; i < L::VEC; ++i) {
-          const float v = x[L::VEC * k + i];
-          before += (int)__popcll(__ballot(v > xy || (v == xy && own(k, i) && first + index(k, i) < y)));
-        }
-    }
+    before += count_before<BF16>(x, first, n, y, xy);
   };
   for (int chunk = begin; chunk < end; chunk += 2) {
     work(chunk, raw[0], raw[1]);
@@ -523,26 +509,22 @@ __global__ __launch_bounds__(kThreads) void logprobs_join_kernel(const Logprobs 
 // The gradient, a chunk of a row at a time: one read and one write of every
 // entry and an exponential between them. (What two threads both hold of a cut
 // group, both write, the same.)
-template <bool BF16, bool FULL>
-__device__ __forceinline__ void gradient_of_chunk(const Logprobs& p, int64_t t, int chunk) {
+template <bool BF16>
+__global__ __launch_bounds__(kThreads) void logprobs_bwd_kernel(const Logprobs p, int chunks) {
   using L = Layout<BF16>;
-  const int first = chunk * kLpChunk, n = FULL ? kLpChunk : p.V - first;
-  const char* from = reinterpret_cast<const char*>(p.logits) + (t * p.stride + first) * L::SIZE;
+  const int64_t t = blockIdx.x / chunks;
+  const int first = (int)(blockIdx.x - t * chunks) * kLpChunk, n = min(p.V - first, kLpChunk);
+  u32x4 raw[L::GROUPS];
+  load_raw<BF16>(reinterpret_cast<const char*>(p.logits) + (t * p.stride + first) * L::SIZE, n, raw);
   char* to = reinterpret_cast<char*>(p.d_logits) + (t * p.V + first) * L::SIZE;
-  const bool few = !FULL && p.V < L::VEC;      // fewer entries than an access has
-  float x[kPer];
-  if (!few) {
-    load_chunk<BF16, FULL>(from, n, x);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) x[i] = i < L::VEC && threadIdx.x == 0 && i < n ? number<BF16>(from, i) : 0.f;
-  }
   const int y = p.targets[t];
   const bool token = y >= 0 && y < p.V;
   const Norm o{p.norm[2 * t], p.norm[2 * t + 1]};
   const float entropy = p.entropy[t], gl = token ? p.d_logprob[t] : 0.f, gh = p.d_entropy[t];
   const bool none = o.m == neg_inf();
   const float shift = fmaf(entropy, gh, gl);      // of p's factor
+  float x[kPer];
+  numbers_of<BF16>(raw, x);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const float lp = (x[i] - o.m) - o.n, e = exp2_fast(lp * kLog2e);
@@ -551,13 +533,13 @@ __device__ __forceinline__ void gradient_of_chunk(const Logprobs& p, int64_t t, 
   }
 #pragma unroll
   for (int k = 0; k < L::GROUPS; ++k) {
-    const int at = few ? L::nominal(k) : L::template at<FULL>(k, n), mine = y - first - at;
+    const int at = L::at(k, n), mine = y - first - at;
     if (token && !none && mine >= 0 && mine < L::VEC) {
 #pragma unroll
       for (int i = 0; i < L::VEC; ++i) x[L::VEC * k + i] += i == mine ? gl : 0.f;
     }
-    if (!FULL && L::nominal(k) >= n) continue;
-    if (few) {
+    if (L::nominal(k) >= n) continue;
+    if (n < L::VEC) {
 #pragma unroll
       for (int i = 0; i < L::VEC; ++i)
         if (i < n) {
@@ -578,16 +560,6 @@ __device__ __forceinline__ void gradient_of_chunk(const Logprobs& p, int64_t t, 
     }
     store16<BF16>(to + (int64_t)L::SIZE * at, d);
   }
-}
-
-template <bool BF16>
-__global__ __launch_bounds__(kThreads) void logprobs_bwd_kernel(const Logprobs p, int chunks) {
-  const int64_t t = blockIdx.x / chunks;
-  const int chunk = (int)(blockIdx.x - t * chunks);
-  if ((chunk + 1) * kLpChunk <= p.V)
-    gradient_of_chunk<BF16, true>(p, t, chunk);
-  else
-    gradient_of_chunk<BF16, false>(p, t, chunk);
 }
 
 template <bool BF16>
