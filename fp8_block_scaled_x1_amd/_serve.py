@@ -12,6 +12,8 @@ A paged cache is a tensor BF16 [pages][page][576], or a triple: FP8 (codes uint8
 [..][256], scales uint8 [..][16], rope bf16 [..][64]).
 """
 
+import functools
+
 import torch
 
 from . import _attn, _lib
@@ -36,6 +38,9 @@ _SIGNATURES = {
 }
 
 _serve = None
+
+# where sizes alone give the answer
+_known_bytes = functools.lru_cache(maxsize=4096)(_bytes)
 
 
 def serve_lib():
@@ -184,7 +189,7 @@ def fp8bs_moe_tokens(x, topk_ids, weights, w_up, s_up, w_down, s_down):
             _ptr(s_up, "s_up", _f32, (E, F // 64, K // 128), device), _ptr(w_down, "w_down", _u8, (E, K, F), device),
             _ptr(s_down, "s_down", _f32, (E, K // 128, F // 128), device), E, F)
     out = torch.empty((T, K), dtype=_bf16, device=device)
-    ws = _workspace(_bytes("fp8bs_moe_tokens_workspace_bytes", T, topk, K, F), device)
+    ws = _workspace(_known_bytes("fp8bs_moe_tokens_workspace_bytes", T, topk, K, F), device)
     _call("fp8bs_moe_tokens", device, *args, out.data_ptr(), ws.data_ptr())
     return out
 
@@ -213,7 +218,7 @@ def fp8bs_logprobs(logits, targets, top=0):
     logprob, entropy = torch.empty((2, T), dtype=_f32, device=device).unbind(0)
     norm = torch.empty((T, 2), dtype=_f32, device=device)
     rank = torch.empty((T,), dtype=_i32, device=device)
-    need = _bytes("fp8bs_logprobs_workspace_bytes", T, V, top)
+    need = _known_bytes("fp8bs_logprobs_workspace_bytes", T, V, top)
     top_ids = torch.empty((T, top), dtype=_i32, device=device)
     top_logprobs = torch.empty((T, top), dtype=_f32, device=device)
     ws = _workspace(need, device)
