@@ -7,13 +7,23 @@
 // rows' queries. A lane is a token and a quarter of its groups: it loads its
 // codes from global memory (400 bytes a token, three tiles ahead, in
 // registers), and the converter turns 8 codes and their group's power of two
-// into an exact BF16 operand. Conversions run at a quarter of the rate of other
-// vector instructions, so an operand is formed once: it goes to the score
+// into an exact BF16 operand. An operand is formed once: it goes to the score
 // product and, as it is, to the tile's place in LDS, which the value product
-// reads transposed. Values: a wave adds all 64 tokens into its 128 columns.
-// Tiles alternate between two places, so a tile's values and the next tile's
-// scores are formed together and the waves meet once a tile; conversions,
-// matrix instructions and LDS fill each other's waits.
+// reads transposed (converted a second time for the values, in another layout,
+// the registers spilled and 128 rows of 128 requests took 946 us). Values: a
+// wave adds all 64 tokens into its 128 columns. Tiles alternate between two
+// places, so a tile's values and the next tile's scores are formed together and
+// the waves meet once a tile; conversions, matrix instructions and LDS fill
+// each other's waits.
+//
+// Bound: a tile takes 3800 clocks, of which the matrix units need 1088, the
+// address unit 1790 and LDS 1460; with one wave on a SIMD the rest is their
+// waits for each other. 128 rows of 128 requests of 300 to 4500 tokens 162 us
+// (505 TFLOP/s), 32 rows of 8 requests of 41000 to 67000 71 us (2.5 TB/s, 433
+// TFLOP/s), 32 rows of 192 requests behind a prefix of 16000 341 us (643
+// TFLOP/s). Not kept: codes through LDS by direct loads (as fast, more code) and
+// loads by whole rows, which take a third of the address unit's time, with the
+// quarters exchanged between lanes (the prefix's call 402 us).
 //
 // Roundings below 32 bits: the weights to BF16 for the matrix unit (2^-9
 // relative, on the terms of a mean) and the output.
@@ -31,7 +41,7 @@ namespace {
 constexpr int kTile = kFp4Tile, kWaves = 4, kWaveTokens = kTile / kWaves;
 static_assert(kTile == 64 && kWaveTokens == 16, "a wave's tokens are the rows of a 16x16x32 product");
 constexpr int kLatent = 512, kKey = 576;
-constexpr int kAhead = 3;                                  // tiles in registers
+constexpr int kAhead = 3;                                  // tiles in registers: a load from memory takes two tiles' time
 constexpr int kRowBytes = 2 * kLatent;
 // A tile in LDS: latent numbers, weights (as the value product's operand), row maxima and wishes of the waves.
 constexpr int kWeightsAt = kTile * kRowBytes, kStatAt = kWeightsAt + kTile * 32 * 2;

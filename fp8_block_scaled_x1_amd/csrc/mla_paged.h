@@ -253,7 +253,8 @@ void launch_mla_join(const MlaDecode& own, const MlaDecode& head, bool behind_pr
   // per row: 512 rows of one request 33.5 and 36.4 us, 768 of one 38.0 and 37.4,
   // 1024 of one 43.4 and 38.2, of 8 requests 48.2 and 46.8; 16384 rows 178 and
   // 156. Behind a prefix of 8000, of 32 requests 512 rows 50.7 and 60.0, 1024 of
-  // 64 65.9 and 66.7, 2048 of 128 93.1 and 92.2.
+  // 64 65.9 and 66.7, 2048 of 128 93.1 and 92.2. Over the 4-bit cache: 128 rows of
+  // one request 28.2 and 33.7, 768 of 6 39.1 and 38.3, 16384 283 and 264.
   if (own.all_rows <= (behind_prefix ? 2048 : 512))
     hipLaunchKernelGGL((mla_join_kernel<4, TILE>), dim3((unsigned)own.all_rows), dim3(kJoinThreads), 0, stream, own, head);
   else

@@ -15,15 +15,24 @@
 //
 // up: a workgroup is 16 columns of h of one expert (16 rows of G and of U), its
 // waves share the inner dimension and add their sums through LDS. down: a
-// workgroup is 32 columns of the output for all tokens and a share of the
-// (expert, 128 wide piece) pairs, which its waves share in turn; a token that
-// an expert was not chosen by adds nothing. The last workgroup of the same
-// columns to be done adds the shares' sums, in order: which one that is depends
-// on chance, the result does not.
+// workgroup is 32 columns of the output and a share of the (expert, 128 wide
+// piece) pairs, which its waves share in turn; an expert's sums go to its
+// tokens' places in the wave's LDS when the wave is done with it. Both kernels
+// work on an expert's own tokens, packed: with a place for each of 64 tokens
+// instead, and zeros added to those that did not choose the expert, the
+// registers spilled and reading h took longer than reading weights (64 tokens,
+// 4 of 32 experts each, 540 us, now 271). A third launch adds the shares' sums,
+// in order, where there are several (added by the last workgroup to be done
+// instead, the fences at device scope cost 50 us).
 //
 // Which experts are chosen is found by every workgroup from the ids (at most
 // 4096 of them): a bitmap in LDS, and a lane per token that looks for the
 // workgroup's expert among its token's ids. An id outside [0, E) sets no bit.
+//
+// Bound: memory. 8 of 32 experts of 7168 x 2048 for one token 71 us (352 MB, 5.0
+// TB/s), 32 tokens on all 32 of them 272 us (1410 MB, 5.2 TB/s). Small layers:
+// launches and a workgroup's start, 5 tokens on 13 of 32 experts of 2048 x 1408
+// 35 us (113 MB, 3.1 TB/s).
 
 #include "attn_common.h"
 #include "serve_internal.h"
@@ -33,10 +42,10 @@ namespace fp8bs {
 namespace {
 
 constexpr int kPiece = 128;       // inner numbers that share a scale
-constexpr int kMaxTiles = kMoeMaxTokens / 16;
 constexpr int kUpWaves = 4, kDownWaves = 8, kJoinThreads = 256;
 constexpr int kDeep = 4;          // pieces of weights under way
 constexpr int kStripBytes = 32 * kPiece;
+constexpr int kSumStride = 36;    // of a token's 32 sums
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
@@ -45,32 +54,49 @@ __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
 }
 __device__ __forceinline__ f32x4 zero4() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
 
+// Tokens of an expert that are worked on together. One that more than these
+// chose is listed a second time (T <= 64), for the rest of them.
+constexpr int kGroup = 32;
+
 // Bytes of the routing, a multiple of 16.
 __host__ __device__ __forceinline__ int routing_bytes_of(const MoeTokens& m) {
-  return (kMoeMaxExperts / 32 + m.T * m.topk + 3) / 4 * 16;
+  return ((m.T > kGroup ? kMoeMaxExperts : 0) + kMoeMaxExperts / 16 + m.T * m.topk + 3) / 4 * 16;
 }
+// Listed pairs of an expert and a group of its tokens, at most.
+__host__ __device__ __forceinline__ int most_listed(const MoeTokens& m) {
+  const int slots = m.T * m.topk;
+  return m.E + (m.T > kGroup ? slots / (kGroup + 1) : 0) < slots ? m.E + (m.T > kGroup ? slots / (kGroup + 1) : 0) : slots;
+}
+constexpr int kMostListed = kMoeMaxExperts + kMoeMaxTokens * kMoeMaxTopk / (kGroup + 1);
 
-// The ids of all slots and a bit per chosen expert, in LDS.
+// The ids of all slots, a bit per chosen expert and one per expert in more
+// than kGroup slots, in LDS.
 struct Routing {
-  uint32_t* bits;
+  uint32_t* bits;      // [2][kMoeMaxExperts / 32]
   int32_t* ids;
   __device__ __forceinline__ Routing(const MoeTokens& m, char* lds, int threads)
-      : bits(reinterpret_cast<uint32_t*>(lds)), ids(reinterpret_cast<int32_t*>(lds) + kMoeMaxExperts / 32) {
-    if (threadIdx.x < kMoeMaxExperts / 32) bits[threadIdx.x] = 0;
+      : bits(reinterpret_cast<uint32_t*>(lds)), ids(reinterpret_cast<int32_t*>(lds) + kMoeMaxExperts / 16) {
+    int32_t* const slots = ids + m.T * m.topk;      // of an expert
+    if (threadIdx.x < kMoeMaxExperts / 16) bits[threadIdx.x] = 0;
+    if (m.T > kGroup)
+      for (int i = threadIdx.x; i < m.E; i += threads) slots[i] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < m.T * m.topk; i += threads) {
       const int e = m.ids[i];
       ids[i] = e;
-      if (e >= 0 && e < m.E) atomicOr(&bits[e >> 5], 1u << (e & 31));
+      if (e >= 0 && e < m.E) {
+        atomicOr(&bits[e >> 5], 1u << (e & 31));
+        if (m.T > kGroup && atomicAdd(&slots[e], 1) == kGroup) atomicOr(&bits[kMoeMaxExperts / 32 + (e >> 5)], 1u << (e & 31));
+      }
     }
     __syncthreads();
   }
 };
-// Lane l of the first 32: the chosen experts of word l (`word`), how many come
-// before it; returns how many there are. Every lane of the wave takes part.
-__device__ __forceinline__ int count_chosen(const Routing& r, uint32_t& word, int& before) {
+// Lane l of the first 32: the experts of word l (`word`) that are chosen, or
+// listed a second time, how many come before it; returns how many there are. Every lane of the wave takes part.
+__device__ __forceinline__ int count_listed(const Routing& r, int time, uint32_t& word, int& before) {
   const int lane = threadIdx.x & 63;
-  word = lane < kMoeMaxExperts / 32 ? r.bits[lane] : 0;
+  word = lane < kMoeMaxExperts / 32 ? r.bits[kMoeMaxExperts / 32 * time + lane] : 0;
   const int own = __popc(word);
   // inclusive sums of each row of 16 lanes, then the first row's total to the second
   int v = own;
@@ -150,17 +176,23 @@ struct Numbers {
 template <int TILES>
 __global__ __launch_bounds__(64 * kUpWaves) void moe_up_kernel(const MoeTokens m) {
   extern __shared__ __align__(16) char lds[];      // routing; the waves' strips, then their sums
-  __shared__ int tok[kMoeMaxTokens], slot_of[kMoeMaxTokens];
+  __shared__ int tok[kGroup], slot_of[kGroup];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int strips = m.F / 16;
-  const int rank = blockIdx.x / strips, strip = blockIdx.x - rank * strips;
+  int rank = blockIdx.x / strips;
+  const int strip = blockIdx.x - rank * strips;
 
   const Routing routing(m, lds, 64 * kUpWaves);
   char* const area = lds + routing_bytes_of(m);
   uint32_t word;
   int before;
-  if (rank >= count_chosen(routing, word, before)) return;
+  int group = 0, listed = count_listed(routing, 0, word, before);
+  if (rank >= listed) {
+    rank -= listed;
+    group = 1;
+    if (m.T <= kGroup || rank >= count_listed(routing, 1, word, before)) return;
+  }
   const uint64_t hit = __ballot(rank >= before && rank < before + __popc(word));
   const int hl = __ffsll((unsigned long long)hit) - 1;
   const int e = __builtin_amdgcn_readfirstlane(32 * hl + nth_bit(__shfl(word, hl, 64), rank - __shfl(before, hl, 64)));
@@ -184,11 +216,12 @@ __global__ __launch_bounds__(64 * kUpWaves) void moe_up_kernel(const MoeTokens m
 
   const Member mine = member_of<false>(m, routing, e);
   const uint64_t members = __ballot(mine.slot >= 0);
-  const int count = (int)__popcll(members);
-  if (wave == 0 && mine.slot >= 0) {
-    const int at = (int)__popcll(members & ((1ull << lane) - 1ull));
-    tok[at] = lane;
-    slot_of[at] = mine.slot;
+  const int count = min((int)__popcll(members) - kGroup * group, kGroup);
+  if (count <= 0) return;      // (an expert that some token names twice may have fewer tokens than slots)
+  const int place = (int)__popcll(members & ((1ull << lane) - 1ull)) - kGroup * group;
+  if (wave == 0 && mine.slot >= 0 && place >= 0 && place < kGroup) {
+    tok[place] = lane;
+    slot_of[place] = mine.slot;
   }
   __syncthreads();
 
@@ -276,7 +309,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void moe_up_kernel(const MoeTokens m
 template <int TILES>
 __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(const MoeTokens m) {
   extern __shared__ __align__(16) char lds[];      // routing; the waves' strips, then their sums
-  __shared__ uint16_t chosen[kMoeMaxExperts];
+  __shared__ uint16_t listed[kMostListed];      // expert, and kMoeMaxExperts added for its second group of tokens
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int strips = m.K / 32, share = blockIdx.x / strips, strip = blockIdx.x - share * strips;
@@ -285,19 +318,26 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(const MoeToke
   char* const area = lds + routing_bytes_of(m);
   uint32_t word;
   int before;
-  const int experts = count_chosen(routing, word, before);
+  int pairs = count_listed(routing, 0, word, before);
   if (wave == 0)
-    for (; word; word &= word - 1) chosen[before++] = (uint16_t)(32 * lane + __ffs((int)word) - 1);
+    for (; word; word &= word - 1) listed[before++] = (uint16_t)(32 * lane + __ffs((int)word) - 1);
+  if (m.T > kGroup) {
+    const int again = count_listed(routing, 1, word, before);
+    if (wave == 0)
+      for (; word; word &= word - 1) listed[pairs + before++] = (uint16_t)(kMoeMaxExperts + 32 * lane + __ffs((int)word) - 1);
+    pairs += again;
+  }
+  // the wave's sums so far: [T][kSumStride], 32 used (the stride spreads tokens over the banks)
+  float* const sums = reinterpret_cast<float*>(area + kDownWaves * kStripBytes);
+  float* const own_sums = sums + wave * m.T * kSumStride;
+  for (int i = lane; i < m.T * kSumStride / 4; i += 64) reinterpret_cast<f32x4*>(own_sums)[i] = zero4();
   __syncthreads();
 
-  const int tiles = (m.T + 15) / 16, pieces = m.F / kPiece;
-  const int units = experts * pieces, parts = m.shares * kDownWaves, part = share * kDownWaves + wave;
+  const int pieces = m.F / kPiece;
+  const int units = pairs * pieces, parts = m.shares * kDownWaves, part = share * kDownWaves + wave;
   const int begin = (int)((int64_t)units * part / parts), end = (int)((int64_t)units * (part + 1) / parts);
-  f32x4 acc[TILES][2];
-#pragma unroll
-  for (int i = 0; i < TILES; ++i) acc[i][0] = acc[i][1] = zero4();
   if (begin < end) {
-    struct At {      // a unit: piece c of the n-th chosen expert
+    struct At {      // a unit: piece c of the n-th listed pair
       int n, c;
     };
     auto next = [&](At& a, int unit) {      // the one after `unit`; the last one stays
@@ -309,7 +349,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(const MoeToke
     };
     const uint8_t* down = m.w_down + (int64_t)(strip * 32 + (lane >> 3)) * m.F + 16 * (lane & 7);
     auto load = [&](Piece& p, const At& a) {
-      const int e = __builtin_amdgcn_readfirstlane((int)chosen[a.n]);
+      const int e = __builtin_amdgcn_readfirstlane((int)listed[a.n]) % kMoeMaxExperts;
       const uint8_t* at = down + (int64_t)e * m.K * m.F + a.c * kPiece;
 #pragma unroll
       for (int i = 0; i < 4; ++i) p.w[i] = *reinterpret_cast<const u32x4*>(at + 8 * i * (int64_t)m.F);
@@ -325,33 +365,57 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(const MoeToke
       load(ring[i], ahead);
       next(ahead, to_load++);
     }
-    uint64_t members = 0;
-    const uint16_t* h[TILES];
+    int count = 0;               // the pair's tokens; tile i has those from 16 i on, a lane one
+    const uint16_t* h[TILES];    // of the lane's token
     float w[TILES];
-    bool in[TILES];
+    int token[TILES];            // -1: none
     const float* sd = nullptr;
     Numbers b[2][TILES];
     auto load_h = [&](Numbers (&to)[TILES], int c) {
 #pragma unroll
       for (int i = 0; i < TILES; ++i)
-        if (i < tiles && ((members >> (16 * i)) & 0xFFFF)) to[i].load(h[i] + c * kPiece);
+        if (i == 0 || 16 * i < count) to[i].load(h[i] + c * kPiece);
     };
-    auto enter = [&](Numbers (&to)[TILES]) {      // the expert of unit `now`
-      const int e = __builtin_amdgcn_readfirstlane((int)chosen[now.n]);
+    auto enter = [&](Numbers (&to)[TILES]) {      // the pair of unit `now`
+      const int pair = __builtin_amdgcn_readfirstlane((int)listed[now.n]), e = pair % kMoeMaxExperts;
       const Member mine = member_of<true>(m, routing, e);
-      members = __ballot(mine.slot >= 0);
+      const uint64_t members = __ballot(mine.slot >= 0);
+      const int skip = pair < kMoeMaxExperts ? 0 : kGroup;
+      count = min(max((int)__popcll(members) - skip, 0), kGroup);
+      // the group's n-th token goes to lane n: (slot + 1, token), 0 where there is none; the others go to lanes that nobody asks
+      const int place = (int)__popcll(members & ((1ull << lane) - 1ull)) - skip;
+      const int to_lane = mine.slot >= 0 && place >= 0 && place < kGroup ? place : 63;
+      const int what = __builtin_amdgcn_ds_permute(4 * to_lane, (mine.slot + 1) << 6 | lane);
+      const int weight = __builtin_amdgcn_ds_permute(4 * to_lane, __float_as_int(mine.weight));
 #pragma unroll
       for (int i = 0; i < TILES; ++i) {
-        // tokens that did not choose the expert read one that did, and add nothing
-        const int of = 16 * i + (lane & 15);
-        const uint32_t some = (uint32_t)(members >> (16 * i)) & 0xFFFFu;
-        in[i] = (members >> of) & 1;
-        w[i] = __shfl(mine.weight, of, 64);
-        const int other = some ? 16 * i + __ffs((int)some) - 1 : 0;
-        h[i] = m.h + (int64_t)__shfl(mine.slot, in[i] ? of : other, 64) * m.F + 32 * (lane >> 4);
+        const int of = 16 * i + (lane & 15), x = __shfl(what, of, 64);
+        token[i] = of < count ? x & 63 : -1;
+        w[i] = __int_as_float(__shfl(weight, of, 64));
+        // where there is no token: the row of the first
+        h[i] = m.h + (int64_t)max((__shfl(what, of < count ? of : 0, 64) >> 6) - 1, 0) * m.F + 32 * (lane >> 4);
       }
       sd = m.s_down + ((int64_t)e * (m.K / kPiece) + strip * 32 / kPiece) * pieces;
       load_h(to, now.c);
+    };
+    f32x4 acc[TILES][2];
+#pragma unroll
+    for (int i = 0; i < TILES; ++i) acc[i][0] = acc[i][1] = zero4();
+    auto leave = [&] {      // the pair's products to its tokens
+#pragma unroll
+      for (int i = 0; i < TILES; ++i) {
+        if (token[i] >= 0) {
+          float* const at = own_sums + token[i] * kSumStride + 4 * (lane >> 4);
+#pragma unroll
+          for (int a = 0; a < 2; ++a) {
+            f32x4 v = *reinterpret_cast<const f32x4*>(at + 16 * a);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = fmaf(w[i], acc[i][a][j], v[j]);
+            *reinterpret_cast<f32x4*>(at + 16 * a) = v;
+          }
+        }
+        acc[i][0] = acc[i][1] = zero4();
+      }
     };
     enter(b[0]);
     auto step = [&](int unit, Piece& p, Numbers (&cur)[TILES], Numbers (&nxt)[TILES]) {
@@ -366,19 +430,19 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(const MoeToke
       trade.read(1, d[1]);
 #pragma unroll
       for (int i = 0; i < TILES; ++i) {
-        if (i < tiles && ((members >> (16 * i)) & 0xFFFF)) {
-          const float fw = f * w[i];
+        if (i == 0 || 16 * i < count) {
 #pragma unroll
           for (int a = 0; a < 2; ++a) {
             f32x4 sum = zero4();
 #pragma unroll
             for (int s = 0; s < 4; ++s) sum = mfma16(d[a][s], cur[i].b[s], sum);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][a][j] = in[i] ? fmaf(fw, sum[j], acc[i][a][j]) : acc[i][a][j];
+            for (int j = 0; j < 4; ++j) acc[i][a][j] = fmaf(f, sum[j], acc[i][a][j]);
           }
         }
       }
       next(now, unit);
+      if (!stays || unit + 1 == end) leave();
       if (!stays && unit + 1 < end) enter(nxt);
     };
     for (int unit = begin; unit < end; unit += kDeep) {
@@ -391,21 +455,12 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(const MoeToke
       step(unit + 3, ring[3], b[1], b[0]);
     }
   }
-  typedef float Sums[TILES][2][64][4];
-  Sums* const sums = reinterpret_cast<Sums*>(area);
-  __syncthreads();      // the strips are done with
-#pragma unroll
-  for (int i = 0; i < TILES; ++i)
-    if (i < tiles) {
-      *reinterpret_cast<f32x4*>(sums[wave][i][0][lane]) = acc[i][0];
-      *reinterpret_cast<f32x4*>(sums[wave][i][1][lane]) = acc[i][1];
-    }
   __syncthreads();
   // a thread: a token and one of the strip's columns
   auto sum_of = [&](int t, int col) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kDownWaves; ++w) v += sums[w][t >> 4][col >> 4][16 * ((col >> 2) & 3) + (t & 15)][col & 3];
+    for (int w = 0; w < kDownWaves; ++w) v += sums[(w * m.T + t) * kSumStride + col];
     return v;
   };
   __bf16* const out = reinterpret_cast<__bf16*>(m.out) + strip * 32;
@@ -431,13 +486,12 @@ __global__ __launch_bounds__(kJoinThreads) void moe_join_kernel(const MoeTokens 
 
 template <int TILES>
 void launch_tiles(const MoeTokens& m, hipStream_t stream) {
-  const int most = m.T * m.topk < m.E ? m.T * m.topk : m.E;
   // the waves' strips, later their sums
   constexpr size_t sums = sizeof(float) * TILES * 2 * 64 * 4, area = sums > kStripBytes ? sums : (size_t)kStripBytes;
-  hipLaunchKernelGGL(moe_up_kernel<TILES>, dim3((unsigned)(most * (m.F / 16))), dim3(64 * kUpWaves),
+  hipLaunchKernelGGL(moe_up_kernel<TILES>, dim3((unsigned)(most_listed(m) * (m.F / 16))), dim3(64 * kUpWaves),
                      routing_bytes_of(m) + kUpWaves * area, stream, m);
   hipLaunchKernelGGL(moe_down_kernel<TILES>, dim3((unsigned)(m.shares * (m.K / 32))), dim3(64 * kDownWaves),
-                     routing_bytes_of(m) + kDownWaves * area, stream, m);
+                     routing_bytes_of(m) + kDownWaves * (kStripBytes + sizeof(float) * m.T * kSumStride), stream, m);
   if (m.shares > 1)
     hipLaunchKernelGGL(moe_join_kernel, dim3((unsigned)(((int64_t)m.T * m.K / 4 + kJoinThreads - 1) / kJoinThreads)), dim3(kJoinThreads), 0, stream, m);
 }
@@ -445,19 +499,22 @@ void launch_tiles(const MoeTokens& m, hipStream_t stream) {
 }  // namespace
 
 // Shares of the second kernel's work, where the output has fewer strips of
-// columns than three quarters of the compute units.
+// columns than three quarters of the compute units: 5 tokens on experts of 2048
+// x 1408 48 us, unshared 61, with half as many shares 50 and with twice as many
+// 53; 64 tokens on 64 experts of 2048 x 1024 unshared 1.8 times the time.
 int moe_shares(int64_t K) {
   const int64_t strips = K / 32;
   return (int)((192 + strips - 1) / strips);
 }
 
 hipError_t launch_moe_tokens(const MoeTokens& m, hipStream_t stream) {
+  // Places for one tile of tokens take fewer registers and leave three workgroups
+  // on a compute unit for two: 5 tokens on small experts 48 us, with two tiles
+  // 51; 16 tokens 242 and 246. Above, an expert's second tile shares its weights.
   if (m.T <= 16)
     launch_tiles<1>(m, stream);
-  else if (m.T <= 32)
-    launch_tiles<2>(m, stream);
   else
-    launch_tiles<4>(m, stream);
+    launch_tiles<2>(m, stream);
   return hipGetLastError();
 }
 

@@ -73,6 +73,23 @@ def test_all_tokens_choose_one_expert(dev, small):
     _check(dev, small, _x(64, 256, 1), np.full((64, 1), 5), np.ones((64, 1)))
 
 
+@pytest.mark.parametrize("tokens", [9, 31, 32, 33, 50, 64])
+def test_tokens_of_one_expert_beside_others(dev, small, tokens):
+    """Expert 2 is chosen by so many of 64 tokens, in the order of a shuffle; some name it several times."""
+    rng = np.random.default_rng(tokens)
+    ids = rng.integers(3, 8, (64, 5))
+    chose = rng.permutation(64)[:tokens]
+    ids[chose, 1] = 2
+    ids[chose[::2], 3:] = 2
+    _check(dev, small, _x(64, 256, tokens), ids, rng.random((64, 5)))
+
+
+@pytest.mark.parametrize("T", [17, 64])
+def test_one_share_of_the_second_kernel(dev, T):
+    layer = Layer(dev, 2, 6144, 128, seed=5)
+    _check(dev, layer, _x(T, 6144, T), *_ids(T, 2, 2, T))
+
+
 def test_experts_elsewhere_and_named_twice(dev, small):
     rng = np.random.default_rng(3)
     ids = rng.integers(-2, 12, (30, 6))
