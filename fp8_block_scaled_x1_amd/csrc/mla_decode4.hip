@@ -16,14 +16,17 @@
 // the waves meet once a tile; conversions, matrix instructions and LDS fill
 // each other's waits.
 //
-// Bound: a tile takes 3800 clocks, of which the matrix units need 1088, the
-// address unit 1790 and LDS 1460; with one wave on a SIMD the rest is their
-// waits for each other. 128 rows of 128 requests of 300 to 4500 tokens 162 us
-// (505 TFLOP/s), 32 rows of 8 requests of 41000 to 67000 71 us (2.5 TB/s, 433
-// TFLOP/s), 32 rows of 192 requests behind a prefix of 16000 341 us (643
-// TFLOP/s). Not kept: codes through LDS by direct loads (as fast, more code) and
-// loads by whole rows, which take a third of the address unit's time, with the
-// quarters exchanged between lanes (the prefix's call 402 us).
+// Bound: a tile takes 3700 clocks, of which the matrix units need 1088, the
+// address unit 1790 and LDS 1460. With one wave on a SIMD the rest is latency:
+// without loads, conversions, writes of the numbers to LDS and waits for the
+// maxima 2800 would be left, products, weights and the meeting of the waves. 128
+// rows of 128 requests of 300 to 4500 tokens 163 us (502 TFLOP/s), 32 rows of 8
+// requests of 41000 to 67000 72 us (2.5 TB/s, 430 TFLOP/s), 32 rows of 192
+// requests behind a prefix of 16000 328 us (670 TFLOP/s); over the FP8 cache
+// these take 159, 82 and 330 us. Not kept: codes through LDS by direct
+// loads (as fast, more code), loads by whole rows, which take a third of the
+// address unit's time, with the quarters exchanged between lanes (the prefix's
+// call 402 us), the waves' wishes looked at beside the next tile's scores (334).
 //
 // Roundings below 32 bits: the weights to BF16 for the matrix unit (2^-9
 // relative, on the terms of a mean) and the output.
@@ -111,7 +114,23 @@ template <bool TWO>
 __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(1, 1))) void mla_decode_fp4_kernel(
     const Problems problems) {
   const bool second = TWO && (int)blockIdx.x >= problems.split;
-  const MlaDecode& p = problems.p[second];
+  MlaDecode p = problems.p[second];
+  // What every tile needs is kept in scalar registers (no instruction): loaded
+  // again from the arguments each time, it makes a wave wait for all of its LDS
+  // accesses as well (the prefix's call 342 us, now 328).
+  auto keep_one = [](auto& x) {
+    if constexpr (std::is_pointer_v<std::remove_reference_t<decltype(x)>>) {
+      // (a pointer from nowhere would be taken for one into any memory)
+      auto* y = (__attribute__((address_space(1))) std::remove_pointer_t<std::remove_reference_t<decltype(x)>>*)x;
+      asm("" : "+s"(y));
+      x = (std::remove_reference_t<decltype(x)>)y;
+    } else {
+      asm("" : "+s"(x));
+    }
+  };
+  auto keep = [&](auto&... x) { (keep_one(x), ...); };
+  keep(p.cache, p.scales, p.rope, p.table, p.lens, p.table_stride, p.len_stride, p.max_len, p.B, p.pages, p.page, p.page_magic,
+       p.page_shift, p.scale_log2, p.tokens);
   const int block = blockIdx.x - (second ? problems.split : 0);
   __shared__ __align__(1024) char tiles[2 * kTileBytes];
 
@@ -272,7 +291,6 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(1, 
     }
     auto group = [&](auto index) {
       constexpr int I = decltype(index)::value;
-      __builtin_amdgcn_sched_barrier(0);
       if constexpr (V) value(index);
       if constexpr (S) {
         score(std::integral_constant<int, 2 * I>{});
@@ -288,7 +306,6 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(1, 
     };
     [&]<int... I>(std::integer_sequence<int, I...>) { (group(std::integral_constant<int, I>{}), ...); }
     (std::make_integer_sequence<int, 8>{});
-    __builtin_amdgcn_sched_barrier(0);
     if constexpr (S) {
       if ((c.tile + 1) * kTile > c.len - (p.tokens - 1)) {
         const int tok0 = c.tile * kTile + kWaveTokens * wave + 4 * q4;

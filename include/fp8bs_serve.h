@@ -122,8 +122,9 @@ FP8BS_API int64_t fp8bs_mla_decode_fp4_workspace_bytes(int B, int T, int H, int6
  *   out       [T][K]        BF16
  * Unlike the grouped GEMMs it does not quantize activations: x and
  * silu(G x) * (U x) (rounded) are BF16 operands, products and all sums FP32,
- * each 128-wide partial sum scaled as it is added. Each chosen expert's
- * weights are read once. Inputs finite; a code 0x7F or 0xFF is a NaN.
+ * each 128-wide partial sum scaled as it is added. A chosen expert's weights
+ * are read once (twice where more than 32 tokens chose it). Inputs finite; a
+ * code 0x7F or 0xFF is a NaN.
  * 0 <= T <= 64, 1 <= topk <= 64, 1 <= E <= 1024; K and F multiples of 128, at
  * least 128 (FP8BS_ERR_TOO_LARGE above 2^16). workspace: at least
  * fp8bs_moe_tokens_workspace_bytes(T, topk, K, F) bytes.
@@ -165,7 +166,8 @@ FP8BS_API int64_t fp8bs_logprobs_workspace_bytes(int64_t T, int64_t V, int top);
  * (without the first term where targets[t] is no token), in FP32, rounded once
  * to the type of logits. Entries of -inf: p_i = 0 and p_i log p_i = 0; a row of
  * nothing else gets zeros.
- *   d_logits [T][V], of dtype, contiguous, aligned to its type
+ *   d_logits [T][V], of dtype, contiguous, aligned to its type; not the logits'
+ *            own memory, which is read while it is written
  */
 FP8BS_API int fp8bs_logprobs_bwd(const void* logits, int dtype, int64_t stride, const int32_t* targets,
                       const float* norm, const float* entropy, const float* d_logprob,
