@@ -200,16 +200,34 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(1, 
   bool first = true;
   int at = 0;                // offset of the tile whose values come next
 
+  // The rows' queries go through LDS (the place whose values are done with):
+  // loaded by each wave as it needs them, a lane a row, they would take the
+  // address unit 9400 clocks, 4 us of every request's part; a row's end is
+  // padded so that 16 rows at one chunk touch every bank once.
   auto start_piece = [&] {
+    constexpr int kChunks = 2 * kKey / 16, kStride = 2 * kKey + 16, kLoads = 8 * kChunks / 64;
+    static_assert(32 / kWaves == 8 && 8 * kChunks % 64 == 0 && 32 * kStride <= kWeightsAt, "a wave loads 8 rows");
+    char* const stage = tiles + at;
+    u32x4 in[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int chunk = 64 * i + lane, r = 8 * wave + chunk / kChunks, c = chunk % kChunks;
+      const int64_t from = min((int64_t)cur.b * p.rows + min(row0 + r, p.rows - 1), p.all_rows - 1);
+      in[i] = *reinterpret_cast<const u32x4*>(p.q + from * kKey + 8 * c);
+    }
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int chunk = 64 * i + lane;
+      *reinterpret_cast<u32x4*>(stage + (8 * wave + chunk / kChunks) * kStride + 16 * (chunk % kChunks)) = in[i];
+    }
+    attn_barrier();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint16_t* qr =
-          p.q + min((int64_t)cur.b * p.rows + min(row0 + 16 * h + tok16, p.rows - 1), p.all_rows - 1) * kKey;
+      const char* qr = stage + opaque((16 * h + tok16) * kStride);
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        qf[h][i] = *reinterpret_cast<const bf16x8*>(qr + 128 * (i >> 2) + 32 * q4 + 8 * (i & 3));
+      for (int i = 0; i < 16; ++i) qf[h][i] = lds_bf16x8(qr + 256 * (i >> 2) + 64 * q4 + 16 * (i & 3));
 #pragma unroll
-      for (int i = 0; i < 2; ++i) qf[h][16 + i] = *reinterpret_cast<const bf16x8*>(qr + kLatent + 32 * i + 8 * q4);
+      for (int i = 0; i < 2; ++i) qf[h][16 + i] = lds_bf16x8(qr + 2 * kLatent + 64 * i + 16 * q4);
       m[h] = neg_inf();
       l[h] = 0.f;
     }
