@@ -20,9 +20,9 @@
 // address unit 1790 and LDS 1460. With one wave on a SIMD the rest is latency:
 // without loads, conversions, writes of the numbers to LDS and waits for the
 // maxima 2800 would be left, products, weights and the meeting of the waves. 128
-// rows of 128 requests of 300 to 4500 tokens 163 us (502 TFLOP/s), 32 rows of 8
-// requests of 41000 to 67000 72 us (2.5 TB/s, 430 TFLOP/s), 32 rows of 192
-// requests behind a prefix of 16000 328 us (670 TFLOP/s); over the FP8 cache
+// rows of 128 requests of 300 to 4500 tokens 151 us (543 TFLOP/s), 32 rows of 8
+// requests of 41000 to 67000 67 us (2.7 TB/s, 465 TFLOP/s), 32 rows of 192
+// requests behind a prefix of 16000 320 us (688 TFLOP/s); over the FP8 cache
 // these take 159, 82 and 330 us. Not kept: codes through LDS by direct
 // loads (as fast, more code), loads by whole rows, which take a third of the
 // address unit's time, with the quarters exchanged between lanes (the prefix's
@@ -117,7 +117,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(1, 
   MlaDecode p = problems.p[second];
   // What every tile needs is kept in scalar registers (no instruction): loaded
   // again from the arguments each time, it makes a wave wait for all of its LDS
-  // accesses as well (the prefix's call 342 us, now 328).
+  // accesses as well (the prefix's call 342 us, then 328).
   auto keep_one = [](auto& x) {
     if constexpr (std::is_pointer_v<std::remove_reference_t<decltype(x)>>) {
       // (a pointer from nowhere would be taken for one into any memory)

@@ -13,8 +13,9 @@
 // (exact) and multiply them with the tokens' numbers, which come from L2. A
 // 128-wide partial sum is scaled by its block's scale as it is added (FP32).
 //
-// up: a workgroup is 16 columns of h of one expert (16 rows of G and of U), its
-// waves share the inner dimension and add their sums through LDS. down: a
+// up: a strip is 16 columns of h of one expert (16 rows of G and of U); a
+// workgroup's waves share its inner dimension and add their sums through LDS, or
+// have a strip each. down: a
 // workgroup is 32 columns of the output and a share of the (expert, 128 wide
 // piece) pairs, which its waves share in turn; an expert's sums go to its
 // tokens' places in the wave's LDS when the wave is done with it. Both kernels
@@ -30,7 +31,7 @@
 // workgroup's expert among its token's ids. An id outside [0, E) sets no bit.
 //
 // Bound: memory. 8 of 32 experts of 7168 x 2048 for one token 71 us (352 MB, 5.0
-// TB/s), 32 tokens on all 32 of them 272 us (1410 MB, 5.2 TB/s). Small layers:
+// TB/s), 32 tokens on all 32 of them 264 us (1410 MB, 5.3 TB/s). Small layers:
 // launches and a workgroup's start, 5 tokens on 13 of 32 experts of 2048 x 1408
 // 35 us (113 MB, 3.1 TB/s).
 
@@ -173,15 +174,16 @@ struct Numbers {
   }
 };
 
-template <int TILES>
+template <int TILES, bool ALONE>
 __global__ __launch_bounds__(64 * kUpWaves) void moe_up_kernel(const MoeTokens m) {
+  constexpr int kShare = ALONE ? 1 : kUpWaves;      // waves of a strip
   extern __shared__ __align__(16) char lds[];      // routing; the waves' strips, then their sums
   __shared__ int tok[kGroup], slot_of[kGroup];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int strips = m.F / 16;
-  int rank = blockIdx.x / strips;
-  const int strip = blockIdx.x - rank * strips;
+  const int blocks = m.F / 16 * kShare / kUpWaves;      // of a pair
+  int rank = blockIdx.x / blocks;
+  const int strip = (int)(blockIdx.x - rank * blocks) * (kUpWaves / kShare) + (ALONE ? wave : 0), part = ALONE ? 0 : wave;
 
   const Routing routing(m, lds, 64 * kUpWaves);
   char* const area = lds + routing_bytes_of(m);
@@ -198,11 +200,11 @@ __global__ __launch_bounds__(64 * kUpWaves) void moe_up_kernel(const MoeTokens m
   const int e = __builtin_amdgcn_readfirstlane(32 * hl + nth_bit(__shfl(word, hl, 64), rank - __shfl(before, hl, 64)));
 
   const int pieces = m.K / kPiece;
-  const int n = (pieces - wave + kUpWaves - 1) / kUpWaves;      // this wave's: wave, wave + 4, ..
+  const int n = (pieces - part + kShare - 1) / kShare;      // this wave's: part, part + kShare, ..
   const uint8_t* gate = m.w_up + ((int64_t)e * 2 * m.F + strip * 16 + (lane >> 3)) * m.K + 16 * (lane & 7);
   const uint8_t* up = gate + (int64_t)m.F * m.K;
   // (past the wave's last piece that one again: loads under a condition would make the waits for earlier ones wait for these too)
-  auto piece_at = [&](int i) { return wave + kUpWaves * max(0, min(i, n - 1)); };
+  auto piece_at = [&](int i) { return part + kShare * max(0, min(i, n - 1)); };
   auto load = [&](Piece& p, int i) {
     const int64_t at = min(piece_at(i), pieces - 1) * kPiece;
     p.w[0] = *reinterpret_cast<const u32x4*>(gate + at);
@@ -280,6 +282,18 @@ __global__ __launch_bounds__(64 * kUpWaves) void moe_up_kernel(const MoeTokens m
     if (i + 3 >= n) break;
     step(i + 3, ring[3], b[1], b[0]);
   }
+  auto gated = [](float g, float u) { return (__bf16)(g / (1.f + exp2_fast(-g * kLog2e)) * u); };
+  if constexpr (ALONE) {      // a lane has four of the strip's columns, of token lane % 16
+#pragma unroll
+    for (int i = 0; i < TILES; ++i) {
+      const int at = 16 * i + (lane & 15);
+      bf16x4 b;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[j] = gated(ag[i][j], au[i][j]);
+      if (at < count) *reinterpret_cast<bf16x4*>(m.h + (int64_t)slot_of[at] * m.F + strip * 16 + 4 * (lane >> 4)) = b;
+    }
+    return;
+  }
   typedef float Sums[TILES][2][64][4];
   Sums* const sums = reinterpret_cast<Sums*>(area);
   __syncthreads();      // the strips are done with
@@ -301,8 +315,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void moe_up_kernel(const MoeTokens m
       g += sums[w][i][0][from][col & 3];
       u += sums[w][i][1][from][col & 3];
     }
-    const float h = g / (1.f + exp2_fast(-g * kLog2e)) * u;
-    reinterpret_cast<__bf16*>(m.h)[(int64_t)slot_of[at] * m.F + strip * 16 + col] = (__bf16)h;
+    reinterpret_cast<__bf16*>(m.h)[(int64_t)slot_of[at] * m.F + strip * 16 + col] = gated(g, u);
   }
 }
 
@@ -488,8 +501,20 @@ template <int TILES>
 void launch_tiles(const MoeTokens& m, hipStream_t stream) {
   // the waves' strips, later their sums
   constexpr size_t sums = sizeof(float) * TILES * 2 * 64 * 4, area = sums > kStripBytes ? sums : (size_t)kStripBytes;
-  hipLaunchKernelGGL(moe_up_kernel<TILES>, dim3((unsigned)(most_listed(m) * (m.F / 16))), dim3(64 * kUpWaves),
-                     routing_bytes_of(m) + kUpWaves * area, stream, m);
+  // Waves have strips of their own where there are many of them or a strip is
+  // short, and none has to wait for the others: 23 tokens on experts of 896 x 640
+  // (5120 strips) 52 us, strips shared by a workgroup's waves 68; 54 tokens on 8
+  // of 768 x 2816 (1408) 50 and 63; 26 of 1280 x 1152 (2304) 43 and 49; 32 on 32
+  // of 7168 x 2048 (4096) 275 and 281. Shared, they start sooner: 5 tokens of
+  // 2048 x 1408 (2640) 38 and 35, 13 of 6528 x 384 (1560) 96 and 84, 8 of 3456 x
+  // 1024 (512) 32 and 26.
+  const int64_t up_strips = (int64_t)most_listed(m) * (m.F / 16);
+  if (up_strips >= 4096 || 2 * up_strips >= 3 * (int64_t)m.K)
+    hipLaunchKernelGGL((moe_up_kernel<TILES, true>), dim3((unsigned)(up_strips / kUpWaves)), dim3(64 * kUpWaves),
+                       routing_bytes_of(m) + kUpWaves * area, stream, m);
+  else
+    hipLaunchKernelGGL((moe_up_kernel<TILES, false>), dim3((unsigned)up_strips), dim3(64 * kUpWaves),
+                       routing_bytes_of(m) + kUpWaves * area, stream, m);
   hipLaunchKernelGGL(moe_down_kernel<TILES>, dim3((unsigned)(m.shares * (m.K / 32))), dim3(64 * kDownWaves),
                      routing_bytes_of(m) + kDownWaves * (kStripBytes + sizeof(float) * m.T * kSumStride), stream, m);
   if (m.shares > 1)

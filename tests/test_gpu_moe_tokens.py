@@ -84,6 +84,15 @@ def test_tokens_of_one_expert_beside_others(dev, small, tokens):
     _check(dev, small, _x(64, 256, tokens), ids, rng.random((64, 5)))
 
 
+@pytest.mark.parametrize("T", [1, 5, 16, 17, 32, 33, 64])
+def test_waves_with_columns_of_their_own(dev, T):
+    """Many columns and few inner numbers: 6 experts of 128 x 1024, some or all of them for every token."""
+    layer = Layer(dev, 6, 128, 1024, seed=T)
+    for topk in (3, 6):
+        _check(dev, layer, _x(T, 128, T), *_ids(T, topk, 6, T + topk))
+    _check(dev, layer, _x(T, 128, T + 1), *_ids(T, 6, 12, T))
+
+
 @pytest.mark.parametrize("T", [17, 64])
 def test_one_share_of_the_second_kernel(dev, T):
     layer = Layer(dev, 2, 6144, 128, seed=5)
