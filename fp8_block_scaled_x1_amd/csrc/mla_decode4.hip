@@ -5,7 +5,7 @@
 // A workgroup has 32 rows; its four waves have one SIMD each and 512 registers.
 // Scores: a wave forms those of 16 of a tile's 64 tokens and holds all of the
 // rows' queries. A lane is a token and a quarter of its groups: it loads its
-// codes from global memory (400 bytes a token, three tiles ahead, in
+// codes from global memory (400 bytes a token, a tile ahead, in
 // registers), and the converter turns 8 codes and their group's power of two
 // into an exact BF16 operand. An operand is formed once: it goes to the score
 // product and, as it is, to the tile's place in LDS, which the value product
@@ -16,17 +16,19 @@
 // the waves meet once a tile; conversions, matrix instructions and LDS fill
 // each other's waits.
 //
-// Bound: a tile takes 3700 clocks, of which the matrix units need 1088, the
+// Bound: a tile takes 3500 clocks, of which the matrix units need 1088, the
 // address unit 1790 and LDS 1460. With one wave on a SIMD the rest is latency:
 // without loads, conversions, writes of the numbers to LDS and waits for the
-// maxima 2800 would be left, products, weights and the meeting of the waves. 128
+// maxima 2700 would be left, products, weights and the meeting of the waves. 128
 // rows of 128 requests of 300 to 4500 tokens 151 us (543 TFLOP/s), 32 rows of 8
 // requests of 41000 to 67000 67 us (2.7 TB/s, 465 TFLOP/s), 32 rows of 192
-// requests behind a prefix of 16000 320 us (688 TFLOP/s); over the FP8 cache
+// requests behind a prefix of 16000 317 us (694 TFLOP/s); over the FP8 cache
 // these take 159, 82 and 330 us. Not kept: codes through LDS by direct
 // loads (as fast, more code), loads by whole rows, which take a third of the
 // address unit's time, with the quarters exchanged between lanes (the prefix's
-// call 402 us), the waves' wishes looked at beside the next tile's scores (334).
+// call 402 us), loads three tiles ahead (a third copy of the code, which a
+// launch fetches cold: 10 requests of 300 behind a prefix of 12000 50.5 us, now
+// 47; long ones as fast), the waves' wishes looked at beside the next tile's scores (334).
 //
 // Roundings below 32 bits: the weights to BF16 for the matrix unit (2^-9
 // relative, on the terms of a mean) and the output.
@@ -44,7 +46,6 @@ namespace {
 constexpr int kTile = kFp4Tile, kWaves = 4, kWaveTokens = kTile / kWaves;
 static_assert(kTile == 64 && kWaveTokens == 16, "a wave's tokens are the rows of a 16x16x32 product");
 constexpr int kLatent = 512, kKey = 576;
-constexpr int kAhead = 3;                                  // tiles in registers: a load from memory takes two tiles' time
 constexpr int kRowBytes = 2 * kLatent;
 // A tile in LDS: latent numbers, weights (as the value product's operand), row maxima and wishes of the waves.
 constexpr int kWeightsAt = kTile * kRowBytes, kStatAt = kWeightsAt + kTile * 32 * 2;
@@ -164,22 +165,19 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(1, 
     if (nxt.left > 1) next_tile(p, nxt);
     fetch_entry();
   };
-  auto load_part = [&](Raw& r, int n) {      // 0 .. 3: codes, 4, 5: rotary numbers, 6: exponents
+  Raw raw;      // of the tile whose scores come next
+  auto load_part = [&](int n) {      // 0 .. 3: codes, 4, 5: rotary numbers, 6: exponents
     if (n < 4)
-      r.codes[n] = *reinterpret_cast<const u32x4*>(p.cache + slot * 256 + 16 * q4 + 64 * n);
+      raw.codes[n] = *reinterpret_cast<const u32x4*>(p.cache + slot * 256 + 16 * q4 + 64 * n);
     else if (n < 6)
-      r.rope[n - 4] = *reinterpret_cast<const bf16x8*>(p.rope + slot * 128 + 16 * q4 + 64 * (n - 4));
+      raw.rope[n - 4] = *reinterpret_cast<const bf16x8*>(p.rope + slot * 128 + 16 * q4 + 64 * (n - 4));
     else
-      r.exps = *reinterpret_cast<const u32x4*>(p.scales + slot * 16);
+      raw.exps = *reinterpret_cast<const u32x4*>(p.scales + slot * 16);
   };
-  Raw raw[kAhead];
   fetch_entry();
+  next_slot();
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) {
-    next_slot();
-#pragma unroll
-    for (int n = 0; n < 7; ++n) load_part(raw[i], n);
-  }
+  for (int n = 0; n < 7; ++n) load_part(n);
 
   // LDS offsets of this lane in a tile: where it writes its token's numbers
   // (16-byte chunk 4 * q4 + s of each 256 bytes, permuted by the token), and
@@ -246,8 +244,8 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(1, 
   };
 
   // What a tile goes through. Scores: those of the wave's 16 tokens, whose
-  // numbers go to the tile's place `to`; as the registers of r are done with,
-  // the loads of the tile three further on follow into them, one at a time (a
+  // numbers go to the tile's place `to`; as the registers of raw are done with,
+  // the next tile's loads follow into them, one at a time (a
   // wave that issues its loads in one go stands still until the address unit
   // has taken them all). Weights against the reference. Values: of the tile at
   // `from`, the one before, 16 products of which half go beside the scores and
@@ -269,7 +267,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(1, 
       *reinterpret_cast<bf16x4*>(tiles + to + weight0 + 256 * h) = b;
     }
   };
-  auto tile_work = [&](auto with_scores, auto with_values, Raw& r, const Cursor& c, int to, int from) {
+  auto tile_work = [&](auto with_scores, auto with_values, const Cursor& c, int to, int from) {
     constexpr bool S = decltype(with_scores)::value, V = decltype(with_values)::value;
     const int put = opaque(put0 + to), val = opaque(val0 + from);
     bf16x8 pb[4];
@@ -295,14 +293,14 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(1, 
     float f[4];
     auto score = [&](auto index) {      // 32 of the key's columns
       constexpr int I = decltype(index)::value, P = I >> 2, C = I & 3;
-      const u32x4 k = cvt8(r.codes[P][C], f[P]);
+      const u32x4 k = cvt8(raw.codes[P][C], f[P]);
       *reinterpret_cast<u32x4*>(tiles + (put ^ (C << 4)) + 256 * P) = k;
 #pragma unroll
       for (int h = 0; h < 2; ++h) s[h] = mfma16(__builtin_bit_cast(bf16x8, k), qf[h][I], s[h]);
     };
     if constexpr (S) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(((r.exps[i] >> (8 * q4)) & 0xFFu) << 23);
+      for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(((raw.exps[i] >> (8 * q4)) & 0xFFu) << 23);
 #pragma unroll
       for (int h = 0; h < 2; ++h) s[h] = f32x4{0.f, 0.f, 0.f, 0.f};
       next_slot();
@@ -315,11 +313,11 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(1, 
         score(std::integral_constant<int, 2 * I + 1>{});
         if constexpr (I < 2) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) s[h] = mfma16(r.rope[I], qf[h][16 + I], s[h]);
+          for (int h = 0; h < 2; ++h) s[h] = mfma16(raw.rope[I], qf[h][16 + I], s[h]);
         }
-        if constexpr (I == 0) load_part(r, 6);
-        if constexpr (I == 2 || I == 4) load_part(r, 4 + (I >> 2));
-        if constexpr (I & 1) load_part(r, I >> 1);
+        if constexpr (I == 0) load_part(6);
+        if constexpr (I == 2 || I == 4) load_part(4 + (I >> 2));
+        if constexpr (I & 1) load_part(I >> 1);
       }
     };
     [&]<int... I>(std::integer_sequence<int, I...>) { (group(std::integral_constant<int, I>{}), ...); }
@@ -423,20 +421,20 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(1, 
   constexpr std::true_type yes{};
   constexpr std::false_type no{};
   bool whole = cur.tile == 0 && cur.left >= cur.tiles, fresh = true;
-  auto step = [&](Raw& r) {      // returns whether a tile follows
+  auto step = [&] {      // returns whether a tile follows
     // (the other place also where nothing is in this one: someone may still read the sums of the last request there)
     if (fresh) {
       start_piece();
-      tile_work(yes, no, r, cur, at ^ kTileBytes, 0);
+      tile_work(yes, no, cur, at ^ kTileBytes, 0);
       fresh = false;
     } else {
-      tile_work(yes, yes, r, cur, at ^ kTileBytes, at);
+      tile_work(yes, yes, cur, at ^ kTileBytes, at);
     }
     at ^= kTileBytes;
     meet(at);
     const bool last = cur.tile + 1 == cur.tiles || cur.left == 1;
     if (last) {
-      tile_work(no, yes, r, cur, 0, at);
+      tile_work(no, yes, cur, 0, at);
       finish_piece(whole);
       first = false;
       fresh = true;
@@ -445,7 +443,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(1, 
     if (last) whole = cur.left >= cur.tiles;
     return cur.left > 0;
   };
-  while (step(raw[0]) && step(raw[1]) && step(raw[2])) {
+  while (step()) {
   }
 }
 
