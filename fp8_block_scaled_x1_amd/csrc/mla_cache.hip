@@ -7,7 +7,8 @@
 // whose range of the packed rows holds it, found by 64-way search of the
 // offsets. The arithmetic of a token is a few dozen instructions; what bounds
 // these kernels is the chain offset -> length -> table entry -> slot at the
-// small end and memory at the large one.
+// small end (96 requests of 1 to 3 tokens: 3.3 us either way) and memory at the
+// large one (36900 tokens, FP8: written in 15.5 us, read in 14.6, 4.5 TB/s).
 
 #include "attn_common.h"
 #include "device_common.h"
