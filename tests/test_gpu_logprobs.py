@@ -101,6 +101,18 @@ def test_masked_entries(dev, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("top", [0, 30])
+@pytest.mark.parametrize("V", [5, 13, 77, 8195, 8199, 8205, 12943])
+def test_masked_tokens_in_the_last_chunk(dev, V, top, dtype):
+    """Most entries masked, the tokens' own among them, where the row's end cuts an access."""
+    x = _logits(5, V, V, dtype)
+    x[torch.rand(x.shape, generator=torch.Generator().manual_seed(V)) < 0.98] = -float("inf")
+    targets = [V - 1, V - 2, V - 3, V - 4, V // 2]
+    x[range(4), targets[:4]] = -float("inf")
+    _check(dev, x, targets, min(V, top))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_far_apart_and_large(dev, dtype):
     x = _logits(4, 9000, 6, dtype, std=100.0)
     x[1] += 10000.0

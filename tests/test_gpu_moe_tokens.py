@@ -93,6 +93,12 @@ def test_waves_with_columns_of_their_own(dev, T):
     _check(dev, layer, _x(T, 128, T + 1), *_ids(T, 6, 12, T))
 
 
+@pytest.mark.parametrize("E", [70, 1024])
+def test_most_tokens_and_slots(dev, E):
+    layer = Layer(dev, E, 128, 128, seed=E)
+    _check(dev, layer, _x(64, 128, 3), *_ids(64, 64, E, 3))
+
+
 @pytest.mark.parametrize("T", [17, 64])
 def test_one_share_of_the_second_kernel(dev, T):
     layer = Layer(dev, 2, 6144, 128, seed=5)
