@@ -165,13 +165,15 @@ __device__ __forceinline__ uint32_t nth_value(uint32_t v, int n, bool counts = t
 struct Sums {      // of a part of a row
   float m, l, w;
 };
-__device__ __forceinline__ float scaled(float a, float b) { return a == 0.f ? 0.f : a * b; }      // 0 of an empty part stays
+// A part's sum moved by the factor e. Where e is 0 the sum has no share,
+// whatever its size: an empty part's maximum of -inf, or a masked part's of the
+// type's lowest value, makes it -inf or a NaN. (A NaN maximum makes e one.)
+__device__ __forceinline__ float moved(float e, float sum) { return e == 0.f ? 0.f : e * sum; }
 // x, moved to the larger maximum m.
 __device__ __forceinline__ void add_part(Sums& s, const Sums& x) {
   const float m = max_nan(s.m, x.m), ref = m == neg_inf() ? 0.f : m;
   const float a = s.m - ref, b = x.m - ref, ea = exp2_fast(a * kLog2e), eb = exp2_fast(b * kLog2e);
-  // an empty part (maximum -inf) has sums of 0, and -inf * 0 must not become a NaN
-  s.w = ea * (s.w + scaled(s.l, a)) + eb * (x.w + scaled(x.l, b));
+  s.w = moved(ea, s.w + s.l * a) + moved(eb, x.w + x.l * b);
   s.l = s.l * ea + x.l * eb;
   s.m = m;
 }

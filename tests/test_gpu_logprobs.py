@@ -230,3 +230,36 @@ def test_no_rows_and_refusals(dev):
             fb.fp8bs_logprobs(x, y, top)
     with pytest.raises(ValueError):
         fb.fp8bs_logprobs_bwd(x, y, x[:, :2].contiguous(), x[0, :3].clone(), x[0, :2].clone(), x[0, :3].clone())
+
+
+def _masked_rows(V, dtype, masks, seed):
+    """Rows masked with finite values, for each of them: three entries left, one of 50 left, a chunk of 8192 masked."""
+    x = _logits(3 * len(masks), V, seed, dtype)
+    keep = torch.zeros((3, V), dtype=torch.bool)
+    keep[0, [5, V // 2, V - 1]] = True
+    keep[1, 7::50] = True
+    keep[2, 8192:] = True
+    for i, value in enumerate(masks):
+        x[3 * i:3 * i + 3][~keep] = value
+    targets = [5, 7, V - 2] * len(masks)
+    targets[2::6] = [100] * len(targets[2::6])         # (a masked token)
+    return x, targets
+
+
+def _check_masked(dev, V, top, dtype, masks):
+    x, targets = _masked_rows(V, dtype, masks, V)
+    got = _check(dev, x, targets, top)
+    # the gradient of the log probability alone, as a policy gradient takes it
+    xd, y = x.to(dev), torch.as_tensor(targets, dtype=torch.int32, device=dev)
+    one, none = torch.ones(len(x), device=dev), torch.zeros(len(x), device=dev)
+    grad = fb.fp8bs_logprobs_bwd(xd, y, got["norm"], got["entropy"], one, none)
+    w, b = os_.logprobs_bwd(x.double().numpy(), targets, np.ones(len(x)), np.zeros(len(x)), torch.finfo(dtype).eps / 2)
+    _inside(grad, w, b, "gradient of the log probability")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("top", [0, 20])
+@pytest.mark.parametrize("V", [20000, 129280])
+def test_masks_near_the_lowest_value(dev, V, top, dtype):
+    """Parts of a row whose sum of exponentials times their distance to the row's maximum overflows."""
+    _check_masked(dev, V, top, dtype, [torch.finfo(dtype).min, -1e38, -1e36])
