@@ -13,9 +13,10 @@
 //
 // The exponentials are 2^(c x - c m), c = log2 e, one fused multiply-add each:
 // what c m loses by its own rounding is a factor of all of them, known exactly
-// and taken back from the sums. An entry comes before the token if it is larger,
-// or equal and ahead of it, so in a chunk that the token is not in one
-// comparison tells, counted by the scalar unit.
+// and taken back from the sums (|m| below 2^20; beyond, 2^(c (x - m))). An entry
+// comes before the token if it is larger, or equal and ahead of it, so in a
+// chunk that the token is not in one comparison tells, counted by the scalar
+// unit.
 //
 // Best entries: an entry's key is its value in an order of whole numbers, then
 // the lowest index, so keys differ. A wave takes the top-th largest of its
@@ -178,8 +179,11 @@ __device__ __forceinline__ void add_part(Sums& s, const Sums& x) {
   s.m = m;
 }
 
-// Sums of exp(x_i - m) and of that times (x_i - m); `usual`: the same for the
-// wave, and |m| < 2^100 if it is set.
+// Sums of exp(x_i - m) and of that times (x_i - m). `usual`: the same for the
+// wave, and |m| < kUsual if it is set: c m is below 2^21 then, its rounding
+// (`lost`) at most 2^-4. It grows with m, and beyond 2^7 (|m| of some 10^10, a
+// mask) the exponentials would leave FP32's range.
+constexpr float kUsual = 0x1p20f;
 __device__ __forceinline__ void sums_against(const float (&x)[kPer], float m, bool usual, float& l, float& w) {
   l = w = 0.f;
   if (usual) {
@@ -193,7 +197,7 @@ __device__ __forceinline__ void sums_against(const float (&x)[kPer], float m, bo
     const float back = exp2_fast(-lost);
     w = fmaf(-lost, l, w) * back * kLn2;
     l *= back;
-  } else {      // far from anything usual (-inf and NaN among them): differences first
+  } else {      // masks, -inf and NaN among them: differences first
     const float ref = m == neg_inf() ? 0.f : m;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -310,7 +314,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_chunk_kernel(const Logprobs
   }
 
   float l, w;
-  sums_against(x, m, fabsf(m) < 0x1p100f, l, w);
+  sums_against(x, m, fabsf(m) < kUsual, l, w);
   l = wave_sum(l);
   w = wave_sum(w);
   int before = count_before<BF16>(x, first, n, y, xy);
@@ -426,7 +430,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_stream_kernel(const Logprob
 #pragma unroll
     for (int i = 1; i < kPer; ++i) c.m = max_nan(c.m, x[i]);
     c.m = max_nan(c.m, mine.m);
-    sums_against(x, c.m, __all(fabsf(c.m) < 0x1p100f), c.l, c.w);
+    sums_against(x, c.m, __all(fabsf(c.m) < kUsual), c.l, c.w);
     add_part(mine, c);
     before += count_before<BF16>(x, first, n, y, xy);
   };

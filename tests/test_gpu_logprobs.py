@@ -263,3 +263,23 @@ def _check_masked(dev, V, top, dtype, masks):
 def test_masks_near_the_lowest_value(dev, V, top, dtype):
     """Parts of a row whose sum of exponentials times their distance to the row's maximum overflows."""
     _check_masked(dev, V, top, dtype, [torch.finfo(dtype).min, -1e38, -1e36])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("top", [0, 20])
+@pytest.mark.parametrize("V", [20000, 129280])
+def test_masks_of_large_finite_values(dev, V, top, dtype):
+    """Maxima of a part whose product with log2 e has a rounding error beyond the range of an exponential."""
+    _check_masked(dev, V, top, dtype, [-1e30, -1e20, -1e10, -1e9, -3e6, -1e6])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("top", [0, 5])
+def test_large_maxima(dev, top, dtype):
+    """The same at the rows' own maxima, of either sign, next to what is their rounding away."""
+    x = _logits(10, 9000, 3, dtype)
+    for i, m in enumerate([2.0 ** 18, 2.0 ** 20, 1e7, 1e9, 1e30]):
+        x[2 * i:2 * i + 2] *= m * 2.0 ** -22           # differences from a fraction of one to far more
+        x[2 * i] += m
+        x[2 * i + 1] -= m
+    _check(dev, x, [1, 8999, 2, 8998, 3, 8997, 4, 8996, 5, 8995], top)
