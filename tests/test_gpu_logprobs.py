@@ -283,3 +283,49 @@ def test_large_maxima(dev, top, dtype):
         x[2 * i] += m
         x[2 * i + 1] -= m
     _check(dev, x, [1, 8999, 2, 8998, 3, 8997, 4, 8996, 5, 8995], top)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,V,pad", [(2048, 16385, 3), (700, 40000, 0), (700, 40000, 5), (1100, 24576, 8), (400, 60001, 1)])
+def test_many_rows_of_several_chunks(dev, T, V, pad, dtype):
+    """Without alternatives, a workgroup goes over several chunks: all three of a row's (2048 rows), two and one of
+    three (1100) or of five (700), two of eight (400). Usual rows, and rows that only some chunks decide."""
+    x = _logits(T, V, V, dtype, pad=pad)
+    targets = _targets(T, V, V)
+    low, inf, at = torch.finfo(dtype).min, float("inf"), 8192
+    x[0] = torch.arange(V) // 7 / V * 30               # every chunk raises the maximum
+    x[1] = -x[0]
+    x[2, :at] = x[3, at:2 * at] = x[4, 2 * at:] = -inf
+    x[5, :at] = x[6, at:2 * at] = x[7, 2 * at:] = low
+    x[8], x[9], x[10] = -inf, low, 0.0
+    x[11, :V - 1] = x[12, 1:] = -inf
+    x[13, :V - 1] = x[14, 1:] = low
+    x[15] = torch.arange(V) % 3                        # ties, here and over chunks' ends
+    x[16, :2 * at] -= 10000.0
+    x[17, at:] += 10000.0
+    x[18] *= 100.0
+    x[19, ::2] = low
+    targets[:20] = [V - 1, V - 1, at, at - 1, 0, at - 1, 2 * at, V - 1, 2 * at, 5, at, V - 1, 0, V - 1, V - 1, 2 * at, V - 1, at, 3, 2]
+    targets[20:24] = [-1, V, at - 1, 2 * at - 1]
+    rows = list(range(28)) + [T // 2, T - 2, T - 1]
+    xd = _on(dev, x)
+    y = torch.as_tensor(targets, dtype=torch.int32, device=dev)
+    got = dict(zip(NAMES, fb.fp8bs_logprobs(xd, y)))
+    some = x[rows].double().numpy()
+    want, bound = os_.logprobs(some, targets[rows], 0)
+    assert np.array_equal(got["rank"][rows].cpu().numpy(), want["rank"])
+    for n in ("logprob", "entropy", "norm"):
+        _inside(got[n][rows], want[n], bound[n], n)
+    g = torch.Generator().manual_seed(5)
+    dl, dh = torch.randn(T, generator=g), torch.randn(T, generator=g)
+    grad = fb.fp8bs_logprobs_bwd(xd, y, got["norm"], got["entropy"], dl.to(dev), dh.to(dev))
+    w, b = os_.logprobs_bwd(some, targets[rows], dl[rows].numpy(), dh[rows].numpy(), torch.finfo(dtype).eps / 2)
+    _inside(grad[rows], w, b, "gradient")
+    # the other rows: the same numbers as when they are asked for by themselves, a chunk per workgroup
+    for first in range(28, T - 9, T // 3):
+        few = slice(first, first + 9)
+        alone = dict(zip(NAMES, fb.fp8bs_logprobs(xd[few], y[few])))
+        assert torch.equal(alone["rank"], got["rank"][few])
+        # (each within FP32's bound of the same number: a few units times 2^-17)
+        for n in ("logprob", "entropy", "norm"):
+            assert torch.allclose(alone[n], got[n][few], rtol=2.0 ** -17, atol=2.0 ** -16), n
