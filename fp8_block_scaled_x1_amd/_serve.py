@@ -215,7 +215,9 @@ def fp8bs_logprobs(logits, targets, top=0):
     apart), targets int32 [T]. Returns (logprob f32 [T], entropy f32 [T], norm f32
     [T][2], rank int32 [T], top_ids int32 [T][top], top_logprobs f32 [T][top])."""
     device, dtype, stride, T, V, px, pt = _rows(logits, targets)
-    logprob, entropy = torch.empty((2, T), dtype=_f32, device=device).unbind(0)
+    # (tensors of their own: views of one could not be changed in place behind an autograd function)
+    logprob = torch.empty((T,), dtype=_f32, device=device)
+    entropy = torch.empty((T,), dtype=_f32, device=device)
     norm = torch.empty((T, 2), dtype=_f32, device=device)
     rank = torch.empty((T,), dtype=_i32, device=device)
     need = _known_bytes("fp8bs_logprobs_workspace_bytes", T, V, top)

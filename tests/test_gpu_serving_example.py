@@ -156,3 +156,18 @@ def test_only_one_of_the_outputs_is_used(dev):
         value = (p.gather(1, targets.clamp_min(0).long()[:, None])[:, 0] * inside).sum() if pick == 0 else -(p.exp() * p).sum()
         want, = torch.autograd.grad(value, x)
         assert (got.double() - want).abs().max() <= 2 ** -18
+
+
+def test_outputs_may_be_changed_in_place(dev):
+    """Masking ignored tokens in place, as a training loss does: the outputs share nothing, with what is kept for the
+    gradient neither."""
+    x = torch.randn(6, 300, generator=torch.Generator().manual_seed(3)).to(dev).requires_grad_()
+    y = torch.tensor([0, 299, 5, -1, 17, 100], dtype=torch.int32, device=dev)
+    ignored = torch.tensor([0, 1, 0, 0, 1, 0], dtype=torch.bool, device=dev)
+    logprob, entropy = ex.LogProbs.apply(x, y)
+    want, = torch.autograd.grad((logprob * ~ignored).sum() + entropy.sum(), x)
+    logprob, entropy = ex.LogProbs.apply(x, y)
+    logprob.masked_fill_(ignored, 0.0)
+    got, = torch.autograd.grad(logprob.sum() + entropy.sum(), x)
+    assert torch.equal(got, want)
+    assert len({t.untyped_storage().data_ptr() for t in fb.fp8bs_logprobs(x.detach(), y, 2)}) == 6
