@@ -501,15 +501,28 @@ template <int TILES>
 void launch_tiles(const MoeTokens& m, hipStream_t stream) {
   // the waves' strips, later their sums
   constexpr size_t sums = sizeof(float) * TILES * 2 * 64 * 4, area = sums > kStripBytes ? sums : (size_t)kStripBytes;
-  // Waves have strips of their own where there are many of them or a strip is
-  // short, and none has to wait for the others: 23 tokens on experts of 896 x 640
-  // (5120 strips) 52 us, strips shared by a workgroup's waves 68; 54 tokens on 8
-  // of 768 x 2816 (1408) 50 and 63; 26 of 1280 x 1152 (2304) 43 and 49; 32 on 32
-  // of 7168 x 2048 (4096) 275 and 281. Shared, they start sooner: 5 tokens of
-  // 2048 x 1408 (2640) 38 and 35, 13 of 6528 x 384 (1560) 96 and 84, 8 of 3456 x
-  // 1024 (512) 32 and 26.
-  const int64_t up_strips = (int64_t)most_listed(m) * (m.F / 16);
-  if (up_strips >= 4096 || 2 * up_strips >= 3 * (int64_t)m.K)
+  // Waves have strips of their own where there are enough for the device, and
+  // none has to wait for the others; shared by a workgroup's waves, strips start
+  // sooner. The host knows how many there are at most (experts whose ids all lie
+  // elsewhere have none). Whole calls, shared and own, us, "in" so many experts:
+  // the others elsewhere, strips in brackets. Two tiles:
+  //   32 tokens on 8 experts of 1024 x 512 (256) 20.7 and 25.4, 16 of 1024 x 1024
+  //   (1024) 33.1 and 29.3, 32 of 2048 x 512 in 256 (1024) 29.0 and 26.0, 32 of 3584
+  //   x 2048 (4096) 156 and 144, 16 of 7168 x 1536 (1536) 144 and 155, 32 of 7168 x
+  //   2048 (4096) 281 and 266, but in 256 180 and 189; 54 tokens on 8 of 2048 x 512
+  //   (672) 35.5 and 40.6, 64 of 4608 x 1536 (7392) 322 and 307. Rows a multiple of
+  //   4096 bytes apart: 32 tokens on 32 of 4096 x 2048 (4096) 184 and 190, of 8192 x
+  //   2048 311 and 327.
+  // One tile:
+  //   5 tokens on 8 of 512 x 512 (256) 14.5 and 15.3, 16 of 512 x 1024 (1024) 21.5
+  //   and 19.9, 32 of 2048 x 512 in 64 (960) 21.9 and 24.2, 32 of 2048 x 2048 (4096)
+  //   89.5 and 84.3, of 2560 x 2048 (3840) 74.1 and 71.8, of 3584 x 2048 in 64 (3840)
+  //   72.7 and 74.1, of 7168 x 2048 (4096) 241 and 246; 16 tokens on 32 of 2560 x
+  //   1408 (2816) 81.7 and 79.0, but in 96 66.6 and 68.6.
+  const int64_t up_strips = (int64_t)most_listed(m) * (m.F / 16), some = 3 * (int64_t)m.K / 2;
+  const bool own = TILES == 1 ? m.K <= 2560 && up_strips >= some
+                              : m.K % 4096 != 0 && up_strips >= (m.K > 4096 ? 4096 : some < 1024 ? some : 1024);
+  if (own)
     hipLaunchKernelGGL((moe_up_kernel<TILES, true>), dim3((unsigned)(up_strips / kUpWaves)), dim3(64 * kUpWaves),
                        routing_bytes_of(m) + kUpWaves * area, stream, m);
   else

@@ -93,6 +93,16 @@ def test_waves_with_columns_of_their_own(dev, T):
     _check(dev, layer, _x(T, 128, T + 1), *_ids(T, 6, 12, T))
 
 
+@pytest.mark.parametrize("T", [16, 17, 32, 33, 64])
+@pytest.mark.parametrize("E,K,F", [(8, 128, 2048), (8, 768, 2048), (4, 4096, 128)])
+def test_strips_around_the_rules_limits(dev, T, E, K, F):
+    """Many strips of short and of longer columns (1024 at least), and few of rows a multiple of 4096 bytes apart;
+    ids of experts elsewhere among the tokens'."""
+    layer = Layer(dev, E, K, F, seed=T)
+    _check(dev, layer, _x(T, K, T), *_ids(T, 4, E, T))
+    _check(dev, layer, _x(T, K, T + 1), *_ids(T, 4, 3 * E, T))
+
+
 @pytest.mark.parametrize("E", [70, 1024])
 def test_most_tokens_and_slots(dev, E):
     layer = Layer(dev, E, 128, 128, seed=E)
