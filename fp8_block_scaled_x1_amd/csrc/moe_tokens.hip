@@ -536,19 +536,25 @@ void launch_tiles(const MoeTokens& m, hipStream_t stream) {
 
 }  // namespace
 
-// Shares of the second kernel's work, where the output has fewer strips of
-// columns than three quarters of the compute units: 5 tokens on experts of 2048
-// x 1408 48 us, unshared 61, with half as many shares 50 and with twice as many
-// 53; 64 tokens on 64 experts of 2048 x 1024 unshared 1.8 times the time.
+// Shares of the second kernel's work: some 192 workgroups where the output has
+// few strips of columns, but no more than 256, a compute unit each. 5 tokens on
+// experts of 2048 x 1408 (64 strips, 3 shares) 50.6 us, unshared 65.0, two shares
+// 54.0, five 57.6; 64 tokens on 64 of 2048 x 1024 97, unshared 146, five shares
+// 111; 2 tokens on 8 of 512 x 512 (16, 12 shares) 13.8, 8 shares 13.0, 16 15.0. 32
+// tokens on 16 experts of 4096 x 1024 (128 strips) two shares 57.4, one 63.0, of
+// 4352 x 1024 (136) 69.5 and 62.2, of 5888 x 1024 (184) 78.2 and 70.6.
 int moe_shares(int64_t K) {
-  const int64_t strips = K / 32;
-  return (int)((192 + strips - 1) / strips);
+  const int64_t strips = K / 32, some = (192 + strips - 1) / strips, most = 256 / strips;
+  return (int)(some < most ? some : most < 1 ? 1 : most);
 }
 
 hipError_t launch_moe_tokens(const MoeTokens& m, hipStream_t stream) {
   // Places for one tile of tokens take fewer registers and leave three workgroups
-  // on a compute unit for two: 5 tokens on small experts 48 us, with two tiles
-  // 51; 16 tokens 242 and 246. Above, an expert's second tile shares its weights.
+  // on a compute unit for two. One tile and two, strips shared: 5 tokens on 32
+  // experts of 1024 x 2048 49.9 and 57.3 us, of 2048 x 2048 74.3 and 80.1, of 7168 x
+  // 2048 190 and 191; 16 tokens of 4096 x 2048 160 and 161, of 7168 x 512 on 8 of them
+  // 30.7 and 29.7. Strips of their own: 16 tokens on 32 of 1024 x 2048 55.7 and 56.0.
+  // Above 16, an expert's second tile shares its weights.
   if (m.T <= 16)
     launch_tiles<1>(m, stream);
   else

@@ -115,6 +115,13 @@ def test_one_share_of_the_second_kernel(dev, T):
     _check(dev, layer, _x(T, 6144, T), *_ids(T, 2, 2, T))
 
 
+@pytest.mark.parametrize("T", [5, 33])
+@pytest.mark.parametrize("K", [128, 1408, 2816, 4096, 4352])
+def test_shares_of_the_second_kernel(dev, K, T):
+    layer = Layer(dev, 3, K, 128, seed=K)
+    _check(dev, layer, _x(T, K, T), *_ids(T, 2, 3, T))
+
+
 def test_experts_elsewhere_and_named_twice(dev, small):
     rng = np.random.default_rng(3)
     ids = rng.integers(-2, 12, (30, 6))
