@@ -47,6 +47,8 @@
 // Roundings below 32 bits: probabilities (times the scale, FP8) to BF16 for
 // the matrix unit (relative 2^-8 at most each, on the terms of a mean), and the output.
 
+#include <atomic>
+
 #include "mla_paged.h"
 
 namespace fp8bs {
@@ -59,6 +61,33 @@ constexpr int kLatent = 512, kRope = 64, kKey = kLatent + kRope;
 // than 2^8 above it: weights up to 2^8 cost no precision in FP32 or BF16, and
 // the accumulators are rescaled a few times per request instead of per tile.
 constexpr float kSlack = 8.f;
+
+__device__ __forceinline__ void advance(const MlaDecode& p, Cursor& c) {
+  --c.left;
+  if (++c.tile < c.tiles || c.left <= 0) return;
+  do {
+    ++c.b;
+    c.len = c.b < p.B ? __builtin_amdgcn_readfirstlane(clamp_len(p, c.b)) : 0;
+  } while (c.len == 0 && c.b < p.B);
+  c.tile = 0;
+  c.tiles = tiles_of<kTile>(c.len);
+}
+
+// Token of the tile's row `lane`. Tokens past the end repeat the last one:
+// always cached, and masked by its position.
+__device__ __forceinline__ int row_token(const Cursor& c, int lane) { return min(c.tile * kTile + lane, c.len - 1); }
+
+inline int compute_units() {
+  static std::atomic<int> cached[64] = {};
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+  if (cached[dev] == 0) {
+    int n = 0;
+    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) n = 256;
+    cached[dev] = n;
+  }
+  return cached[dev];
+}
 
 template <bool FP8>
 struct Tile {
@@ -91,7 +120,7 @@ struct Loader {
   const int64_t flat;
   const int chunk;
   __device__ __forceinline__ static int64_t flat_of(const MlaDecode& p, const Cursor& c, int lane, int entry) {
-    const int tok = row_token<kTile>(c, lane);
+    const int tok = row_token(c, lane);
     return (int64_t)min(max(entry, 0), p.pages - 1) * p.page + (tok - page_of(p, tok) * p.page);
   }
   __device__ __forceinline__ Loader(const MlaDecode& p_, const Cursor& c, int r0_, int lane_, int entry, uint32_t lds_)
@@ -202,12 +231,12 @@ __global__ __launch_bounds__(256 * kTeams) __attribute__((amdgpu_waves_per_eu(2)
   Cursor nxt = cur;      // the tile that is loaded next
   Cursor ent = cur;      // the tile whose block-table entries are fetched next
   auto fetch_entries = [&] {
-    const int* src = p.table + (int64_t)ent.b * p.table_stride + page_of(p, row_token<kTile>(ent, lane));
+    const int* src = p.table + (int64_t)ent.b * p.table_stride + page_of(p, row_token(ent, lane));
     if constexpr (NBUF == 2)
       entry = *src;
     else
       dma4(src, lds_entries);
-    advance<kTile>(p, ent);
+    advance(p, ent);
   };
   auto start_next = [&](int to) {      // the loads of the tile `nxt`, into buffer `to`
     if constexpr (NBUF > 2) {
@@ -216,7 +245,7 @@ __global__ __launch_bounds__(256 * kTeams) __attribute__((amdgpu_waves_per_eu(2)
     }
     const int e = opaque(entry);      // waited for here, before the next fetch is under way
     const Cursor c = nxt;
-    advance<kTile>(p, nxt);
+    advance(p, nxt);
     if (ent.left > 0) fetch_entries();
     return Load(p, c, wave * kRows, lane, e, lds_tiles + to * T::kBytes);
   };
@@ -280,7 +309,7 @@ __global__ __launch_bounds__(256 * kTeams) __attribute__((amdgpu_waves_per_eu(2)
       auto step = [&] {
         last = cur.tile + 1 == cur.tiles || cur.left == 1;
         if (last) return;
-        advance<kTile>(p, cur);
+        advance(p, cur);
         buf = buf + 1 == NBUF ? 0 : buf + 1;
       };
       // any wave's wish to raise the reference: the answer is the same for all
@@ -513,7 +542,7 @@ __global__ __launch_bounds__(256 * kTeams) __attribute__((amdgpu_waves_per_eu(2)
       }
     }
     first = false;
-    advance<kTile>(p, cur);
+    advance(p, cur);
     buf = buf + 1 == NBUF ? 0 : buf + 1;
   }
 }

@@ -3,8 +3,6 @@
 // partial results that the cuts leave. TILE: tokens of a tile.
 #pragma once
 
-#include <atomic>
-
 #include "attn_internal.h"
 #include "mla_tiles.h"
 
@@ -24,18 +22,6 @@ struct Cursor {
 };
 
 __device__ __forceinline__ int clamp_len(const MlaDecode& p, int b) { return min(max(p.lens[b * p.len_stride], 0), p.max_len); }
-
-template <int TILE>
-__device__ __forceinline__ void advance(const MlaDecode& p, Cursor& c) {
-  --c.left;
-  if (++c.tile < c.tiles || c.left <= 0) return;
-  do {
-    ++c.b;
-    c.len = c.b < p.B ? __builtin_amdgcn_readfirstlane(clamp_len(p, c.b)) : 0;
-  } while (c.len == 0 && c.b < p.B);
-  c.tile = 0;
-  c.tiles = (c.len + TILE - 1) / TILE;
-}
 
 __device__ __forceinline__ int wave_scan(int v) {
   const int lane = threadIdx.x & 63;
@@ -105,11 +91,6 @@ __device__ __forceinline__ Cursor first_tile(const MlaDecode& p, int g) {
 __device__ __forceinline__ int page_of(const MlaDecode& p, int tok) {
   return (int)(((uint64_t)(uint32_t)tok * p.page_magic) >> p.page_shift);
 }
-
-// Token of the tile's row `lane`. Tokens past the end repeat the last one:
-// always cached, and masked by its position.
-template <int TILE>
-__device__ __forceinline__ int row_token(const Cursor& c, int lane) { return min(c.tile * TILE + lane, c.len - 1); }
 
 // Joins the partials of the rows whose request was cut between groups (and, in
 // the shared form, the prefix's with the request's own). W waves per row, lane
@@ -259,18 +240,6 @@ void launch_mla_join(const MlaDecode& own, const MlaDecode& head, bool behind_pr
     hipLaunchKernelGGL((mla_join_kernel<4, TILE>), dim3((unsigned)own.all_rows), dim3(kJoinThreads), 0, stream, own, head);
   else
     hipLaunchKernelGGL((mla_join_kernel<1, TILE>), dim3((unsigned)((own.all_rows + 3) / 4)), dim3(kJoinThreads), 0, stream, own, head);
-}
-
-inline int compute_units() {
-  static std::atomic<int> cached[64] = {};
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-  if (cached[dev] == 0) {
-    int n = 0;
-    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) n = 256;
-    cached[dev] = n;
-  }
-  return cached[dev];
 }
 
 }  // namespace
