@@ -28,8 +28,9 @@
 // is taken by keys: then only `top` lanes, so 32 * top entries, reach it.
 //
 // Bound: memory. 2048 rows of 129280 BF16 106 us (5.0 TB/s), with the gradient
-// 319 (two reads and a write, 5.0 TB/s). With alternatives the chain of a
-// workgroup: 96 rows of 129280 FP32 with 20 of them 24 us (17 and 6.4 for the
+// 318 (two reads and a write, 5.0 TB/s); forward with one entry of 50 left and the
+// others masked, by whatever value, 109 to 111. With alternatives the chain of a
+// workgroup: 96 rows of 129280 FP32 with 20 of them 25 us (17 and 6.4 for the
 // join, 2.0 TB/s), without 17.
 
 #include "attn_common.h"
@@ -274,7 +275,7 @@ __device__ __forceinline__ void put_top(const Logprobs& p, int64_t t, const Norm
 
 // With alternatives: a workgroup has one chunk of a row. The code is kept short
 // (what is rare reads the chunk again in loops): with 53 KB of it, all unrolled,
-// fetching it once cold took most of a call's time, 546 rows of 12943 67 us.
+// 546 rows of 12943 took 67 us, with 15 KB 27.
 template <bool BF16>
 __global__ __launch_bounds__(kThreads) void logprobs_chunk_kernel(const Logprobs p, int chunks) {
   using L = Layout<BF16>;

@@ -22,16 +22,17 @@
 // maxima 2700 would be left, products, weights and the meeting of the waves. 128
 // rows of 128 requests of 300 to 4500 tokens 151 us (543 TFLOP/s), 32 rows of 8
 // requests of 41000 to 67000 67 us (2.7 TB/s, 465 TFLOP/s), 32 rows of 192
-// requests behind a prefix of 16000 317 us (694 TFLOP/s); over the FP8 cache
-// these take 159, 82 and 330 us. Not kept: codes through LDS by direct
+// requests behind a prefix of 16000 317 us (694 TFLOP/s). In graphs over the BF16,
+// FP8 and this cache they take 153, 161 and 144 us, 112, 82 and 63, 298, 339 and
+// 313 (the kernel over the others has two waves on a SIMD, with half of the key's
+// columns each; not built here). Not kept: codes through LDS by direct
 // loads (as fast, more code), loads by whole rows, which take a third of the
 // address unit's time, with the quarters exchanged between lanes (the prefix's
-// call 402 us), loads three tiles ahead (a third copy of the code, which a
-// launch fetches cold: 10 requests of 300 behind a prefix of 12000 50.5 us, now
-// 47; long ones as fast), the waves' wishes looked at beside the next tile's scores (334).
+// call 402 us), loads three tiles ahead (a third copy of the code: 10
+// requests of 300 behind a prefix of 12000 50.5 us, now 47; long ones as fast), the waves' wishes looked at beside the next tile's scores (334).
 //
-// Roundings below 32 bits: the weights to BF16 for the matrix unit (2^-9
-// relative, on the terms of a mean) and the output.
+// Roundings below 32 bits: the weights to BF16 for the matrix unit (relative 2^-8
+// at most each, on the terms of a mean) and the output.
 
 #include <type_traits>
 #include <utility>

@@ -1,5 +1,6 @@
 // A whole mixture-of-experts layer for a few tokens: two kernels that read each
-// chosen expert's weights once.
+// chosen expert's weights once (twice if more than 32 tokens chose it), and a
+// third that joins sums where the output is narrow.
 //
 //   up    h = bf16(silu(G_e x) * (U_e x)) for every (expert, token) that meet
 //   down  out_t = bf16(sum over t's experts of w * D_e h)
@@ -15,14 +16,13 @@
 //
 // up: a strip is 16 columns of h of one expert (16 rows of G and of U); a
 // workgroup's waves share its inner dimension and add their sums through LDS, or
-// have a strip each. down: a
-// workgroup is 32 columns of the output and a share of the (expert, 128 wide
-// piece) pairs, which its waves share in turn; an expert's sums go to its
+// have a strip each. down: a workgroup is 32 columns of the output and a share of
+// the (expert, 128 wide piece) pairs, which its waves share in turn; an expert's sums go to its
 // tokens' places in the wave's LDS when the wave is done with it. Both kernels
 // work on an expert's own tokens, packed: with a place for each of 64 tokens
 // instead, and zeros added to those that did not choose the expert, the
 // registers spilled and reading h took longer than reading weights (64 tokens,
-// 4 of 32 experts each, 540 us, now 271). A third launch adds the shares' sums,
+// 4 of 32 experts each, 540 us, now 260). A third launch adds the shares' sums,
 // in order, where there are several (added by the last workgroup to be done
 // instead, the fences at device scope cost 50 us).
 //
@@ -33,7 +33,7 @@
 // Bound: memory. 8 of 32 experts of 7168 x 2048 for one token 71 us (352 MB, 5.0
 // TB/s), 32 tokens on all 32 of them 264 us (1410 MB, 5.3 TB/s). Small layers:
 // launches and a workgroup's start, 5 tokens on 13 of 32 experts of 2048 x 1408
-// 35 us (113 MB, 3.1 TB/s).
+// 36 us (113 MB, 3.1 TB/s), 54 tokens on 8 of 768 x 2816 49 us (52 MB).
 
 #include "attn_common.h"
 #include "serve_internal.h"

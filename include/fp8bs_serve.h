@@ -146,6 +146,7 @@ FP8BS_API int64_t fp8bs_moe_tokens_workspace_bytes(int T, int topk, int64_t K, i
  *   logprob, entropy [T] float32   rank [T] int32
  *   norm    [T][2] float32: m and n (their sum is the log of the sum of exp(x_i))
  *   top_ids [T][top] int32, top_logprobs [T][top] float32 (NULL where top is 0)
+ * Logits may be of any finite size (masks of the type's lowest value, say).
  * Entries of -inf have no probability. A row of nothing else has m = -inf and
  * n = 0, logprob and top_logprobs -inf and entropy 0. A NaN or +inf in a row
  * gives NaN in its logprob (of a token), entropy and n; its rank and
